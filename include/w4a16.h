@@ -381,6 +381,162 @@ int unpack_gptq_v2(const int32_t *qweight, uint8_t *codes, int64_t K, int64_t N)
  * before any HIP call for the first three. */
 int w4a16_read_probe(const void *data, int64_t bytes, void *sink, void *stream);
 
+/* ---- The attention block around the linear: a 4-bit key/value cache ----
+ *
+ * Between the merged QKV linear and the output linear: the norm of each query
+ * and key head and the position rotation, keys and values stored in 4 bits in
+ * a paged cache, softmax attention over it, the attention weight each cached
+ * slot got, and the eviction of the slots with the least.
+ *
+ * Cache.  `pages` is one device buffer [num_pages][kv_heads][page_size / 32]
+ * of tiles; a tile is 32 slots (tokens) of one head, 32 * (D + 8 * D / g)
+ * bytes for D = head_dim channels in groups of g = group_size.  A group of one
+ * slot has a step s and an offset m in the activation type and codes c in
+ * 0..15, and stands for m + s c:
+ *     m = round(min), s = round((max - min) * (1/15)), c = rint((x - m) * (1/s))
+ * in fp32 (both reciprocals rounded to fp32) from the unrounded x (a step below the smallest normal fp32 counts
+ * as zero; a group with a value that is not finite is stored as NaN).  Words
+ * of a tile (lane = 16 b + r with b < 4, r < 16; nibble n):
+ *     [D/64][64 lanes][4 words i]  key codes: w = 4 * first + i, slot
+ *         16 (w / (D/32)) + r, channel 32 (w mod (D/32)) + 8 b + 2 (n mod 4) + n / 4
+ *     [D/64][64 lanes][4 words i]  value codes: w = 4 * first + i, channel
+ *         16 w + r, slot 4 b + n mod 4 + 16 (n / 4)
+ *     [D/g][32 slots]  key parameters, s in the low half and m in the high half
+ *     [D/g][32 slots]  value parameters
+ *
+ * Sequences.  Slot t of sequence b lies on page table[b][t / page_size]
+ * (table int32 [batch][table_stride]).  kv_len int32 [batch] counts the slots
+ * in use, the tokens of the current call among them: the call's tokens are
+ * rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [batch + 1]) of q, k and
+ * v, and they occupy the last slots.  A sequence may have no tokens or no
+ * slots.  All three are read on the device, so a captured graph may be
+ * replayed with other contents; slots past the table and page ids outside
+ * [0, num_pages) are never read or written (attention does not see them).
+ *
+ * Common rules: head_dim 64, 128 or 256; group_size 32, 64 or 128, at most
+ * head_dim and at least head_dim / 8; page_size a multiple of 32; q_heads a
+ * multiple of kv_heads; strides in elements, multiples of 8 and at least
+ * heads * D (the D channels and the heads of a token are contiguous); pointers
+ * 16-byte aligned (int32 arrays and lse: 4); flags W4A16_X_BF16 (q, k, v, the
+ * outputs and the cache's parameters bfloat16, else fp16) and the ones named
+ * at each call.  Weights, cos and sin, lse and accumulated weights are fp32.
+ * Every check runs before any HIP call; calls are asynchronous on `stream`,
+ * allocate nothing, can be captured into a graph, and give the same bits for
+ * the same inputs. */
+#define W4A16_ROPE_INTERLEAVED 0x10u  /* pairs (2i, 2i + 1), else (i, i + rot_dim / 2) */
+#define W4A16_NONCAUSAL 0x20u         /* every query sees all of its sequence's slots */
+
+/* Bytes of one page, kv_heads * (page_size / 32) tiles; 0 for a geometry that
+ * the cache does not take. */
+size_t w4a16_kv4_page_bytes(int64_t kv_heads, int64_t head_dim, int64_t group_size,
+                            int64_t page_size);
+
+/* Norm and rotation of queries and keys in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight     over the D channels of a head
+ *     (a, b) -> (a cos - b sin, b cos + a sin)   pairs of the first rot_dim
+ * in fp32, rounded once to the activation type.
+ *   q, k : [T, q_heads, D] and [T, kv_heads, D] (either may have no heads)
+ *   q_weight, k_weight : [D], or null: no norm of those heads
+ *   cos, sin : [max_pos, rot_dim / 2], or null (both): no rotation;
+ *   rot_dim a multiple of 16, at most D; positions int32 [T] (a position
+ *   outside [0, max_pos) gives NaN)
+ *   q_out, k_out : may be q and k themselves (with the same strides) */
+int w4a16_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                       const float *q_weight, const float *k_weight, float eps, const float *cos,
+                       const float *sin, const int32_t *positions, void *q_out,
+                       int64_t q_out_stride, void *k_out, int64_t k_out_stride, int64_t T,
+                       int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
+                       int64_t max_pos, unsigned flags, void *stream);
+
+/* The call's keys and values into the cache, and in the same launch the norm
+ * and rotation of keys (before they are quantised, from the fp32 values) and
+ * of queries (to q_out).  q_heads = 0: keys and values only.  max_q: at least
+ * the most tokens of any sequence.  Two calls that write the same tile must
+ * not overlap in time; older slots of the tile are kept. */
+int w4a16_kv4_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const float *q_weight,
+                     const float *k_weight, float eps, const float *cos, const float *sin,
+                     const int32_t *positions, void *q_out, int64_t q_out_stride, void *pages,
+                     const int32_t *table, const int32_t *cu_seqlens, const int32_t *kv_len,
+                     int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                     int64_t rot_dim, int64_t max_pos, int64_t group_size, int64_t page_size,
+                     int64_t num_pages, int64_t batch, int64_t table_stride, int64_t max_q,
+                     unsigned flags, void *stream);
+
+/* The values of the last cu_seqlens[b + 1] - cu_seqlens[b] slots of every
+ * sequence: k, v [rows, kv_heads, D], m + s c rounded to the activation type
+ * (NaN for a slot that is not there).  rows = cu_seqlens[batch]. */
+int w4a16_kv4_read(const void *pages, const int32_t *table, const int32_t *cu_seqlens,
+                   const int32_t *kv_len, void *k, void *v, int64_t rows, int64_t kv_heads,
+                   int64_t head_dim, int64_t group_size, int64_t page_size, int64_t num_pages,
+                   int64_t batch, int64_t table_stride, unsigned flags, void *stream);
+
+/* out = softmax(scale q . k) v over the slots each query sees.  Token i of the
+ * n new ones of a sequence with len slots sits in slot len - n + i; it sees
+ * the slots up to its own (with W4A16_NONCAUSAL all len of them), and with
+ * window > 0 only the window last of those up to its own (not with
+ * W4A16_NONCAUSAL: W4A16_ERR_FLAGS).  A query that sees none gets zeros and
+ * lse = -inf.  Query head j attends with key/value head j / (q_heads / kv_heads).
+ *   q : [T, q_heads, D];  out : [T, q_heads, D]
+ *   lse : [T, q_heads] log of the sum of exp(scale q . k), or null
+ *   max_q, max_kv : at least the most new tokens and slots of any sequence
+ *   (the work is laid out for them; further tokens and slots are not seen)
+ *   scale : finite and positive
+ *   workspace : w4a16_kv4_attention_workspace_bytes(...) bytes, caller-owned,
+ *   no initial contents (null when that is 0); calls that overlap in time must
+ *   not share one.
+ * Sums and softmax statistics are fp32; the products p s of a weight and a
+ * value step are rounded to the activation type before the second product,
+ * with the sum of the rounded ones taken along (u = 2^-11 for fp16, 2^-8 for
+ * bfloat16: |out - exact| <= u |exact| + 1.1 u sum_t p_t s_t |c_t - 8| and a
+ * few 2^-24 of the sums' magnitudes, sum_t p_t = 1). */
+int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
+                        const int32_t *cu_seqlens, const int32_t *kv_len, void *out,
+                        int64_t out_stride, float *lse, int64_t T, int64_t q_heads,
+                        int64_t kv_heads, int64_t head_dim, int64_t group_size,
+                        int64_t page_size, int64_t num_pages, int64_t batch,
+                        int64_t table_stride, int64_t max_q, int64_t max_kv, float scale,
+                        int64_t window, unsigned flags, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Workspace bytes of w4a16_kv4_attention (partial results of long sequences
+ * that are split over workgroups); 0 also for arguments it rejects. */
+size_t w4a16_kv4_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                           int64_t head_dim, int64_t max_q, int64_t max_kv,
+                                           int64_t window);
+
+/* acc[b][h][t] += sum of exp(scale q . k_t - lse) over the new tokens of
+ * sequence b that see slot t and the query heads of key/value head h: the
+ * attention weight that slot t got.  q, lse, scale, window and flags as the
+ * attention call had and gave them; acc fp32 [batch, kv_heads, acc_stride],
+ * acc_stride >= max_kv.  A query with lse = -inf adds nothing. */
+int w4a16_kv4_attention_mass(const void *q, int64_t q_stride, const void *pages,
+                             const int32_t *table, const int32_t *cu_seqlens,
+                             const int32_t *kv_len, const float *lse, float *acc,
+                             int64_t acc_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+                             int64_t head_dim, int64_t group_size, int64_t page_size,
+                             int64_t num_pages, int64_t batch, int64_t table_stride,
+                             int64_t max_q, int64_t max_kv, float scale, int64_t window,
+                             unsigned flags, void *stream);
+
+/* Every sequence and head cut to at most `budget` slots: the last `recent`
+ * (0 <= recent <= budget) and, of the others, those with the largest acc
+ * (equal ones: the lowest slots; NaN counts as the largest).  Sequences with
+ * at most budget slots keep all.  What is kept is copied in its order to slots
+ * 0 .. new_len - 1 of the pages in dst_table (same buffer; they must be none of
+ * the pages that `table` names for slots in use), so heads no longer hold the
+ * same tokens in a slot; the rotation of a key stays that of its token.
+ *   dst_table int32 [batch][dst_stride], dst_stride * page_size >= budget
+ *   acc : fp32 [batch, kv_heads, acc_stride], acc_stride >= max_kv
+ *   kept int32, acc_out fp32 : [batch, kv_heads, budget], the source slot and
+ *   its acc (-1 and 0 beyond new_len);  new_len int32 [batch] */
+int w4a16_kv4_evict(void *pages, const int32_t *table, const int32_t *kv_len, const float *acc,
+                    int64_t acc_stride, int64_t budget, int64_t recent, const int32_t *dst_table,
+                    int64_t dst_stride, int32_t *kept, int32_t *new_len, float *acc_out,
+                    int64_t kv_heads, int64_t head_dim, int64_t group_size, int64_t page_size,
+                    int64_t num_pages, int64_t batch, int64_t table_stride, int64_t max_kv,
+                    unsigned flags, void *stream);
+
 /* Static, human-readable name of a status code (never null). */
 const char *w4a16_status_string(int status);
 

@@ -14,7 +14,8 @@ Names match the C ABI in ``include/w4a16.h``:
   w4a16_status_string, and the measurement aid w4a16_read_probe
 plus ``linear``, ``gate_up_silu``, ``linear_lora`` and ``linear_zp`` (allocate
 y, and a workspace, with torch, then call the entry point of x's and the
-scales' dtypes).
+scales' dtypes).  The attention block on a 4-bit key/value cache (``kv4_*``,
+``qk_norm_rope``) is bound in ``kv4``.
 """
 
 from __future__ import annotations
@@ -60,7 +61,9 @@ EXPORTS = ("w4a16_linear", "w4a16_linear_noalloc", "w4a16_linear_ex", "w4a16_lin
            "w4a16_lora_workspace_bytes", "w4a16_linear_zp", "w4a16_linear_zp_bf16",
            "w4a16_zp_workspace_bytes", "w4a16_linear_typed", "w4a16_stream_release",
            "pack_gptq_v2", "unpack_gptq_v2",
-           "w4a16_read_probe", "w4a16_status_string")
+           "w4a16_read_probe", "w4a16_kv4_page_bytes", "w4a16_qk_norm_rope", "w4a16_kv4_append",
+           "w4a16_kv4_read", "w4a16_kv4_attention", "w4a16_kv4_attention_workspace_bytes",
+           "w4a16_kv4_attention_mass", "w4a16_kv4_evict", "w4a16_status_string")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -122,6 +125,7 @@ def load_library() -> ctypes.CDLL:
     lib.w4a16_read_probe.restype = i32
     lib.w4a16_status_string.argtypes = [i32]
     lib.w4a16_status_string.restype = ctypes.c_char_p
+    kv4.declare(lib)
     _lib = lib
     return lib
 
@@ -473,3 +477,9 @@ def linear(x, qweight, scales, group_size: int, out=None, stream=None,
         call = w4a16_linear_bf16_ex if x.dtype == torch.bfloat16 else w4a16_linear_ex
         call(x, qweight, scales, out, M, K, N, group_size, stream, kernel)
     return out
+
+
+from . import kv4  # noqa: E402  (needs the names above)
+from .kv4 import (W4A16_NONCAUSAL, W4A16_ROPE_INTERLEAVED, kv4_append,  # noqa: E402,F401
+                  kv4_attention, kv4_attention_mass, kv4_attention_workspace_bytes, kv4_evict,
+                  kv4_new_pages, kv4_page_bytes, kv4_read, qk_norm_rope)

@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "../../include/w4a16.h"
+#include "kv4_launch.h"
 #include "w4a16_launch.h"
 
 namespace {
@@ -57,8 +58,10 @@ std::atomic<int> g_arch[kMaxDevices];      // 0 unknown, 1 gfx950, 2 other
 std::atomic<int> g_cus[kMaxDevices];
 std::atomic<size_t> g_lds[kMaxDevices];    // LDS bytes per workgroup
 
+}  // namespace
+
 // Current device if it is a gfx950 (with its CU count and LDS limit), else -1.
-int usable_device(int *num_cus, size_t *max_lds) {
+int w4a16::usable_device(int *num_cus, size_t *max_lds) {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return -1;
     int state = g_arch[dev].load(std::memory_order_acquire);
@@ -75,6 +78,10 @@ int usable_device(int *num_cus, size_t *max_lds) {
     *max_lds = g_lds[dev].load(std::memory_order_relaxed);
     return state == 1 ? dev : -1;
 }
+
+namespace {
+
+using w4a16::usable_device;
 
 // Kernel workspaces, one per (device, stream, kind): calls on one stream run
 // in stream order and calls on different streams use different workspaces,
