@@ -1,15 +1,19 @@
 // Softmax attention over the 4-bit key/value cache.
 //
 // Rows are (new token, query head of the group) pairs; for row q and slot t
-//   x_t = q . k_t,  k_t = m + s c per group of channels
-//       = sum_g s_g (q_g . (16 + c_g)) + (m_g - 16 s_g) sum(q_g)
+//   x_t = q . k_t,  k_t = m + s c per group of channels, B = 64 or 128
+//       = sum_g s_g (q_g . (B + c_g) - B sum(q_g)) + m_g sum(q_g)
 //   p_t = exp2(scale log2(e) x_t - ref),  out = sum_t p_t v_t / sum_t p_t,
-//   sum_t p_t v_t = sum_t P_t (16 + c_t) - 24 sum_t P_t + sum_t p_t (m_t + 8 s_t),
+//   sum_t p_t v_t = sum_t P_t (B + c_t) - (B + 8) sum_t P_t + sum_t p_t (m_t + 8 s_t),
 //   P_t = p_t s_t rounded to the activation type.
 // The codes go into the matrix instructions as the exact 16-bit numbers
-// 16 + c; steps and offsets act on the fp32 sums.  The sum of the P_t comes
+// B + c; steps and offsets act on the fp32 sums.  The sum of the P_t comes
 // from one more matrix product with ones, of the same rounded P_t, so that
-// the 24 comes off exactly and only P_t (c_t - 8) feels their rounding.
+// B + 8 comes off exactly and only P_t (c_t - 8) feels their rounding.
+// A slot that a row does not see has p_t = 0 and adds nothing, whatever is
+// stored there: its product with a step is the one in which 0 x NaN is 0, and
+// a NaN offset is made finite (a group with a NaN has it in both, so that a
+// slot with weight still gives NaN).
 // ref is a running reference per row, moved only when a tile's maximum
 // passes it by more than kSlack: p_t stays below 2^kSlack, and P_t below
 // 2^kSlack * (2 * 65504 / 15), which fp16 holds.
@@ -26,6 +30,13 @@ constexpr int kThreads = 64 * kWaves;
 constexpr float kSlack = 2.0f;
 constexpr float kNone = -3e38f;        // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
+
+// a * b with 0 * anything = 0.
+__device__ __forceinline__ float mul_legacy(float a, float b) {
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
 
 // What a workgroup works on: a tile of rows of one head of one sequence, and
 // a range of its slots.
@@ -58,78 +69,172 @@ __device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int 
 }
 
 // Rows per tile of rows: 16 NT.  Partial results of one (sequence, head, tile
-// of rows, chunk): 16 NT x (D sums, reference, sum of p).
+// of rows, chunk): rows x (D sums), rows references, rows sums of p.
 struct Plan {
-    int nt, row_tiles, chunk, chunks;      // chunk: tiles of slots a workgroup takes
+    int rows, row_tiles, chunk, chunks;    // chunk: tiles of slots a workgroup takes
 };
 
-constexpr int kPlanSlots = 256 * 3;      // workgroups the chip holds at a time
+// Chunks.  A few sequences: two workgroups for each CU, all of them at work at once, since a
+// workgroup's start and end cost about as much as eight tiles (one sequence of 131071 slots, 8
+// heads: 36.6 us with 512 workgroups, 39 with 1024, 43.6 with 2048).  More sequences may differ
+// in length, and smaller chunks even that out (32 sequences of 1000 to 24000 slots: 136 us with
+// 512, 123 with 1024 to 3072).
+constexpr int kFewSlots = 512, kManySlots = 1536, kFewSequences = 4;
 
 Plan plan_of(const Kv4AttnArgs &a) {
     Plan p;
     const int rows = a.q_heads / a.c.kv_heads * a.max_q;
-    p.nt = rows > 16 && a.c.head_dim <= 128 ? 2 : 1;      // (256 channels: two would not fit the registers)
-    p.row_tiles = (rows + 16 * p.nt - 1) / (16 * p.nt);
+    p.rows = rows > 16 && a.c.head_dim <= 128 ? 32 : 16;   // (256 channels: 32 would not fit the registers)
+    p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min(tiles, (a.window + a.max_q) / 32 + 2);
     const int64_t groups = (int64_t)a.c.batch * a.c.kv_heads * p.row_tiles;
-    const int64_t want = std::max<int64_t>(1, kPlanSlots / groups);
-    p.chunk = (int)std::max<int64_t>(kWaves, (tiles + want - 1) / want);
-    p.chunk = (p.chunk + kWaves - 1) / kWaves * kWaves;
+    const int64_t want = std::max<int64_t>(
+        1, (a.c.batch <= kFewSequences ? kFewSlots : kManySlots) / groups);
+    int64_t chunk = ((tiles + want - 1) / want + kWaves - 1) / kWaves * kWaves;
+    // page ids of a chunk sit in the 64 lanes of a wave
+    if (a.c.tiles_per_page < (1 << 20)) chunk = std::min<int64_t>(chunk, 62 * (int64_t)a.c.tiles_per_page);
+    p.chunk = (int)std::max<int64_t>(kWaves, chunk / kWaves * kWaves);
     p.chunks = std::max(1, (tiles + p.chunk - 1) / p.chunk);
     return p;
 }
 
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) void lds_void;
+template <typename T>
+__device__ __forceinline__ T lds_get(const lds_u8 *p) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) T *>(p);
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
+    *reinterpret_cast<__attribute__((address_space(3))) T *>(p) = v;
+}
+
+// s_waitcnt vmcnt(n): at most n of this wave's vector memory instructions are still under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// One tile copied to LDS without passing through registers (lane l's 16 bytes of an
+// instruction land at 16 l): the codes 1 KiB an instruction, the parameters 256 bytes, or
+// 1 KiB where there are that many.  `bytes` 0 reads nothing and writes zeros.
 template <int D, int NG>
-struct Stage {
-    u4 k[D / 64], v[D / 64];
-    uint32_t par[NG];
-    bool there;
+struct TileCopy {
+    using T = Tile<D, NG>;
+    static constexpr bool kWidePar = NG % 4 == 0;
+    static constexpr int kParLoads = kWidePar ? NG / 4 : NG;
+    static constexpr int kLoads = D / 32 + kParLoads;       // instructions of a tile
+    static __device__ __forceinline__ void issue(const uint8_t *tile, uint32_t bytes, lds_u8 *to, int lane) {
+        const auto rsrc = make_rsrc(tile, bytes);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + 1024 * j), 16, 16 * lane, 1024 * j, 0, 0);
+        constexpr int kAt = 2 * T::kCodes;
+#pragma unroll
+        for (int j = 0; j < kParLoads; ++j) {
+            if constexpr (kWidePar)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + kAt + 1024 * j), 16, 16 * lane,
+                                                         kAt + 1024 * j, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + kAt + 256 * j), 4, 4 * lane,
+                                                         kAt + 256 * j, 0, 0);
+        }
+    }
+};
+
+// Up to 32 rows of one head against a chunk of slots.  Each wave takes every fourth tile of the
+// chunk, on its own until the end.  Tiles go through a ring of kRing in LDS that is the wave's
+// own: kRing - 1 are under way while one is worked on, and no barrier is needed.
+template <int D, int NG, int NT>
+struct AttendShape {
+    using T = Tile<D, NG>;
+    static constexpr int kRing = 2;
+    static constexpr int kRows = 16 * NT;
+    static constexpr int kOutRow = 4 * (D + 4);                            // bytes
+    static constexpr int kTiles = kWaves * kRing * T::kBytes;
+    static constexpr int kOuts = kWaves * kRows * kOutRow;                 // the waves' sums, at the end
+    static constexpr int kStats = kTiles > kOuts ? kTiles : kOuts;         // references and sums of p
+    static constexpr int kLds = kStats + 2 * kWaves * kRows * 4;
 };
 
 template <bool BF, int D, int NG, int NT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan plan) {
+__global__ void __launch_bounds__(kThreads)
+    __attribute__((amdgpu_waves_per_eu(NT * D <= 128 ? 3 : 1, NT * D <= 128 ? 3 : 1))) attend_kernel(Kv4AttnArgs a, Plan plan) {
     using T = Tile<D, NG>;
+    using Shape = AttendShape<D, NG, NT>;
+    using Copy = TileCopy<D, NG>;
     constexpr int kSteps = D / 32;            // 32-channel products of a slot
     constexpr int kPer = kSteps / NG;         // of them per group
-    constexpr int kRows = 16 * NT;
+    constexpr int kRows = Shape::kRows, kRing = Shape::kRing;
     constexpr int kOut = D / 16;              // 16-channel blocks of the output
     constexpr int kBlocks = kOut / NG;        // of them per group
-    struct Shared {
-        __align__(16) uint32_t par[kWaves][64 * NG];
-        float ref[kWaves][kRows], sum[kWaves][kRows];
-        float out[kWaves][kRows][D + 4];
-    };
-    __shared__ Shared sh;
+    // Offsets of the values: with one group 24 operations in every lane, with more a matrix
+    // product whose rows are the groups (about 36, whatever the number of groups).
+    constexpr bool kMidRows = NG > 1;
+    __shared__ __align__(16) uint8_t lds_raw[Shape::kLds];
+    lds_u8 *const lds = (lds_u8 *)lds_raw;
 
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, b4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, r = lane & 15, b4 = lane >> 4;
+    // The page ids of the chunk, one in each lane (the host keeps a chunk within 64 pages), so
+    // that no copy waits for a page id.  Without a window a chunk's place does not depend on the
+    // sequence's lengths, and the ids are loaded beside them.
+    const int tpp = a.c.tiles_per_page, kvh = a.c.kv_heads;
+    auto load_ids = [&](int tile) {
+        const int at = tile / tpp + lane;
+        return at < a.c.table_stride ? a.c.table[(int64_t)blockIdx.z * a.c.table_stride + at] : -1;
+    };
+    int ids = load_ids((int)blockIdx.x * plan.chunk);
     Work w;
-    const int kvh = a.c.kv_heads;
     if (!work_of(a, blockIdx.z, blockIdx.y % kvh, (blockIdx.y / kvh) * kRows, kRows, &w)) return;
     const int chunk0 = w.t0 + (int)blockIdx.x * plan.chunk;
     const int chunk1 = min(chunk0 + plan.chunk, w.t1);
     if (blockIdx.x > 0 && chunk0 >= w.t1) return;
     const int G = a.q_heads / kvh;
 
+    const int page0 = chunk0 / tpp;
+    if (w.t0 > 0) ids = load_ids(chunk0);
+    // (page, in): where the next copy's tile lies
+    int next = chunk0 + wave, page = 0, in = chunk0 - page0 * tpp + wave, slot_next = 0;
+    uint32_t there = 0;                       // bit s: the tile in ring slot s exists
+    auto issue = [&]() {
+        while (in >= tpp) {
+            in -= tpp;
+            ++page;
+        }
+        const int id = next < chunk1 ? __builtin_amdgcn_readlane(ids, page) : -1;
+        const bool ok = (unsigned)id < (unsigned)a.c.num_pages;
+        const uint8_t *p = a.c.pages + (((int64_t)(ok ? id : 0) * kvh + w.h) * tpp + in) * T::kBytes;
+        Copy::issue(p, ok ? T::kBytes : 0, lds + (wave * kRing + slot_next) * T::kBytes, lane);
+        there = (there & ~(1u << slot_next)) | ((ok ? 1u : 0u) << slot_next);
+        slot_next = slot_next + 1 == kRing ? 0 : slot_next + 1;
+        next += kWaves;
+        in += kWaves;
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) issue();
+
     // this lane's columns: NT rows of q, their channels as matrix operands, and what they see
-    u4 q[NT][kSteps];
-    f4 init[NT][NG];
+    u4 q[NT][kSteps], qparts[NT];
     float qsum[NT][NG];
+    f4 init[NT][NG];                          // -B sum(q_g)
     int lo[NT], hi[NT];
     int all_lo = 0, all_hi = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int row = w.row0 + 16 * t + r;
-        const bool there = row < w.rows;
-        const int i = there ? row / G : 0;
-        lo[t] = there ? row_lo(i, w.n, w.len, a.window) : 0;
-        hi[t] = there ? row_hi(i, w.n, w.len, a.causal) : 0;
-        if (there) {
+        const bool in_seq = row < w.rows;
+        const int i = in_seq ? row / G : 0;
+        lo[t] = in_seq ? row_lo(i, w.n, w.len, a.window) : 0;
+        hi[t] = in_seq ? row_hi(i, w.n, w.len, a.causal) : 0;
+        if (in_seq) {
             all_lo = max(all_lo, lo[t]);
             all_hi = min(all_hi, hi[t]);
         }
         const uint16_t *src = static_cast<const uint16_t *>(a.q) + (int64_t)(w.first + i) * a.q_stride +
-                              (int64_t)(w.h * G + (there ? row - i * G : 0)) * D + 8 * b4;
+                              (int64_t)(w.h * G + (in_seq ? row - i * G : 0)) * D + 8 * b4;
 #pragma unroll
         for (int g = 0; g < NG; ++g) qsum[t][g] = 0.f;
 #pragma unroll
@@ -142,8 +247,18 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan pl
         for (int g = 0; g < NG; ++g) {
             qsum[t][g] += __shfl_xor(qsum[t][g], 16);
             qsum[t][g] += __shfl_xor(qsum[t][g], 32);
-            const float z = -16.0f * qsum[t][g];
+            const float z = -kCodeBase<BF> * qsum[t][g];
             init[t][g] = f4{z, z, z, z};
+        }
+        // bfloat16: sum_g m_g sum(q_g) is one matrix product over 8 groups x 4 parts, the sums of q
+        // in three parts of eight bits each (the m_g are exact)
+        if constexpr (BF) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float z0 = 2 * e < NG ? qsum[t][2 * e < NG ? 2 * e : 0] : 0.f;
+                const float z1 = 2 * e + 1 < NG ? qsum[t][2 * e + 1 < NG ? 2 * e + 1 : 0] : 0.f;
+                qparts[t][e] = b4 < 3 ? pack2<BF>(bf16_part(z0, b4), bf16_part(z1, b4)) : 0u;
+            }
         }
     }
     // the slots that every row sees, over the 16 columns
@@ -159,57 +274,56 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan pl
     const CodeConsts cc = code_consts<BF>();
     const uint32_t one16 = BF ? 0x3F803F80u : 0x3C003C00u;
     const u4 ones = {one16, one16, one16, one16};
-    float ref[NT], sum[NT], corr[NT][NG];
-    f4 out[NT][kOut], psum[NT][NG];
+    float ref[NT], sum[NT];
+    f4 out[NT][kOut], psum[NT][NG], mids[NT];      // mids: sum_t p_t (m_t + 8 s_t)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         ref[t] = kNone;
         sum[t] = 0.f;
+        mids[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            corr[t][g] = 0.f;
-            psum[t][g] = f4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int g = 0; g < NG; ++g) psum[t][g] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int o = 0; o < kOut; ++o) out[t][o] = f4{0.f, 0.f, 0.f, 0.f};
     }
 
-    auto load = [&](int tile, Stage<D, NG> &s) {
-        s.there = false;
-        if (tile >= chunk1) return;
-        const uint8_t *p = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, w.b, w.h, tile);
-        if (!p) return;
-        s.there = true;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            s.k[j] = *reinterpret_cast<const u4 *>(p + 1024 * j + 16 * lane);
-            s.v[j] = *reinterpret_cast<const u4 *>(p + T::kCodes + 1024 * j + 16 * lane);
-        }
-        const uint32_t *par = reinterpret_cast<const uint32_t *>(p + 2 * T::kCodes);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) s.par[j] = par[64 * j + lane];
-    };
-
-    auto step = [&](int tile, const Stage<D, NG> &s) {
-        // parameters: one load of the tile's words, then broadcasts out of LDS (a wave's own
-        // area; its LDS operations are in order)
-#pragma unroll
-        for (int j = 0; j < NG; ++j) sh.par[wave][64 * j + lane] = s.par[j];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const u4 *par = reinterpret_cast<const u4 *>(sh.par[wave]);
+    auto step = [&](int tile, const lds_u8 *at) {
+        // whether some row does not see some of the tile's slots; the same in every lane
+        const bool masked = 32 * tile < all_lo || 32 * tile + 32 > all_hi;
+        const lds_u8 *params = at + 2 * T::kCodes + 16 * b4;
         float x[NT][8];
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
             u4 kc[kSteps];
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
-                const int word = sub * kSteps + j;
-                kc[j] = codes16<BF>(s.k[word >> 2][word & 3], cc);
+                if constexpr (D == 64) {
+                    const u4 words = lds_get<u4>(at + 16 * lane);
+                    kc[j] = based_codes<BF>(words[sub * kSteps + j], cc);
+                } else if (j % 4 == 0) {
+                    const u4 words = lds_get<u4>(at + 1024 * ((sub * kSteps + j) / 4) + 16 * lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kc[j + i] = based_codes<BF>(words[i], cc);
+                }
+            }
+            if constexpr (BF) {
+                u4 m = {0u, 0u, 0u, 0u};         // offsets of the slot that is this lane's row
+                const lds_u8 *mine = at + 2 * T::kCodes + 64 * sub + 4 * r;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t p = lds_get<uint32_t>(mine + 128 * g);
+                    m[g / 2] = g % 2 ? __builtin_amdgcn_perm(p, m[g / 2], 0x07060100u) : p >> 16;
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const f4 z = mfma16x16x32_t<BF>(m, qparts[t], f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[t][4 * sub + e] = z[e];
+                }
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const u4 kp = par[8 * g + 4 * sub + b4];
+                const u4 kp = lds_get<u4>(params + 128 * g + 64 * sub);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     f4 acc = init[t][g];
@@ -217,30 +331,22 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan pl
                     for (int j = g * kPer; j < (g + 1) * kPer; ++j) acc = mfma16x16x32_t<BF>(kc[j], q[t][j], acc);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float m = par_offset<BF>(kp[e]), st = par_step<BF>(kp[e]);
                         float &y = x[t][4 * sub + e];
-                        y = g == 0 ? m * qsum[t][0] : __builtin_fmaf(m, qsum[t][g], y);
-                        y = __builtin_fmaf(st, acc[e], y);
+                        if constexpr (!BF) y = __builtin_fmaf(par_offset<BF>(kp[e]), qsum[t][g], g ? y : 0.f);
+                        y = __builtin_fmaf(par_step<BF>(kp[e]), acc[e], y);
                     }
                 }
             }
         }
-        const int base = 32 * tile;
-        const bool masked = base < all_lo || base + 32 > all_hi;      // the same in every lane
-        uint32_t see[NT];
+        if (masked) {
+            asm volatile("");                    // (a branch, not sixteen selects in every tile)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            see[t] = 0xFFu;
-            if (masked) {
-                see[t] = 0;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int slot = base + 16 * (e >> 2) + 4 * b4 + (e & 3);
-                    const bool ok = slot >= lo[t] && slot < hi[t];
-                    see[t] |= (ok ? 1u : 0u) << e;
-                    if (!ok) x[t][e] = -__builtin_inff();
+                    const int slot = 32 * tile + 16 * (e >> 2) + 4 * b4 + (e & 3);
+                    if (!((slot >= lo[t]) & (slot < hi[t]))) x[t][e] = -__builtin_inff();
                 }
-            }
         }
         float top[NT];
         bool move = false;
@@ -262,115 +368,163 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan pl
                 const float f = __builtin_amdgcn_exp2f(ref[t] - m);
                 ref[t] = m;
                 sum[t] *= f;
+                mids[t] *= f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    corr[t][g] *= f;
-                    psum[t][g] *= f;
-                }
+                for (int g = 0; g < NG; ++g) psum[t][g] *= f;
 #pragma unroll
                 for (int o = 0; o < kOut; ++o) out[t][o] *= f;
             }
         }
         // weights, and their products with the values' steps as matrix operands
+        u4 pr[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][e], c1, -ref[t]));
                 sum[t] += x[t][e];
             }
+            if constexpr (kMidRows)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pr[t][e] = pack2<BF>(x[t][e], x[t][4 + e]);
+        }
+        if constexpr (kMidRows) {
+            // sum_t p_t (m_t + 8 s_t) of all groups in two matrix products, row g of the first
+            // operand holding group g: the rounded p_t with the middles in two parts
+            const lds_u8 *mine = at + 2 * T::kCodes + 128 * (NG + (r < NG ? r : NG - 1)) + 16 * b4;
+            const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
+            constexpr float kFloor = BF ? -3e38f : -65504.0f;        // in place of a NaN
+            u4 high, low;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float m0 = fmaxf(__builtin_fmaf(8.0f, par_step<BF>(p0[e]), par_offset<BF>(p0[e])), kFloor);
+                const float m1 = fmaxf(__builtin_fmaf(8.0f, par_step<BF>(p1[e]), par_offset<BF>(p1[e])), kFloor);
+                high[e] = pack2<BF>(m0, m1);
+                low[e] = pack2<BF>(m0 - lo_f32<BF>(high[e]), m1 - hi_f32<BF>(high[e]));
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mids[t] = mfma16x16x32_t<BF>(high, pr[t], mids[t]);
+                mids[t] = mfma16x16x32_t<BF>(low, pr[t], mids[t]);
+            }
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const u4 p0 = par[8 * NG + 8 * g + b4], p1 = par[8 * NG + 8 * g + 4 + b4];
-            float st[8], mid[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t p = e < 4 ? p0[e & 3] : p1[e & 3];
-                st[e] = par_step<BF>(p);
-                mid[e] = __builtin_fmaf(8.0f, st[e], par_offset<BF>(p));
-            }
+            const u4 p0 = lds_get<u4>(params + 128 * (NG + g)), p1 = lds_get<u4>(params + 128 * (NG + g) + 64);
             u4 pw[NT];
+            float st[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) st[e] = par_step<BF>(e < 4 ? p0[e & 3] : p1[e & 3]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float ps[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float m = mid[e];
-                    ps[e] = x[t][e] * st[e];
-                    if (masked && !(see[t] >> e & 1)) ps[e] = m = 0.f;     // unseen: whatever is stored there
-                    corr[t][g] = __builtin_fmaf(x[t][e], m, corr[t][g]);
-                }
+                for (int e = 0; e < 8; ++e) ps[e] = mul_legacy(x[t][e], st[e]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pw[t][e] = pack2<BF>(ps[e], ps[4 + e]);
                 psum[t][g] = mfma16x16x32_t<BF>(ones, pw[t], psum[t][g]);
             }
+            if constexpr (!kMidRows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // (a NaN of an unseen slot becomes finite here; of a seen one, P_t is NaN)
+                    const float mid = fmaxf(
+                        __builtin_fmaf(8.0f, st[e], par_offset<BF>(e < 4 ? p0[e & 3] : p1[e & 3])), -3e38f);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mids[t][0] = __builtin_fmaf(x[t][e], mid, mids[t][0]);
+                }
+            }
 #pragma unroll
             for (int o = g * kBlocks; o < (g + 1) * kBlocks; ++o) {
-                const u4 vc = codes16<BF>(s.v[o >> 2][o & 3], cc);
+                if constexpr (kBlocks >= 4) {
+                    if (o % 4 == 0) {
+                        const u4 words = lds_get<u4>(at + T::kCodes + 256 * o + 16 * lane);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) out[t][o] = mfma16x16x32_t<BF>(vc, pw[t], out[t][o]);
+                        for (int i = 0; i < 4; ++i) {
+                            const u4 vc = based_codes<BF>(words[i], cc);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                out[t][o + i] = mfma16x16x32_t<BF>(vc, pw[t], out[t][o + i]);
+                        }
+                    }
+                } else if (o % 2 == 0) {         // two words a group
+                    const u2 words = lds_get<u2>(at + T::kCodes + 1024 * (o / 4) + 16 * lane + 4 * (o % 4));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const u4 vc = based_codes<BF>(words[i], cc);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            out[t][o + i] = mfma16x16x32_t<BF>(vc, pw[t], out[t][o + i]);
+                    }
+                }
             }
         }
     };
 
-    Stage<D, NG> s0, s1;
-    int tile = chunk0 + wave;
-    load(tile, s0);
-    while (tile < chunk1) {
-        load(tile + kWaves, s1);
-        if (s0.there) step(tile, s0);
-        tile += kWaves;
-        if (tile >= chunk1) break;
-        load(tile + kWaves, s0);
-        if (s1.there) step(tile, s1);
-        tile += kWaves;
+    int at_slot = 0;
+    for (int tile = chunk0 + wave; tile < chunk1; tile += kWaves) {
+        issue();
+        wait_loads<(kRing - 1) * Copy::kLoads>();            // the oldest tile has landed
+        __builtin_amdgcn_sched_barrier(0);
+        if (there >> at_slot & 1) {
+            const lds_u8 *at = lds + (wave * kRing + at_slot) * T::kBytes;
+            step(tile, at);
+        }
+        at_slot = at_slot + 1 == kRing ? 0 : at_slot + 1;
+        __builtin_amdgcn_sched_barrier(0);                   // its reads are done before a copy may overwrite it
     }
+    wait_loads<0>();
 
-    // join the waves: common reference, then the sums through LDS
+    // join the waves: common reference, then the sums through LDS (which the tiles leave)
+    lds_u8 *const refs = lds + Shape::kStats, *const sums = refs + 4 * kWaves * kRows;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         sum[t] += __shfl_xor(sum[t], 16);
         sum[t] += __shfl_xor(sum[t], 32);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            corr[t][g] += __shfl_xor(corr[t][g], 16);
-            corr[t][g] += __shfl_xor(corr[t][g], 32);
+        if constexpr (!kMidRows) {
+            mids[t][0] += __shfl_xor(mids[t][0], 16);
+            mids[t][0] += __shfl_xor(mids[t][0], 32);
         }
         if (b4 == 0) {
-            sh.ref[wave][16 * t + r] = ref[t];
-            sh.sum[wave][16 * t + r] = sum[t];
+            lds_put(refs + 4 * (wave * kRows + 16 * t + r), ref[t]);
+            lds_put(sums + 4 * (wave * kRows + 16 * t + r), sum[t]);
         }
     }
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        float m = sh.ref[0][16 * t + r];
+        float m = lds_get<float>(refs + 4 * (16 * t + r));
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.ref[i][16 * t + r]);
+        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, lds_get<float>(refs + 4 * (i * kRows + 16 * t + r)));
         const float f = __builtin_amdgcn_exp2f(ref[t] - m);
+        float mid[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)         // row g of the product: register g % 4 of the lanes with b4 = g / 4
+            mid[g] = kMidRows ? __shfl(mids[t][g % 4], 16 * (g / 4) + r) : mids[t][0];
 #pragma unroll
         for (int o = 0; o < kOut; ++o) {
             const int g = o / kBlocks;
-            const f4 y = (out[t][o] - 24.0f * psum[t][g] + corr[t][g]) * f;
-            *reinterpret_cast<f4 *>(&sh.out[wave][16 * t + r][16 * o + 4 * b4]) = y;
+            const f4 y = (out[t][o] - (kCodeBase<BF> + 8.0f) * psum[t][g] + mid[g]) * f;
+            lds_put(lds + (wave * kRows + 16 * t + r) * Shape::kOutRow + 64 * o + 16 * b4, y);
         }
     }
     __syncthreads();
     const bool whole = w.t1 - w.t0 <= plan.chunk;       // this workgroup saw everything
     float *part = static_cast<float *>(a.workspace) +
                   (((int64_t)w.b * gridDim.y + blockIdx.y) * plan.chunks + blockIdx.x) * kRows * (D + 2);
-    for (int at = threadIdx.x; at < kRows * (D / 4); at += kThreads) {
-        const int col = at / (D / 4), d = 4 * (at % (D / 4));
+    for (int idx = threadIdx.x; idx < kRows * (D / 4); idx += kThreads) {
+        const int col = idx / (D / 4), d = 4 * (idx % (D / 4));
         const int row = w.row0 + col;
         if (row >= w.rows) break;
-        float m = sh.ref[0][col], total = 0.f;
+        float m = lds_get<float>(refs + 4 * col), total = 0.f;
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.ref[i][col]);
+        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, lds_get<float>(refs + 4 * (i * kRows + col)));
         f4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
-            total += sh.sum[i][col] * __builtin_amdgcn_exp2f(sh.ref[i][col] - m);
-            y += *reinterpret_cast<const f4 *>(&sh.out[i][col][d]);
+            total += lds_get<float>(sums + 4 * (i * kRows + col)) *
+                     __builtin_amdgcn_exp2f(lds_get<float>(refs + 4 * (i * kRows + col)) - m);
+            y += lds_get<f4>(lds + (i * kRows + col) * Shape::kOutRow + 4 * d);
         }
         if (whole) {
             const int i = row / G;
@@ -393,32 +547,56 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(Kv4AttnArgs a, Plan pl
 }
 
 // Joins the chunks of one row: out = sum_c 2^(ref_c - ref) out_c / sum_c 2^(ref_c - ref) sum_c.
+// D/4 lanes take four channels each; the other lanes of the workgroup take other chunks.
+constexpr int kJoin = 256;
 template <bool BF, int D>
-__global__ void __launch_bounds__(D) join_kernel(Kv4AttnArgs a, Plan plan) {
-    const int kRows = 16 * plan.nt, kvh = a.c.kv_heads, G = a.q_heads / kvh;
+__global__ void __launch_bounds__(kJoin) join_kernel(Kv4AttnArgs a, Plan plan) {
+    constexpr int kLanes = D / 4, kSets = kJoin / kLanes;
+    const int rows = plan.rows, kvh = a.c.kv_heads, G = a.q_heads / kvh;
     Work w;
     const int col = blockIdx.x;
-    if (!work_of(a, blockIdx.z, blockIdx.y % kvh, (blockIdx.y / kvh) * kRows, kRows, &w)) return;
+    if (!work_of(a, blockIdx.z, blockIdx.y % kvh, (blockIdx.y / kvh) * rows, rows, &w)) return;
     const int row = w.row0 + col;
     if (row >= w.rows || w.t1 - w.t0 <= plan.chunk) return;
     const int chunks = (w.t1 - w.t0 + plan.chunk - 1) / plan.chunk;
+    const int64_t step = (int64_t)rows * (D + 2);
     const float *part = static_cast<const float *>(a.workspace) +
-                        ((int64_t)w.b * gridDim.y + blockIdx.y) * plan.chunks * kRows * (D + 2);
-    const int64_t step = (int64_t)kRows * (D + 2);
+                        ((int64_t)w.b * gridDim.y + blockIdx.y) * plan.chunks * step;
+    const float *refs = part + rows * D + col, *sums = refs + rows;
+    __shared__ float tops[kJoin / 64], totals[kSets];
+    __shared__ f4 outs[kSets][kLanes];
     float m = kNone;
-    for (int c = 0; c < chunks; ++c) m = fmaxf(m, part[c * step + kRows * D + col]);
-    float total = 0.f, y = 0.f;
-    for (int c = 0; c < chunks; ++c) {
-        const float f = __builtin_amdgcn_exp2f(part[c * step + kRows * D + col] - m);
-        total += f * part[c * step + kRows * D + kRows + col];
-        y += f * part[c * step + col * D + threadIdx.x];
+    for (int c = threadIdx.x; c < chunks; c += kJoin) m = fmaxf(m, refs[c * step]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoin / 64; ++i) m = fmaxf(m, tops[i]);
+    const int set = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    float total = 0.f;
+    f4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = set; c < chunks; c += kSets) {
+        const float f = __builtin_amdgcn_exp2f(refs[c * step] - m);
+        total += f * sums[c * step];
+        y += f * *reinterpret_cast<const f4 *>(part + c * step + col * D + 4 * lane);
+    }
+    outs[set][lane] = y;
+    if (lane == 0) totals[set] = total;
+    __syncthreads();
+    if (set > 0) return;
+#pragma unroll
+    for (int i = 1; i < kSets; ++i) {
+        y += outs[i][lane];
+        total += totals[i];
     }
     const int i = row / G, head = w.h * G + row - i * G;
     const int64_t at = w.first + i;
     const float inv = total == 0.f ? 0.f : 1.0f / total;
-    static_cast<uint16_t *>(a.out)[at * a.out_stride + (int64_t)head * D + threadIdx.x] =
-        (uint16_t)pack2<BF>(y * inv, 0.f);
-    if (a.lse && threadIdx.x == 0)
+    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at * a.out_stride + (int64_t)head * D + 4 * lane) =
+        pack4<BF>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && lane == 0)
         a.lse[at * a.q_heads + head] = total == 0.f ? -__builtin_inff() : (m + __log2f(total)) * (1.0f / kLog2e);
 }
 
@@ -442,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(Kv4AttnArgs a) {
     for (int j = 0; j < D / 64; ++j) {
         const u4 words = *reinterpret_cast<const u4 *>(p + 1024 * j + 16 * lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kc[(4 * j + i) / kSteps][(4 * j + i) % kSteps] = codes16<BF>(words[i], cc);
+        for (int i = 0; i < 4; ++i) kc[(4 * j + i) / kSteps][(4 * j + i) % kSteps] = based_codes<BF>(words[i], cc);
     }
     const uint32_t *params = reinterpret_cast<const uint32_t *>(p + 2 * T::kCodes);
     for (int j = lane; j < 32 * NG; j += 64) shared[wave][j] = params[j];
@@ -489,7 +667,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(Kv4AttnArgs a) {
         for (int g = 0; g < NG; ++g) {
             qsum[g] += __shfl_xor(qsum[g], 16);
             qsum[g] += __shfl_xor(qsum[g], 32);
-            const float z = -16.0f * qsum[g];
+            const float z = -kCodeBase<BF> * qsum[g];
             init[g] = f4{z, z, z, z};
         }
 #pragma unroll
@@ -540,20 +718,21 @@ hipError_t by_shape(const Kv4Cache &c, F f) {
 size_t kv4_attention_workspace_bytes(const Kv4AttnArgs &a) {
     const Plan p = plan_of(a);
     if (p.chunks <= 1) return 0;
-    return (size_t)a.c.batch * a.c.kv_heads * p.row_tiles * p.chunks * 16 * p.nt * (a.c.head_dim + 2) * 4;
+    return (size_t)a.c.batch * a.c.kv_heads * p.row_tiles * p.chunks * p.rows * (a.c.head_dim + 2) * 4;
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
     const Plan p = plan_of(a);
     const dim3 grid((unsigned)p.chunks, (unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)a.c.batch);
     return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-        if (p.nt == 1)
+        if (p.rows == 16)
             attend_kernel<bf(), d(), ng(), 1><<<grid, kThreads, 0, stream>>>(a, p);
         else if constexpr (d() <= 128)
             attend_kernel<bf(), d(), ng(), 2><<<grid, kThreads, 0, stream>>>(a, p);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess && p.chunks > 1) {
-            join_kernel<bf(), d()><<<dim3(16 * p.nt, grid.y, grid.z), d(), 0, stream>>>(a, p);
+            const int rows = a.q_heads / a.c.kv_heads * a.max_q;
+            join_kernel<bf(), d()><<<dim3(std::min(p.rows, rows), grid.y, grid.z), kJoin, 0, stream>>>(a, p);
             e = hipGetLastError();
         }
         return e;

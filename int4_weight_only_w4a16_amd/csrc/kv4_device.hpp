@@ -64,34 +64,44 @@ __device__ __forceinline__ int value_word(int r32, int d) {
 __device__ __forceinline__ int value_shift(int r32) { return 4 * ((r32 & 3) + 4 * (r32 >> 4)); }
 
 // Masks of the nibble unpack, opaque to the compiler so that each pair of
-// codes is one shift and one v_and_or_b32.
+// codes is at most one shift and one v_and_or_b32.
 struct CodeConsts { uint32_t mask, one; };
 template <bool BF>
 __device__ __forceinline__ CodeConsts code_consts() {
-    CodeConsts c = BF ? CodeConsts{0x00780078u, 0x41804180u} : CodeConsts{0x03C003C0u, 0x4C004C00u};
+    CodeConsts c = BF ? CodeConsts{0x000F000Fu, 0x43004300u} : CodeConsts{0x00F000F0u, 0x54005400u};
     asm volatile("" : "+v"(c.mask), "+v"(c.one));
     return c;
 }
 
-// The eight codes of a word as 16 + c in the activation type, exactly: the
-// four bits become the top mantissa bits of 16.0.  Dword i holds nibbles i
-// and i + 4.  16 is the smallest power of two for which all sixteen values
-// share an exponent, so the sums that take the 16 off again lose least.
+// The eight codes of a word as kCodeBase + c in the activation type, exactly:
+// the four bits become mantissa bits of 64.0 (fp16) or 128.0 (bfloat16), the
+// places that one of the four pairs of nibbles already has.  Dword i holds
+// nibbles i and i + 4.
 template <bool BF>
-__device__ __forceinline__ u4 codes16(uint32_t w, const CodeConsts &c) {
+constexpr float kCodeBase = BF ? 128.0f : 64.0f;
+template <bool BF>
+__device__ __forceinline__ u4 based_codes(uint32_t w, const CodeConsts &c) {
     u4 r;
     if constexpr (BF) {
-        r[0] = ((w << 3) & c.mask) | c.one;
-        r[1] = ((w >> 1) & c.mask) | c.one;
-        r[2] = ((w >> 5) & c.mask) | c.one;
-        r[3] = ((w >> 9) & c.mask) | c.one;
+        r[0] = (w & c.mask) | c.one;
+        r[1] = ((w >> 4) & c.mask) | c.one;
+        r[2] = ((w >> 8) & c.mask) | c.one;
+        r[3] = ((w >> 12) & c.mask) | c.one;
     } else {
-        r[0] = ((w << 6) & c.mask) | c.one;
-        r[1] = ((w << 2) & c.mask) | c.one;
-        r[2] = ((w >> 2) & c.mask) | c.one;
-        r[3] = ((w >> 6) & c.mask) | c.one;
+        r[0] = ((w << 4) & c.mask) | c.one;
+        r[1] = (w & c.mask) | c.one;
+        r[2] = ((w >> 4) & c.mask) | c.one;
+        r[3] = ((w >> 8) & c.mask) | c.one;
     }
     return r;
+}
+
+// v as three bfloat16 parts, v = part 0 + part 1 + part 2 to fp32's precision.
+__device__ __forceinline__ float bf16_part(float v, int part) {
+    const float a = round_act<true>(v);
+    if (part == 0) return a;
+    const float b = round_act<true>(v - a);
+    return part == 1 ? b : round_act<true>(v - a - b);
 }
 
 // The slots that query row `i` of a sequence sees: [lo, hi).
