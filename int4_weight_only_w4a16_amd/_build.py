@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libw4a16.so")
 
 SOURCES = ("w4a16_capi.hip", "decode_gfx950.hip", "prefill_gfx950.hip", "lora_gfx950.hip",
            "probe_gfx950.hip", "kv4_capi.hip", "kv4_store_gfx950.hip", "kv4_attn_gfx950.hip",
-           "kv4_evict_gfx950.hip")
+           "kv4_prefill_gfx950.hip", "kv4_evict_gfx950.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,71 @@
+// What the attention kernels of the 4-bit key/value cache share: a workgroup's rows and
+// slots, the plan of a launch, LDS access.
+#pragma once
+
+#include "kv4_device.hpp"
+
+namespace w4a16 {
+
+// A launch: rows of a workgroup's tile of rows, tiles of rows, tiles of slots of a workgroup
+// (a chunk), chunks.  Partial results of one (sequence, head, tile of rows, chunk): rows x (D
+// sums), rows references, rows sums of p.
+struct Plan {
+    int rows, row_tiles, chunk, chunks;
+};
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kNone = -3e38f;        // reference of a row that has seen nothing
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What a workgroup works on: a tile of rows of one head of one sequence, and
+// a range of its slots.
+struct Work {
+    int b, h, len, n, first;      // sequence, head, slots, new tokens, row of q of the first new token
+    int row0, rows;               // first row of the tile; rows of the sequence
+    int t0, t1;                   // tiles of slots that any row of the tile sees
+};
+
+__device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int row0, int rows_per, Work *w) {
+    const int64_t first = a.cu[b];
+    const int64_t n64 = min((int64_t)a.cu[b + 1], a.T) - first;
+    if (first < 0 || n64 <= 0) return false;
+    w->b = b;
+    w->h = h;
+    w->first = (int)first;
+    w->n = (int)min(n64, (int64_t)a.max_q);
+    const int64_t cap = (int64_t)a.c.table_stride * a.c.tiles_per_page * 32;
+    w->len = (int)min((int64_t)min(max(a.kv_len[b], 0), a.max_kv), cap);
+    const int G = a.q_heads / a.c.kv_heads;
+    w->row0 = row0;
+    w->rows = w->n * G;
+    if (row0 >= w->rows) return false;
+    const int last = min(row0 + rows_per, w->rows) - 1;
+    const int lo = row_lo(row0 / G, w->n, w->len, a.window);
+    const int hi = row_hi(last / G, w->n, w->len, a.causal);
+    w->t0 = lo >> 5;
+    w->t1 = hi > lo ? (hi + 31) >> 5 : w->t0;
+    return true;
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) void lds_void;
+template <typename T>
+__device__ __forceinline__ T lds_get(const lds_u8 *p) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) T *>(p);
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
+    *reinterpret_cast<__attribute__((address_space(3))) T *>(p) = v;
+}
+
+
+}  // namespace
+
+// The kernel for many rows, and its plan (kv4_prefill_gfx950.hip).
+Plan prefill_plan(const Kv4AttnArgs &a);
+hipError_t launch_kv4_prefill(const Kv4AttnArgs &a, const Plan &p, hipStream_t stream);
+
+}  // namespace w4a16

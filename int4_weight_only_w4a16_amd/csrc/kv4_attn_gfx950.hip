@@ -20,16 +20,12 @@
 
 #include <algorithm>
 
-#include "kv4_device.hpp"
+#include "kv4_attn.hpp"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr float kSlack = 2.0f;
-constexpr float kNone = -3e38f;        // reference of a row that has seen nothing
-constexpr float kLog2e = 1.4426950408889634f;
 
 // a * b with 0 * anything = 0.
 __device__ __forceinline__ float mul_legacy(float a, float b) {
@@ -38,42 +34,6 @@ __device__ __forceinline__ float mul_legacy(float a, float b) {
     return r;
 }
 
-// What a workgroup works on: a tile of rows of one head of one sequence, and
-// a range of its slots.
-struct Work {
-    int b, h, len, n, first;      // sequence, head, slots, new tokens, row of q of the first new token
-    int row0, rows;               // first row of the tile; rows of the sequence
-    int t0, t1;                   // tiles of slots that any row of the tile sees
-};
-
-__device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int row0, int rows_per, Work *w) {
-    const int64_t first = a.cu[b];
-    const int64_t n64 = min((int64_t)a.cu[b + 1], a.T) - first;
-    if (first < 0 || n64 <= 0) return false;
-    w->b = b;
-    w->h = h;
-    w->first = (int)first;
-    w->n = (int)min(n64, (int64_t)a.max_q);
-    const int64_t cap = (int64_t)a.c.table_stride * a.c.tiles_per_page * 32;
-    w->len = (int)min((int64_t)min(max(a.kv_len[b], 0), a.max_kv), cap);
-    const int G = a.q_heads / a.c.kv_heads;
-    w->row0 = row0;
-    w->rows = w->n * G;
-    if (row0 >= w->rows) return false;
-    const int last = min(row0 + rows_per, w->rows) - 1;
-    const int lo = row_lo(row0 / G, w->n, w->len, a.window);
-    const int hi = row_hi(last / G, w->n, w->len, a.causal);
-    w->t0 = lo >> 5;
-    w->t1 = hi > lo ? (hi + 31) >> 5 : w->t0;
-    return true;
-}
-
-// Rows per tile of rows: 16 NT.  Partial results of one (sequence, head, tile
-// of rows, chunk): rows x (D sums), rows references, rows sums of p.
-struct Plan {
-    int rows, row_tiles, chunk, chunks;    // chunk: tiles of slots a workgroup takes
-};
-
 // Chunks.  A few sequences: two workgroups for each CU, all of them at work at once, since a
 // workgroup's start and end cost about as much as eight tiles (one sequence of 131071 slots, 8
 // heads: 36.6 us with 512 workgroups, 39 with 1024, 43.6 with 2048).  More sequences may differ
@@ -81,9 +41,14 @@ struct Plan {
 // 512, 123 with 1024 to 3072).
 constexpr int kFewSlots = 512, kManySlots = 1536, kFewSequences = 4;
 
+// Rows above which the kernel for many rows runs.
+constexpr int kFewRows = 64;
+int rows_of(const Kv4AttnArgs &a) { return a.q_heads / a.c.kv_heads * a.max_q; }
+
 Plan plan_of(const Kv4AttnArgs &a) {
+    const int rows = rows_of(a);
+    if (rows > kFewRows) return prefill_plan(a);
     Plan p;
-    const int rows = a.q_heads / a.c.kv_heads * a.max_q;
     p.rows = rows > 16 && a.c.head_dim <= 128 ? 32 : 16;   // (256 channels: 32 would not fit the registers)
     p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
@@ -97,17 +62,6 @@ Plan plan_of(const Kv4AttnArgs &a) {
     p.chunk = (int)std::max<int64_t>(kWaves, chunk / kWaves * kWaves);
     p.chunks = std::max(1, (tiles + p.chunk - 1) / p.chunk);
     return p;
-}
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __attribute__((address_space(3))) void lds_void;
-template <typename T>
-__device__ __forceinline__ T lds_get(const lds_u8 *p) {
-    return *reinterpret_cast<const __attribute__((address_space(3))) T *>(p);
-}
-template <typename T>
-__device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
-    *reinterpret_cast<__attribute__((address_space(3))) T *>(p) = v;
 }
 
 // s_waitcnt vmcnt(n): at most n of this wave's vector memory instructions are still under way.
@@ -725,14 +679,16 @@ hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
     const Plan p = plan_of(a);
     const dim3 grid((unsigned)p.chunks, (unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)a.c.batch);
     return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-        if (p.rows == 16)
+        if (rows_of(a) > kFewRows) {
+            const hipError_t e = launch_kv4_prefill(a, p, stream);
+            if (e != hipSuccess) return e;
+        } else if (p.rows == 16)
             attend_kernel<bf(), d(), ng(), 1><<<grid, kThreads, 0, stream>>>(a, p);
         else if constexpr (d() <= 128)
             attend_kernel<bf(), d(), ng(), 2><<<grid, kThreads, 0, stream>>>(a, p);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess && p.chunks > 1) {
-            const int rows = a.q_heads / a.c.kv_heads * a.max_q;
-            join_kernel<bf(), d()><<<dim3(std::min(p.rows, rows), grid.y, grid.z), kJoin, 0, stream>>>(a, p);
+            join_kernel<bf(), d()><<<dim3(std::min(p.rows, rows_of(a)), grid.y, grid.z), kJoin, 0, stream>>>(a, p);
             e = hipGetLastError();
         }
         return e;
