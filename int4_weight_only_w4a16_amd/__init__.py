@@ -480,6 +480,13 @@ def linear(x, qweight, scales, group_size: int, out=None, stream=None,
 
 
 from . import kv4  # noqa: E402  (needs the names above)
-from .kv4 import (W4A16_NONCAUSAL, W4A16_ROPE_INTERLEAVED, kv4_append,  # noqa: E402,F401
-                  kv4_attention, kv4_attention_mass, kv4_attention_workspace_bytes, kv4_evict,
-                  kv4_new_pages, kv4_page_bytes, kv4_read, qk_norm_rope)
+from .kv4 import (W4A16_NONCAUSAL, W4A16_ROPE_INTERLEAVED, kv4_attention_workspace_bytes,  # noqa: E402,F401
+                  kv4_new_pages, kv4_page_bytes)
+
+
+def __getattr__(name: str):
+    """The operators of kv4, loaded with their binding when first used."""
+    if name not in kv4.OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = kv4.operator(name)
+    return globals()[name]
