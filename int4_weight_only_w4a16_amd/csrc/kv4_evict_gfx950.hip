@@ -7,10 +7,12 @@
 // the order it had, to slots 0 .. of another table's pages: nothing is read
 // that the same call writes, so all tiles move at the same time.
 //
-// select_kernel: the threshold by a radix selection over eight bits at a time
-// (a histogram in LDS, integer counts, so the order of the adds does not
-// matter), then the kept slots in order by a scan.  Bound by the passes over
-// the weights, which stay in L2.
+// select_kernel: a workgroup per sequence and head.  The threshold by a radix
+// selection over 11, 11 and 10 bits (a histogram in LDS; integer counts, so the
+// order of the adds does not matter): 11 bits first, since the weights' few
+// exponents alone would send a wave's adds to a handful of counters.  Then each
+// wave counts its part of the slots, and after one exchange of counts writes
+// them in order.  Bound by latency: five passes over weights that stay in L2.
 // copy_kernel: a workgroup per tile of the destination.
 
 #include "kv4_device.hpp"
@@ -56,63 +58,102 @@ __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
     }
     if (want == 0) return;
 
-    __shared__ unsigned hist[256];
-    __shared__ unsigned s_prefix, s_left;
-    __shared__ unsigned waves[kSelect / 64];
+    constexpr int kBins = 2048, kWaves = kSelect / 64;
+    __shared__ unsigned hist[kBins];
+    __shared__ unsigned s_bin, s_left;
+    __shared__ unsigned counts[kWaves], counts2[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t prefix = 0;                         // the threshold's known high bits
     unsigned left = want;                        // how many to take among those with that prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digit = pass < 2 ? 2047u : 1023u;
+        for (int i = threadIdx.x; i < kBins; i += kSelect) hist[i] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < old; i += kSelect) {
-            const uint32_t k = key_of(acc[i]);
-            if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        for (int i0 = threadIdx.x; i0 < old; i0 += 8 * kSelect) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + j * kSelect, old - 1)];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t k = key_of(f[j]);
+                const uint32_t high = pass == 0 ? 0u : pass == 1 ? k >> 21 : k >> 10;
+                if (i0 + j * kSelect < old && high == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+            }
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            unsigned n = left;
-            int bin = 255;
-            while (hist[bin] < n) n -= hist[bin--];      // (the counts above add up to at least `left`)
-            s_prefix = prefix << 8 | (unsigned)bin;
-            s_left = n;
+        // the bin, counted from the top, in which `left` is reached: thread t has bins 2047 - 2t
+        // and 2046 - 2t, a scan over the workgroup the counts above them
+        const unsigned h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
+        unsigned run = h0 + h1;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const unsigned up = __shfl_up(run, d);
+            if (lane >= d) run += up;
+        }
+        if (lane == 63) counts[wave] = run;
+        __syncthreads();
+        unsigned above = run - h0 - h1;
+        for (int j = 0; j < wave; ++j) above += counts[j];
+        if (above < left && above + h0 >= left) {
+            s_bin = kBins - 1 - 2 * threadIdx.x;
+            s_left = left - above;
+        } else if (above + h0 < left && above + h0 + h1 >= left) {
+            s_bin = kBins - 2 - 2 * threadIdx.x;
+            s_left = left - above - h0;
         }
         __syncthreads();
-        prefix = s_prefix;
+        prefix = prefix << (pass < 2 ? 11 : 10) | s_bin;
         left = s_left;
         __syncthreads();
     }
-    // slots above the threshold, and the first `left` equal to it
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    unsigned above0 = 0, equal0 = 0;             // counts before this chunk
-    for (int i0 = 0; i0 < old; i0 += kSelect) {
-        const int i = i0 + threadIdx.x;
-        const float f = i < old ? acc[i] : 0.f;
-        const uint32_t k = key_of(f);
-        const bool above = i < old && k > prefix, equal = i < old && k == prefix;
-        const uint64_t ma = __builtin_amdgcn_ballot_w64(above), me = __builtin_amdgcn_ballot_w64(equal);
-        const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
-        unsigned na = __popcll(ma & below), ne = __popcll(me & below);
-        if (lane == 0) waves[wave] = (unsigned)__popcll(ma) | (unsigned)__popcll(me) << 16;
-        __syncthreads();
-        unsigned all = 0;
-        for (int j = 0; j < kSelect / 64; ++j) {
-            const unsigned c = waves[j];
-            if (j < wave) {
-                na += c & 0xFFFFu;
-                ne += c >> 16;
+    // slots above the threshold, and the first `left` equal to it: a part of the slots, whole
+    // groups of 64, for each wave
+    const int part = ((old + 63) / 64 + kWaves - 1) / kWaves * 64;
+    const int from = min(wave * part, old), to = min(from + part, old);
+    const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
+    unsigned na = 0, ne = 0;
+    for (int i0 = from; i0 < to; i0 += 8 * 64) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + 64 * j + lane, to - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = i0 + 64 * j + lane < to;
+            const uint32_t k = key_of(f[j]);
+            na += __popcll(__builtin_amdgcn_ballot_w64(in && k > prefix));
+            ne += __popcll(__builtin_amdgcn_ballot_w64(in && k == prefix));
+        }
+    }
+    if (lane == 0) {
+        counts[wave] = na;
+        counts2[wave] = ne;
+    }
+    __syncthreads();
+    na = ne = 0;
+    for (int j = 0; j < wave; ++j) {
+        na += counts[j];
+        ne += counts2[j];
+    }
+    for (int i0 = from; i0 < to; i0 += 8 * 64) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + 64 * j + lane, to - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + 64 * j + lane;
+            const uint32_t k = key_of(f[j]);
+            const bool above = i < to && k > prefix, equal = i < to && k == prefix;
+            const uint64_t ma = __builtin_amdgcn_ballot_w64(above), me = __builtin_amdgcn_ballot_w64(equal);
+            const unsigned a0 = na + __popcll(ma & below), e0 = ne + __popcll(me & below);
+            if (above || (equal && e0 < left)) {
+                const unsigned at = a0 + min(e0, left);
+                kept[at] = i;
+                out[at] = f[j];
             }
-            all += c;                            // each half at most 1024
+            na += __popcll(ma);
+            ne += __popcll(me);
         }
-        na += above0;
-        ne += equal0;
-        if (above || (equal && ne < left)) {
-            const unsigned at = na + min(ne, left);
-            kept[at] = i;
-            out[at] = f;
-        }
-        above0 += all & 0xFFFFu;
-        equal0 += all >> 16;
-        __syncthreads();
     }
 }
 
@@ -127,40 +168,72 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(Kv4EvictArgs a) {
     if (base >= len) return;
     uint8_t *dst = tile_at<D, NG>(a.c, a.dst_table, a.dst_stride, b, h, tile);
     if (!dst) return;
-    if (threadIdx.x < 32) {
-        const int i = base + threadIdx.x;
+    __shared__ uint32_t there_mask;              // bit r32: the slot has a source
+    if (threadIdx.x < 64) {
+        // (the others take part as slot 0 of the destination: loads without conditions, of which
+        // nothing is used)
+        const int i = threadIdx.x < 32 ? base + (int)threadIdx.x : len;
         const uint8_t *p = nullptr;
         int s = 0;
         if (i < len) {
             s = a.kept[((int64_t)b * a.c.kv_heads + h) * a.budget + i];
             p = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b, h, s >> 5);
         }
-        from[threadIdx.x] = reinterpret_cast<const uint32_t *>(p);
-        slot[threadIdx.x] = s & 31;
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(p != nullptr);
+        if (threadIdx.x < 32) {
+            from[threadIdx.x] = reinterpret_cast<const uint32_t *>(p ? p : dst);
+            slot[threadIdx.x] = p ? s & 31 : 0;
+        }
+        if (threadIdx.x == 0) there_mask = (uint32_t)mask;
     }
     __syncthreads();
+    const uint32_t there = there_mask;
     uint32_t *words = reinterpret_cast<uint32_t *>(dst);
-    for (int idx = threadIdx.x; idx < 32 * (D / 8); idx += kCopy) {
-        const int r32 = idx / (D / 8), i = idx % (D / 8);
-        if (from[r32]) words[key_word<D>(r32, i)] = from[r32][key_word<D>(slot[r32], i)];
-    }
     constexpr int kCodeWords = T::kCodes / 4;
-    for (int at = threadIdx.x; at < 4 * D; at += kCopy) {
-        const int lane = (at >> 2) & 63;
+    constexpr int kKeyWords = 32 * (D / 8) / kCopy, kValueWords = 4 * D / kCopy ? 4 * D / kCopy : 1;
+    static_assert(32 * (D / 8) % kCopy == 0, "a whole number of key words a thread");
+    uint32_t keys[kKeyWords], values[kValueWords][8];
+#pragma unroll
+    for (int k = 0; k < kKeyWords; ++k) {
+        const int idx = threadIdx.x + k * kCopy, r32 = idx / (D / 8), i = idx % (D / 8);
+        keys[k] = from[r32][key_word<D>(slot[r32], i)];
+    }
+#pragma unroll
+    for (int k = 0; k < kValueWords; ++k) {
+        const int at = threadIdx.x + k * kCopy, lane = (at >> 2) & 63;
         const int d = 16 * (4 * (at >> 8) + (at & 3)) + (lane & 15);
-        uint32_t w = 0;
 #pragma unroll
         for (int nib = 0; nib < 8; ++nib) {
             const int r32 = 4 * (lane >> 4) + (nib & 3) + 16 * (nib >> 2);
-            const uint32_t *p = from[r32];
-            if (p)
-                w |= (p[kCodeWords + value_word(slot[r32], d)] >> value_shift(slot[r32]) & 15u) << (4 * nib);
+            values[k][nib] = from[r32][kCodeWords + value_word(slot[r32], d)] >> value_shift(slot[r32]) & 15u;
+        }
+    }
+    uint32_t params[(64 * NG + kCopy - 1) / kCopy];
+#pragma unroll
+    for (int k = 0; k < (64 * NG + kCopy - 1) / kCopy; ++k) {
+        const int at = threadIdx.x + k * kCopy, r32 = at & 31;
+        if (at < 64 * NG) params[k] = from[r32][2 * kCodeWords + (at & ~31) + slot[r32]];
+    }
+#pragma unroll
+    for (int k = 0; k < kKeyWords; ++k) {
+        const int idx = threadIdx.x + k * kCopy, r32 = idx / (D / 8);
+        if (there >> r32 & 1) words[key_word<D>(r32, idx % (D / 8))] = keys[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kValueWords; ++k) {
+        const int at = threadIdx.x + k * kCopy;
+        uint32_t w = 0;
+#pragma unroll
+        for (int nib = 0; nib < 8; ++nib) {
+            const int r32 = 4 * (((at >> 2) & 63) >> 4) + (nib & 3) + 16 * (nib >> 2);
+            if (there >> r32 & 1) w |= values[k][nib] << (4 * nib);
         }
         words[kCodeWords + at] = w;
     }
-    for (int at = threadIdx.x; at < 64 * NG; at += kCopy) {
-        const int r32 = at & 31;
-        if (from[r32]) words[2 * kCodeWords + at] = from[r32][2 * kCodeWords + (at & ~31) + slot[r32]];
+#pragma unroll
+    for (int k = 0; k < (64 * NG + kCopy - 1) / kCopy; ++k) {
+        const int at = threadIdx.x + k * kCopy;
+        if (at < 64 * NG && (there >> (at & 31) & 1)) words[2 * kCodeWords + at] = params[k];
     }
 }
 

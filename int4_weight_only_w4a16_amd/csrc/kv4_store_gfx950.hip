@@ -244,32 +244,67 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv4AppendArgs a, int t
     }
 }
 
-// 32 rows of one head: the last cu[b + 1] - cu[b] slots of each sequence b, as
-// values m + s c (exact in fp32 up to one rounding) rounded to the activation type.
+// Rows of one head: the last cu[b + 1] - cu[b] slots of each sequence b, as values m + s c (exact
+// in fp32 up to one rounding) rounded to the activation type.  A workgroup takes 32 rows.  Where
+// they are one sequence's, the two tiles that they lie in are copied to LDS whole (16-byte
+// loads, each word once for the eight slots in it); else each row reads its own words.
+constexpr int kSearch = 1024;      // sequences whose ends fit LDS
 template <bool BF, int D, int NG>
 __global__ void __launch_bounds__(kThreads) read_kernel(Kv4ReadArgs a) {
     constexpr int kLanes = D / 8;
     using T = Tile<D, NG>;
-    __shared__ int seq0;
-    const int h = blockIdx.y;
+    __shared__ __align__(16) uint8_t tiles[2 * T::kBytes];
+    __shared__ int ends[kSearch];
+    const int h = blockIdx.y, batch = a.c.batch;
     const int64_t row0 = (int64_t)blockIdx.x * 32;
-    if (threadIdx.x == 0) seq0 = 0;
-    __syncthreads();
-    // the sequence of row0: how many sequences end at or before it
-    int ended = 0;
-    for (int b = threadIdx.x; b < a.c.batch; b += kThreads) ended += a.cu[b + 1] <= row0 ? 1 : 0;
-    if (ended) atomicAdd(&seq0, ended);
-    __syncthreads();
+    const bool in_lds = batch <= kSearch;
+    if (in_lds) {
+        for (int b = threadIdx.x; b < batch; b += kThreads) ends[b] = a.cu[b + 1];
+        __syncthreads();
+    }
+    // the sequence that a row belongs to: the first that ends after it
+    auto sequence_of = [&](int64_t row) {
+        int lo = 0, hi = batch;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if ((in_lds ? ends[mid] : a.cu[mid + 1]) <= row)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    const int64_t last = min(row0 + 31, a.rows - 1);
+    const int b0 = __builtin_amdgcn_readfirstlane(sequence_of(row0));
+    const int64_t end0 = b0 < batch ? a.cu[b0 + 1] : 0;
+    const int slot0 = b0 < batch ? a.kv_len[b0] - (int)(end0 - row0) : 0;
+    const bool one = b0 < batch && last < end0 && slot0 >= 0;      // all rows are b0's, from slot0 on
+    const uint8_t *from0 = nullptr, *from1 = nullptr;
+    if (one) {
+        from0 = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b0, h, slot0 >> 5);
+        from1 = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b0, h, (slot0 >> 5) + 1);
+        for (int i = threadIdx.x; i < T::kBytes / 16; i += kThreads) {
+            if (from0) reinterpret_cast<u4 *>(tiles)[i] = reinterpret_cast<const u4 *>(from0)[i];
+            if (from1 && slot0 % 32) reinterpret_cast<u4 *>(tiles + T::kBytes)[i] = reinterpret_cast<const u4 *>(from1)[i];
+        }
+        __syncthreads();
+    }
     for (int idx = threadIdx.x; idx < 32 * kLanes; idx += kThreads) {
         const int64_t row = row0 + idx / kLanes;
         const int i = idx % kLanes;
         if (row >= a.rows) return;
-        int b = seq0;
-        while (b < a.c.batch && a.cu[b + 1] <= row) ++b;
-        if (b >= a.c.batch) return;
-        const int slot = a.kv_len[b] - (int)(a.cu[b + 1] - row);
-        const uint8_t *p = slot < 0 ? nullptr
-                                    : tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b, h, slot >> 5);
+        const uint8_t *p;
+        int slot;
+        if (one) {
+            slot = slot0 + idx / kLanes;
+            const bool second = (slot >> 5) != (slot0 >> 5);
+            p = (second ? from1 : from0) ? tiles + (second ? T::kBytes : 0) : nullptr;
+        } else {
+            const int b = sequence_of(row);
+            if (b >= batch) return;
+            slot = a.kv_len[b] - (int)(a.cu[b + 1] - row);
+            p = slot < 0 ? nullptr : tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b, h, slot >> 5);
+        }
         const int r32 = slot & 31, g = 8 * i / T::kGroup;
         float k[8], v[8];
         if (p) {
