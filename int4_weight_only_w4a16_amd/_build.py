@@ -16,7 +16,8 @@ BINDING_PATH = os.path.join(PKG_DIR, "_kv4.so")
 
 SOURCES = ("w4a16_capi.hip", "decode_gfx950.hip", "prefill_gfx950.hip", "lora_gfx950.hip",
            "probe_gfx950.hip", "kv4_capi.hip", "kv4_store_gfx950.hip", "kv4_attn_gfx950.hip",
-           "kv4_prefill_gfx950.hip", "kv4_evict_gfx950.hip")
+           "kv4_prefill_gfx950.hip", "kv4_mass_gfx950.hip",
+           "kv4_evict_gfx950.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

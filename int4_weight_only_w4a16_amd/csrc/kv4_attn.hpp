@@ -62,6 +62,21 @@ __device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
 }
 
 
+// A workgroup barrier for LDS alone: this wave's LDS operations are done, and loads from memory
+// stay under way (__syncthreads waits for those too).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// s_waitcnt vmcnt(n): at most n of this wave's vector memory instructions are still under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
 }  // namespace
 
 // The kernel for many rows, and its plan (kv4_prefill_gfx950.hip).

@@ -64,13 +64,6 @@ Plan plan_of(const Kv4AttnArgs &a) {
     return p;
 }
 
-// s_waitcnt vmcnt(n): at most n of this wave's vector memory instructions are still under way.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    static_assert(N < 64, "six bits");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
 // One tile copied to LDS without passing through registers (lane l's 16 bytes of an
 // instruction land at 16 l): the codes 1 KiB an instruction, the parameters 256 bytes, or
 // 1 KiB where there are that many.  `bytes` 0 reads nothing and writes zeros.
@@ -554,111 +547,6 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Kv4AttnArgs a, Plan plan) {
         a.lse[at * a.q_heads + head] = total == 0.f ? -__builtin_inff() : (m + __log2f(total)) * (1.0f / kLog2e);
 }
 
-// acc[b, h, t] += sum over the rows of head h of exp(scale q . k_t - lse): a
-// wave owns a tile of slots, so every sum has one owner and one order.
-template <bool BF, int D, int NG>
-__global__ void __launch_bounds__(kThreads) mass_kernel(Kv4AttnArgs a) {
-    using T = Tile<D, NG>;
-    constexpr int kSteps = D / 32, kPer = kSteps / NG;
-    __shared__ __align__(16) uint32_t shared[kWaves][32 * NG];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, b4 = lane >> 4;
-    Work w;
-    if (!work_of(a, blockIdx.z, blockIdx.y, 0, 0x3fffffff, &w)) return;
-    const int tile = w.t0 + (int)blockIdx.x * kWaves + wave;
-    if (tile >= w.t1) return;
-    const uint8_t *p = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, w.b, w.h, tile);
-    if (!p) return;
-    const CodeConsts cc = code_consts<BF>();
-    u4 kc[2][kSteps];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-        const u4 words = *reinterpret_cast<const u4 *>(p + 1024 * j + 16 * lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kc[(4 * j + i) / kSteps][(4 * j + i) % kSteps] = based_codes<BF>(words[i], cc);
-    }
-    const uint32_t *params = reinterpret_cast<const uint32_t *>(p + 2 * T::kCodes);
-    for (int j = lane; j < 32 * NG; j += 64) shared[wave][j] = params[j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    float st[NG][8], off[NG][8];
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t v = shared[wave][32 * g + 16 * (e >> 2) + 4 * b4 + (e & 3)];
-            st[g][e] = par_step<BF>(v);
-            off[g][e] = par_offset<BF>(v);
-        }
-    const int G = a.q_heads / a.c.kv_heads, base = 32 * tile;
-    const float c1 = a.scale * kLog2e;
-    // rows that see any slot of the tile: with a causal mask those from the slots' own on
-    const int i0 = a.causal ? max(0, base - (w.len - w.n)) : 0;
-    const int i1 = a.window > 0 ? min(w.n, base + 31 + a.window - (w.len - w.n)) : w.n;
-    float mass[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int row0 = i0 * G / 16 * 16; row0 < i1 * G; row0 += 16) {
-        const int row = row0 + r;
-        const bool there = row < w.rows;
-        const int i = there ? row / G : 0;
-        const int head = w.h * G + (there ? row - i * G : 0);
-        const int lo = there ? row_lo(i, w.n, w.len, a.window) : 0;
-        const int hi = there ? row_hi(i, w.n, w.len, a.causal) : 0;
-        const int64_t token = w.first + i;
-        const uint16_t *src = static_cast<const uint16_t *>(a.q) + token * a.q_stride + (int64_t)head * D + 8 * b4;
-        const float lse = a.lse[token * a.q_heads + head];
-        const float shift = lse == -__builtin_inff() ? lse : -lse * kLog2e;     // (a row that saw nothing adds nothing)
-        u4 q[kSteps];
-        float qsum[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) qsum[g] = 0.f;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            q[j] = *reinterpret_cast<const u4 *>(src + 32 * j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) qsum[j / kPer] += lo_f32<BF>(q[j][e]) + hi_f32<BF>(q[j][e]);
-        }
-        f4 init[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            qsum[g] += __shfl_xor(qsum[g], 16);
-            qsum[g] += __shfl_xor(qsum[g], 32);
-            const float z = -kCodeBase<BF> * qsum[g];
-            init[g] = f4{z, z, z, z};
-        }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            float x[4];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                f4 acc = init[g];
-#pragma unroll
-                for (int j = g * kPer; j < (g + 1) * kPer; ++j) acc = mfma16x16x32_t<BF>(kc[sub][j], q[j], acc);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = g == 0 ? off[0][4 * sub + e] * qsum[0] : __builtin_fmaf(off[g][4 * sub + e], qsum[g], x[e]);
-                    x[e] = __builtin_fmaf(st[g][4 * sub + e], acc[e], x[e]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int slot = base + 16 * sub + 4 * b4 + e;
-                const bool ok = slot >= lo && slot < hi;
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c1, shift));
-                mass[4 * sub + e] += ok ? y : 0.f;
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) mass[e] += __shfl_xor(mass[e], d);
-        const int slot = base + 16 * (e >> 2) + 4 * b4 + (e & 3);
-        if (r == 0 && slot < w.len) {
-            float *to = a.acc + ((int64_t)w.b * a.c.kv_heads + w.h) * a.acc_stride + slot;
-            *to += mass[e];
-        }
-    }
-}
-
 template <typename F>
 hipError_t by_shape(const Kv4Cache &c, F f) {
     auto typed = [&](auto d, auto ng) {
@@ -692,15 +580,6 @@ hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
             e = hipGetLastError();
         }
         return e;
-    });
-}
-
-hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream) {
-    const int tiles = (a.max_kv + 31) / 32;
-    const dim3 grid((unsigned)((tiles + kWaves - 1) / kWaves), (unsigned)a.c.kv_heads, (unsigned)a.c.batch);
-    return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-        mass_kernel<bf(), d(), ng()><<<grid, kThreads, 0, stream>>>(a);
-        return hipGetLastError();
     });
 }
 

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     parameters(chunk0, lds);
     bool now0 = exists0, now1 = exists1;
     fetch();
-    __syncthreads();
+    lds_barrier();
     int stage = 0;
     for (int tile = chunk0; tile < chunk1; tile += 2) {
         const lds_u8 *const at = lds + stage * Shape::kStage;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         now0 = exists0;
         now1 = exists1;
         fetch();
-        __syncthreads();
+        lds_barrier();
     }
 
     // ---- the rows' results: register 4 i + e of block o holds channel 32 o + 8 i + 4 half + e ----
