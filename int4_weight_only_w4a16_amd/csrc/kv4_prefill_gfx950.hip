@@ -40,7 +40,7 @@ template <int D, int NG>
 struct ManyShape {
     static constexpr int kWaves = kManyThreads<D> / 64;
     static constexpr int kRows = 32 * kWaves;
-    static constexpr int kTerms = (kPairs * NG + 15) / 16;      // 16-deep products of the offset term
+    static constexpr int kTerms = (kPairs * NG + 3 + 15) / 16;  // 16-deep products of the offset term
     // one stage: two tiles' key operands, value operands, offset operands, steps, NaN masks
     static constexpr int kKeys = 64 * D;                        // bytes of one tile's
     static constexpr int kValues = 64 * D;
@@ -294,7 +294,9 @@ __global__ void __launch_bounds__(kManyThreads<D>)
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             const int k = 16 * term + 8 * hh + 2 * e + o;
-                            if (k < kPairs * NG && wave == hh) f[o] = bf16_part(off[k % NG], part_of_offset(k / NG));
+                            if (wave != hh) continue;
+                        if (k < kPairs * NG) f[o] = bf16_part(off[k % NG], part_of_offset(k / NG));
+                        else if (k < kPairs * NG + 3) f[o] = 1.0f;       // the reference's parts
                         }
                     }
                     v[e] = pack2<true>(f[0], f[1]);
@@ -305,11 +307,11 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     };
 
     // ---- the softmax of a stage's 64 slots and its products ----
-    // x = c1 q . k - ref comes out of the first products as it is: -ref is what they start from
+    // x = c1 q . k - ref comes out of the first products as it is: -ref, in three parts, has
+    // places of its own in the offset term
     float ref = kNone, sum = 0.f, nans[NG];      // nans: NaN once the row saw one in that group, else 0
-    f16v out[kOut], start;
+    f16v out[kOut];
     const f16v zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    start = zero;
 #pragma unroll
     for (int g = 0; g < NG; ++g) nans[g] = 0.f;
 #pragma unroll
@@ -317,11 +319,12 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     auto logits = [&](const lds_u8 *at, int t) {
         const lds_u8 *const keys = at + t * Shape::kKeys + 16 * lane;
         const lds_u8 *const steps = at + Shape::kAtSteps + t * Shape::kSteps + 16 * half;
-        f16v x = start;
+        f16v x;
 #pragma unroll
         for (int term = 0; term < kTerms; ++term)
             x = mfma32x32x16_t<true>(
-                lds_get<u4>(at + Shape::kAtOffsets + t * Shape::kOffsets + 1024 * term + 16 * lane), sums[term], x);
+                lds_get<u4>(at + Shape::kAtOffsets + t * Shape::kOffsets + 1024 * term + 16 * lane), sums[term],
+                term ? x : zero);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f16v acc;
@@ -350,7 +353,14 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         for (int i = 0; i < 16; ++i) {
             x[0][i] -= by;
             x[1][i] -= by;
-            start[i] -= by;
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            constexpr int kFirst = kPairs * NG;
+            const int k = kFirst + part, t = k / 16, e = k % 8 / 2;
+            const uint32_t bits = pack2<true>(bf16_part(ref == kNone ? 0.f : -ref, part), 0.f);
+            const uint32_t both = k % 2 ? (sums[t][e] & 0xFFFFu) | bits << 16 : (sums[t][e] & 0xFFFF0000u) | bits;
+            if (half == k % 16 / 8) sums[t][e] = both;
         }
 #pragma unroll
         for (int o = 0; o < kOut; ++o) out[o] *= f;
