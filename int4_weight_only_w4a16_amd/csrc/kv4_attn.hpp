@@ -62,6 +62,12 @@ __device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
 }
 
 
+// One KiB from `base + at` to LDS without passing through registers, lane l's 16 bytes to 16 l; what
+// lies at or past base + bytes comes as zeros.
+__device__ __forceinline__ void copy_kib(const uint8_t *base, uint32_t bytes, uint32_t at, lds_u8 *to, int lane) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_void *)to, 16, 16 * lane, at, 0, 0);
+}
+
 // A workgroup barrier for LDS alone: this wave's LDS operations are done, and loads from memory
 // stay under way (__syncthreads waits for those too).
 __device__ __forceinline__ void lds_barrier() {

@@ -38,20 +38,28 @@ constexpr int kManyThreads = D <= 128 ? 512 : 256;
 
 template <int D, int NG>
 struct ManyShape {
+    using T = Tile<D, NG>;
     static constexpr int kWaves = kManyThreads<D> / 64;
     static constexpr int kRows = 32 * kWaves;
+    static constexpr int kTiles = D <= 128 ? 2 : 1;             // tiles of a stage
     static constexpr int kTerms = (kPairs * NG + 3 + 15) / 16;  // 16-deep products of the offset term
-    // one stage: two tiles' key operands, value operands, offset operands, steps, NaN masks
+    // one stage: the tiles' key operands, value operands, offset operands, steps, NaN masks
     static constexpr int kKeys = 64 * D;                        // bytes of one tile's
     static constexpr int kValues = 64 * D;
     static constexpr int kOffsets = 1024 * kTerms;
     static constexpr int kSteps = 128 * NG;
-    static constexpr int kAtValues = 2 * kKeys;
-    static constexpr int kAtOffsets = kAtValues + 2 * kValues;
-    static constexpr int kAtSteps = kAtOffsets + 2 * kOffsets;
-    static constexpr int kAtBad = kAtSteps + 2 * kSteps;
+    static constexpr int kAtValues = kTiles * kKeys;
+    static constexpr int kAtOffsets = kAtValues + kTiles * kValues;
+    static constexpr int kAtSteps = kAtOffsets + kTiles * kOffsets;
+    static constexpr int kAtBad = kAtSteps + kTiles * kSteps;
     static constexpr int kStage = kAtBad + 80;
-    static_assert(4 + 2 * NG * 4 <= 80, "NaN masks");
+    static_assert(4 + kTiles * NG * 4 <= 80, "NaN masks");
+    // the packed tiles on their way: a ring of three stages' worth, a KiB a copy instruction
+    static constexpr int kRawTile = (T::kBytes + 1023) / 1024 * 1024;
+    static constexpr int kRing = 3;
+    static constexpr int kCopies = (kTiles * kRawTile / 1024 + kWaves - 1) / kWaves;     // of a stage in each wave
+    static constexpr int kAtRaw = 2 * kStage / 1024 * 1024 + 1024;
+    static constexpr int kLds = kAtRaw + kRing * kTiles * kRawTile;
 };
 
 __device__ __forceinline__ int row_of_slot(int s) { return (s & 7) | (s & 8) << 1 | (s & 16) >> 1; }
@@ -61,18 +69,16 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     __attribute__((amdgpu_waves_per_eu(D <= 128 ? 2 : 1, D <= 128 ? 2 : 1))) prefill_kernel(Kv4AttnArgs a, Plan plan) {
     using T = Tile<D, NG>;
     using Shape = ManyShape<D, NG>;
-    constexpr int kTerms = Shape::kTerms, kWaves = Shape::kWaves;
+    constexpr int kTerms = Shape::kTerms, kWaves = Shape::kWaves, kTiles = Shape::kTiles, kRing = Shape::kRing;
     constexpr int kDeep = D / 16;                 // 16-channel products
     constexpr int kPer = kDeep / NG;              // of them per group
     constexpr int kOut = D / 32;                  // 32-channel blocks of the output
-    // codes of a stage: D/32 KiB of keys and as much of values, in each wave kUnits times kWords
-    // of the four words that a lane of such a KiB has
-    constexpr int kAll = D / 32;
-    constexpr int kUnits = kAll > kWaves ? kAll / kWaves : 1;
-    constexpr int kParts = kAll > kWaves ? 1 : kWaves / kAll;
-    constexpr int kWords = 4 / kParts;
+    // codes of a stage: kAll KiB of keys and as much of values, in each wave kWords of the four
+    // words that a lane of one such KiB has
+    constexpr int kAll = kTiles * (D / 64), kParts = kWaves / kAll, kWords = 4 / kParts;
+    static_assert(kAll * kParts == kWaves && kWords * kParts == 4, "every wave has the same share");
     constexpr int kValGroups = T::kGroup == 32 && kWords == 4 ? 2 : 1;     // groups that they touch
-    __shared__ __align__(16) uint8_t lds_raw[2 * Shape::kStage];
+    __shared__ __align__(16) uint8_t lds_raw[Shape::kLds];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -136,146 +142,138 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-    // ---- unpacking: two tiles from memory into a stage of LDS, the same share in every wave ----
-    const float c1 = a.scale * kLog2e;
-    const CodeConsts cc = code_consts<BF>();
-    uint32_t kcodes[kUnits][kWords], vcodes[kUnits][kWords], kpar[NG];
-    u4 vpar[kUnits][kValGroups][2];
-    bool exists0 = false, exists1 = false;
-    const int r16 = lane & 15, b4 = lane >> 4;
-    // the words of this wave: unit i is a KiB of codes of keys and of values, `part` of four words
-    auto unit_of = [&](int i) { return kParts > 1 ? wave / kParts : wave + kWaves * i; };
-    const int word0 = kParts > 1 ? wave % kParts * kWords : 0;
-    // 64 page ids at a time sit in the lanes, so that no load waits for one; (page, in) is where
-    // the next tile to fetch lies
+    // ---- packed tiles into the ring ----
+    // 64 page ids at a time sit in the lanes, so that no copy waits for one; (page, in) is where
+    // the next tile to copy lies, `place` its address
     const int tpp = a.c.tiles_per_page;
     const int32_t *const table = a.c.table + (int64_t)w.b * a.c.table_stride;
-    int window = chunk0 / tpp, page = window, in = chunk0 - window * tpp, next_tile = chunk0;
+    int window = chunk0 / tpp, page = window, in = chunk0 - window * tpp, next_tile = chunk0, ring_next = 0;
     auto load_ids = [&]() { return window + lane < a.c.table_stride ? table[window + lane] : -1; };
     int ids = load_ids();
-    auto next_place = [&]() -> const uint8_t * {
-        if (next_tile >= chunk1) return nullptr;
+    const uint8_t *place = nullptr;
+    bool on_page = false;
+    auto enter_page = [&]() {
         if (page - window >= 64) {
             window = page;
             ids = load_ids();
         }
         const int id = __builtin_amdgcn_readlane(ids, page - window);
-        const uint8_t *p = (unsigned)id < (unsigned)a.c.num_pages
-                               ? a.c.pages + (((int64_t)id * kvh + w.h) * tpp + in) * T::kBytes
-                               : nullptr;
-        ++next_tile;
-        if (++in == tpp) {
-            in = 0;
-            ++page;
-        }
-        return p;
+        on_page = (unsigned)id < (unsigned)a.c.num_pages;
+        place = a.c.pages + (((int64_t)(on_page ? id : 0) * kvh + w.h) * tpp + in) * T::kBytes;
     };
-    auto fetch = [&]() {
-        const uint8_t *const p0 = next_place(), *const p1 = next_place();
-        exists0 = p0 != nullptr;
-        exists1 = p1 != nullptr;
+    enter_page();
+    // copies the tiles of the next stage; bit t of the result: tile t is there
+    auto copy = [&]() {
+        uint32_t found = 0;
+        const uint8_t *at[kTiles];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int unit = unit_of(i), chunk = unit % (D / 64);
-            const uint8_t *const t = unit >= D / 64 ? p1 : p0;
-            if (t) {
-                const uint8_t *const from = t + 1024 * chunk + 16 * lane + 4 * word0;
-                __builtin_memcpy(kcodes[i], __builtin_assume_aligned(from, 4 * kWords), 4 * kWords);
-                __builtin_memcpy(vcodes[i], __builtin_assume_aligned(from + T::kCodes, 4 * kWords), 4 * kWords);
-#pragma unroll
-                for (int g = 0; g < kValGroups; ++g) {
-                    const int group = (64 * chunk + 16 * word0) / T::kGroup + g;
-                    const uint8_t *par = t + 2 * T::kCodes + 128 * (NG + group) + 16 * b4;
-                    vpar[i][g][0] = *reinterpret_cast<const u4 *>(par);
-                    vpar[i][g][1] = *reinterpret_cast<const u4 *>(par + 64);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) kcodes[i][k] = vcodes[i][k] = 0u;
-#pragma unroll
-                for (int g = 0; g < kValGroups; ++g) vpar[i][g][0] = vpar[i][g][1] = u4{0u, 0u, 0u, 0u};
+        for (int t = 0; t < kTiles; ++t) {
+            at[t] = place;
+            found |= next_tile < chunk1 && on_page ? 1u << t : 0u;
+            ++next_tile;
+            place += T::kBytes;
+            if (++in == tpp) {
+                in = 0;
+                ++page;
+                if (next_tile < chunk1) enter_page();
             }
         }
-        // waves 0 to 2 read key parameters, wave 3 value parameters: lane l those of slot l
-        const uint8_t *mine = lane < 32 ? p0 : p1;
-        if (wave < 4)
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-                kpar[g] = mine ? *reinterpret_cast<const uint32_t *>(mine + 2 * T::kCodes +
-                                                                     128 * (g + (wave == 3 ? NG : 0)) + 4 * (lane & 31))
-                               : 0u;
+        for (int i = 0; i < Shape::kCopies; ++i) {
+            // (a wave without a copy of its own repeats the last one)
+            constexpr int kPerTile = Shape::kRawTile / 1024;
+            const int unit = min(wave + kWaves * i, kTiles * kPerTile - 1), t = unit / kPerTile, u = unit % kPerTile;
+            const uint8_t *from = kTiles > 1 && t ? at[kTiles - 1] : at[0];
+            copy_kib(from, found >> t & 1 ? T::kBytes : 0, 1024 * u,
+                     lds + Shape::kAtRaw + (ring_next * kTiles + t) * Shape::kRawTile + 1024 * u, lane);
+        }
+        ring_next = ring_next + 1 == kRing ? 0 : ring_next + 1;
+        return found;
     };
-    // slots past the sequence's: their parameters mean nothing
-    auto clear_unused = [&](int tile) {
-        if (32 * tile + 64 <= w.len) return;
-        asm volatile("");
+
+    // ---- unpacking: a stage's tiles from the ring, the same share in every wave ----
+    const float c1 = a.scale * kLog2e;
+    const CodeConsts cc = code_consts<BF>();
+    const int r16 = lane & 15, b4 = lane >> 4;
+    const int unit = wave / kParts, word0 = wave % kParts * kWords;
+    const int unit_tile = unit / (D / 64), chunk64 = unit % (D / 64);
+    auto unpack = [&](int tile, const lds_u8 *ring, lds_u8 *to) {
+        const lds_u8 *const raw = ring + unit_tile * Shape::kRawTile;
+        lds_u8 *const keys = to + unit_tile * Shape::kKeys;
+        lds_u8 *const values = to + Shape::kAtValues + unit_tile * Shape::kValues;
+        uint32_t kcodes[kWords], vcodes[kWords];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int left = w.len - 32 * (tile + unit_of(i) / (D / 64));
+        for (int k = 0; k < kWords; ++k) {
+            const lds_u8 *from = raw + 1024 * chunk64 + 16 * lane + 4 * word0;
+            kcodes[k] = lds_get<uint32_t>(from + 4 * k);
+            vcodes[k] = lds_get<uint32_t>(from + T::kCodes + 4 * k);
+        }
 #pragma unroll
-            for (int g = 0; g < kValGroups; ++g)
+        for (int k = 0; k < kWords; ++k) {
+            const int word = 4 * chunk64 + word0 + k;
+            const int row = row_of_slot(16 * (word / (D / 32)) + r16);
+            const int j = 2 * (word % (D / 32)) + (b4 >> 1);
+            lds_put(keys + 1024 * j + 16 * (32 * (b4 & 1) + row), based_codes<BF>(kcodes[k], cc));
+        }
+#pragma unroll
+        for (int g = 0; g < kValGroups; ++g) {
+            const int group = (64 * chunk64 + 16 * word0) / T::kGroup + g;
+            const lds_u8 *const par = raw + 2 * T::kCodes + 128 * (NG + group) + 16 * b4;
+            u4 p[2] = {lds_get<u4>(par), lds_get<u4>(par + 64)};
+            const int left = w.len - 32 * (tile + unit_tile);
+            if (left < 32) {                     // slots past the sequence's: their parameters mean nothing
+                asm volatile("");
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (16 * (e >> 2) + 4 * b4 + (e & 3) >= left) vpar[i][g][e >> 2][e & 3] = 0u;
-        }
-    };
-    auto unpack = [&](lds_u8 *to) {
+                    if (16 * (e >> 2) + 4 * b4 + (e & 3) >= left) p[e >> 2][e & 3] = 0u;
+            }
+            float st[8], off[8];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int unit = unit_of(i), t = unit / (D / 64), chunk = unit % (D / 64);
-            lds_u8 *const keys = to + t * Shape::kKeys;
-            lds_u8 *const values = to + Shape::kAtValues + t * Shape::kValues;
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-                const int word = 4 * chunk + word0 + k;
-                const int row = row_of_slot(16 * (word / (D / 32)) + r16);
-                const int j = 2 * (word % (D / 32)) + (b4 >> 1);
-                lds_put(keys + 1024 * j + 16 * (32 * (b4 & 1) + row), based_codes<BF>(kcodes[i][k], cc));
+            for (int e = 0; e < 8; ++e) {
+                // NaN becomes a number here; the masks below bring it back
+                st[e] = fmaxf(par_step<BF>(p[e >> 2][e & 3]), 0.f);
+                off[e] = fmaxf(par_offset<BF>(p[e >> 2][e & 3]), BF ? -3e38f : -65504.0f);
             }
 #pragma unroll
-            for (int g = 0; g < kValGroups; ++g) {
-                float st[8], off[8];
+            for (int k = g * kWords / kValGroups; k < (g + 1) * kWords / kValGroups; ++k) {
+                uint32_t even = vcodes[k] & 0x0F0F0F0Fu, odd = (vcodes[k] >> 4) & 0x0F0F0F0Fu;
+                asm("" : "+v"(even), "+v"(odd));
+                u4 v;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // NaN becomes a number here; the masks below bring it back
-                    const uint32_t p = vpar[i][g][e >> 2][e & 3];
-                    st[e] = fmaxf(par_step<BF>(p), 0.f);
-                    off[e] = fmaxf(par_offset<BF>(p), BF ? -3e38f : -65504.0f);
+                for (int e = 0; e < 4; ++e) {               // nibbles e and e + 4
+                    const uint32_t src = e & 1 ? odd : even;
+                    v[e] = pack2<BF>(__builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]),
+                                     __builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]));
                 }
-#pragma unroll
-                for (int k = g * kWords / kValGroups; k < (g + 1) * kWords / kValGroups; ++k) {
-                    uint32_t even = vcodes[i][k] & 0x0F0F0F0Fu, odd = (vcodes[i][k] >> 4) & 0x0F0F0F0Fu;
-                    asm("" : "+v"(even), "+v"(odd));
-                    u4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {               // nibbles e and e + 4
-                        const uint32_t src = e & 1 ? odd : even;
-                        v[e] = pack2<BF>(__builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]),
-                                         __builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]));
-                    }
-                    const int d = 64 * chunk + 16 * (word0 + k) + r16;
-                    lds_put(values + 1024 * (2 * (d / 32) + (b4 >> 1)) + 16 * (32 * (b4 & 1) + d % 32), v);
-                }
+                const int d = 64 * chunk64 + 16 * (word0 + k) + r16;
+                lds_put(values + 1024 * (2 * (d / 32) + (b4 >> 1)) + 16 * (32 * (b4 & 1) + d % 32), v);
             }
         }
     };
-    auto parameters = [&](int tile, lds_u8 *to) {
-        const int t = lane >> 5, s = lane & 31;
+    auto parameters = [&](int tile, const lds_u8 *ring, lds_u8 *to) {
+        const int t = kTiles > 1 ? lane >> 5 : 0, s = lane & 31;
+        if (wave > 3) return;
+        uint32_t kpar[NG];                       // wave 3: of the values
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            kpar[g] = lds_get<uint32_t>(ring + t * Shape::kRawTile + 2 * T::kCodes +
+                                        128 * (g + (wave == 3 ? NG : 0)) + 4 * s);
+        const bool lane_in = kTiles > 1 || lane < 32;        // (one tile: half a wave's slots)
         if (wave == 3) {
             // value groups with NaN: whether there are any, then a bit for each slot in use
             uint64_t any = 0;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const float st = par_step<BF>(kpar[g]);
-                const uint64_t bad = __builtin_amdgcn_ballot_w64(st != st && 32 * tile + lane < w.len);
+                const uint64_t bad = __builtin_amdgcn_ballot_w64(lane_in && st != st && 32 * tile + lane < w.len);
                 any |= bad;
-                if (lane < 2) lds_put(to + Shape::kAtBad + 4 + 4 * (2 * g + lane), (uint32_t)(bad >> (32 * lane)));
+                if (lane < kTiles) lds_put(to + Shape::kAtBad + 4 + 4 * (kTiles * g + lane), (uint32_t)(bad >> (32 * lane)));
             }
             if (lane == 0) lds_put(to + Shape::kAtBad, any ? 1u : 0u);
         } else if (wave == 2) {
 #pragma unroll
             for (int g = 0; g < NG; ++g)
-                lds_put(to + Shape::kAtSteps + t * Shape::kSteps + 4 * (32 * g + s), c1 * par_step<BF>(kpar[g]));
+                if (lane_in) lds_put(to + Shape::kAtSteps + t * Shape::kSteps + 4 * (32 * g + s), c1 * par_step<BF>(kpar[g]));
         } else if (wave < 2) {
             // offsets c1 (m - B s), half `wave` of each product's depth
             float off[NG];
@@ -301,7 +299,8 @@ __global__ void __launch_bounds__(kManyThreads<D>)
                     }
                     v[e] = pack2<true>(f[0], f[1]);
                 }
-                lds_put(to + Shape::kAtOffsets + t * Shape::kOffsets + 1024 * term + 16 * (32 * wave + row_of_slot(s)), v);
+                if (lane_in)
+                    lds_put(to + Shape::kAtOffsets + t * Shape::kOffsets + 1024 * term + 16 * (32 * wave + row_of_slot(s)), v);
             }
         }
     };
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         }
         return x;            // register 4 i + e: slot 16 (i & 1) + 8 (i >> 1) + 4 half + e of the tile
     };
-    auto move_reference = [&](float top, f16v (&x)[2]) {
+    auto move_reference = [&](float top, f16v (&x)[kTiles]) {
         top = fmaxf(top, __shfl_xor(top, 32));
         const bool unset = ref == kNone;
         // (an infinite maximum stays out of the reference: its weight becomes infinite)
@@ -350,10 +349,9 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         ref = unset ? (top > -__builtin_inff() ? by : kNone) : ref + by;
         sum *= f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[0][i] -= by;
-            x[1][i] -= by;
-        }
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[t][i] -= by;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
             constexpr int kFirst = kPairs * NG;
@@ -383,41 +381,46 @@ __global__ void __launch_bounds__(kManyThreads<D>)
                 out[o] = mfma32x32x16_t<BF>(lds_get<u4>(values + 1024 * (2 * o + s)), pw[s], out[o]);
     };
 
-    // ---- main loop: unpack the next two tiles while these are worked on ----
-    fetch();
-    clear_unused(chunk0);
-    unpack(lds);
-    parameters(chunk0, lds);
-    bool now0 = exists0, now1 = exists1;
-    fetch();
+    // ---- main loop: unpack the next stage while this one is worked on, the one after it on its way ----
+    uint32_t found = copy(), found1 = copy(), found2 = 0;
+    wait_loads<Shape::kCopies>();
     lds_barrier();
-    int stage = 0;
-    for (int tile = chunk0; tile < chunk1; tile += 2) {
+    auto raw_of = [&](int slot) { return lds + Shape::kAtRaw + slot * kTiles * Shape::kRawTile; };
+    unpack(chunk0, raw_of(0), lds);
+    parameters(chunk0, raw_of(0), lds);
+    found2 = copy();
+    wait_loads<Shape::kCopies>();
+    lds_barrier();
+    int stage = 0, ring_slot = 1;                // of the stage to unpack
+    for (int tile = chunk0; tile < chunk1; tile += kTiles) {
         const lds_u8 *const at = lds + stage * Shape::kStage;
         stage ^= 1;
         lds_u8 *const to = lds + stage * Shape::kStage;
-        clear_unused(tile + 2);
-        f16v x[2];
-        x[0] = logits(at, 0);
-        x[1] = logits(at, 1);
-        unpack(to);
-        // (pinned: else the last steps of x are taken past the branch, and all their operands live on)
-        asm volatile("" : "+v"(x[0]), "+v"(x[1]));
-        if (!now0 || !now1 || 32 * tile < all_lo || 32 * tile + 64 > all_hi) {
-            // (opaque bounds: the 64 differences with them are not kept in registers from stage to stage)
+        const lds_u8 *const ring = raw_of(ring_slot);
+        f16v x[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) x[t] = logits(at, t);
+        // (pinned: else the last steps of x are taken past the branches below, and all their operands live on)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) asm volatile("" : "+v"(x[t]));
+        unpack(tile + kTiles, ring, to);
+        if (found != (1u << kTiles) - 1 || 32 * tile < all_lo || 32 * (tile + kTiles) > all_hi) {
+            // (opaque bounds: the differences with them are not kept in registers from stage to stage)
             int from = lo - 32 * tile - 4 * half, to_slot = hi - 32 * tile - 4 * half;
             asm volatile("" : "+v"(from), "+v"(to_slot));
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int slot = 32 * t + 16 * ((i >> 2) & 1) + 8 * (i >> 3) + (i & 3);
-                    if (!((t ? now1 : now0) & (slot >= from) & (slot < to_slot))) x[t][i] = -__builtin_inff();
+                    if (!((found >> t & 1) & (slot >= from) & (slot < to_slot))) x[t][i] = -__builtin_inff();
                 }
         }
-        float top = fmaxf(x[0][0], x[1][0]);
+        float top = x[0][0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(x[0][i], x[1][i]));
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, x[t][i]);
         if (__builtin_amdgcn_ballot_w64(top > kSlackMany || (ref == kNone && top > -__builtin_inff())))
             move_reference(top, x);
         // a NaN that a row sees makes its group NaN
@@ -426,8 +429,8 @@ __global__ void __launch_bounds__(kManyThreads<D>)
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t bad = lds_get<uint32_t>(at + Shape::kAtBad + 4 + 4 * (2 * g + t));
+                for (int t = 0; t < kTiles; ++t) {
+                    const uint32_t bad = lds_get<uint32_t>(at + Shape::kAtBad + 4 + 4 * (kTiles * g + t));
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int s = 16 * ((i >> 2) & 1) + 8 * (i >> 3) + 4 * half + (i & 3);
@@ -435,14 +438,17 @@ __global__ void __launch_bounds__(kManyThreads<D>)
                     }
                 }
         }
-        products(at, 0, x[0]);
-        products(at, 1, x[1]);
-        parameters(tile + 2, to);
-        now0 = exists0;
-        now1 = exists1;
-        fetch();
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) products(at, t, x[t]);
+        parameters(tile + kTiles, ring, to);
+        found = found1;
+        found1 = found2;
+        found2 = copy();                         // over the tiles that were unpacked a stage ago
+        ring_slot = ring_slot + 1 == kRing ? 0 : ring_slot + 1;
+        wait_loads<Shape::kCopies>();            // this wave's copies of the stage after the next are there
         lds_barrier();
     }
+    wait_loads<0>();
 
     // ---- the rows' results: register 4 i + e of block o holds channel 32 o + 8 i + 4 half + e ----
     const bool whole = w.t1 - w.t0 <= plan.chunk;
