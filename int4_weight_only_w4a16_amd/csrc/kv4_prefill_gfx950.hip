@@ -11,9 +11,13 @@
 // eight bits, the six products of parts that matter at 24 bits (its rounding
 // is that of the fp32 sums).  So a weight takes one fma a group, and
 //   p_t = exp2(scale log2(e) x_t - ref),  out = sum_t p_t v_t / sum_t p_t
-// with v_t = m + s c rounded to the activation type when it is unpacked (the
-// value that kv4_read gives) and p_t rounded to it for the second product:
-// values cost all waves one unpacking and the weights nothing a group.
+// with v_t = m + s c unpacked into two parts of the activation type (high and
+// low: 2^-17 or better of v_t) and p_t rounded to it for the second product.
+// So values cost all waves one unpacking and the weights nothing a group, and
+// only the p_t are rounded: with values of one part the result is off by
+// sqrt(3) roundings of the output instead of sqrt(2) (measured 2.8e-3 instead
+// of 2.4e-3 in bfloat16; the plain form's one rounding is 1.7e-3).  The
+// matrix cores have the time for the low parts.
 //
 // The transposed products K Q^T and V^T P^T put a row of the softmax in one
 // column: a lane's weights are the second product's operand as they stand,
@@ -45,7 +49,7 @@ struct ManyShape {
     static constexpr int kTerms = (kPairs * NG + 3 + 15) / 16;  // 16-deep products of the offset term
     // one stage: the tiles' key operands, value operands, offset operands, steps, NaN masks
     static constexpr int kKeys = 64 * D;                        // bytes of one tile's
-    static constexpr int kValues = 64 * D;
+    static constexpr int kValues = 128 * D;                     // high parts, then low parts
     static constexpr int kOffsets = 1024 * kTerms;
     static constexpr int kSteps = 128 * NG;
     static constexpr int kAtValues = kTiles * kKeys;
@@ -238,15 +242,19 @@ __global__ void __launch_bounds__(kManyThreads<D>)
             for (int k = g * kWords / kValGroups; k < (g + 1) * kWords / kValGroups; ++k) {
                 uint32_t even = vcodes[k] & 0x0F0F0F0Fu, odd = (vcodes[k] >> 4) & 0x0F0F0F0Fu;
                 asm("" : "+v"(even), "+v"(odd));
-                u4 v;
+                u4 high, low;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {               // nibbles e and e + 4
                     const uint32_t src = e & 1 ? odd : even;
-                    v[e] = pack2<BF>(__builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]),
-                                     __builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]));
+                    const float v0 = __builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]);
+                    const float v1 = __builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]);
+                    high[e] = pack2<BF>(v0, v1);
+                    low[e] = pack2<BF>(v0 - lo_f32<BF>(high[e]), v1 - hi_f32<BF>(high[e]));
                 }
                 const int d = 64 * chunk64 + 16 * (word0 + k) + r16;
-                lds_put(values + 1024 * (2 * (d / 32) + (b4 >> 1)) + 16 * (32 * (b4 & 1) + d % 32), v);
+                lds_u8 *const to_value = values + 1024 * (2 * (d / 32) + (b4 >> 1)) + 16 * (32 * (b4 & 1) + d % 32);
+                lds_put(to_value, high);
+                lds_put(to_value + 64 * D, low);
             }
         }
     };
@@ -378,7 +386,9 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         for (int o = 0; o < kOut; ++o)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                out[o] = mfma32x32x16_t<BF>(lds_get<u4>(values + 1024 * (2 * o + s)), pw[s], out[o]);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    out[o] = mfma32x32x16_t<BF>(lds_get<u4>(values + 64 * D * part + 1024 * (2 * o + s)), pw[s], out[o]);
     };
 
     // ---- main loop: unpack the next stage while this one is worked on, the one after it on its way ----

@@ -46,6 +46,14 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     }
 }
 
+// 1 / sqrt(v) rounded to nearest: one Newton step in fp64 on the hardware's approximation, which
+// is off by an ulp for a ninth of all arguments.  A head's channels all share this factor, and a
+// stored code should not turn on its last bit.
+__device__ __forceinline__ float inverse_root(float v) {
+    const double r = (double)__builtin_amdgcn_rsqf(v);
+    return (float)(r * (1.5 - 0.5 * (double)v * r * r));
+}
+
 // Norm and rotation of channels 8 i .. 8 i + 7 of a head whose D/8 lanes call
 // this together.  pos: the token's position; one outside the tables gives NaN.
 // No contraction: the products and sums round as the formulas above say.
@@ -59,7 +67,7 @@ __device__ __forceinline__ void norm_rope(float (&x)[8], int i, const float *wei
                     (((x[4] * x[4] + x[5] * x[5]) + x[6] * x[6]) + x[7] * x[7]);
 #pragma unroll
         for (int d = 1; d < D / 8; d *= 2) sum += __shfl_xor(sum, d);
-        const float rstd = rsqrtf(sum * (1.0f / D) + r.eps);
+        const float rstd = inverse_root(sum * (1.0f / D) + r.eps);
         float w[8];
         load8(weight + 8 * i, w);
 #pragma unroll
