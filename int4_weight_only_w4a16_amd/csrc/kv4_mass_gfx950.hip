@@ -12,7 +12,7 @@
 //
 // Many rows (a prompt): a wave keeps the keys of 32 slots in registers, as
 // two 16-bit parts each (k = high + low to 2^-17 or better), and the rows
-// pass by in LDS, 64 at a time, shared by eight waves.  Two products a
+// pass by in LDS, 64 at a time, shared by the waves of eight such tiles.  Two products a
 // channel block instead of one, but a weight then takes one fma, one
 // exponential and one add.  Bound by the matrix cores.
 
@@ -199,22 +199,31 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(Kv4AttnArgs a, int c
 
 // ---- many rows ----
 
-constexpr int kManyWaves = 8, kManySlots = 32 * kManyWaves, kStageRows = 64;
+// A workgroup's eight tiles of slots, and how many waves share one: with two, each takes the
+// other 32 rows of a stage, so that four waves on a SIMD cover each other's exponentials and
+// products (256 channels: the keys' registers allow one).
+constexpr int kManyTiles = 8, kManySlots = 32 * kManyTiles, kStageRows = 64;
+template <int D>
+constexpr int kSplit = D <= 128 ? 2 : 1;
+template <int D>
+constexpr int kManyThreads = 64 * kManyTiles * kSplit<D>;
 
 template <bool BF, int D, int NG>
-__global__ void __launch_bounds__(64 * kManyWaves) many_rows_kernel(Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kManyThreads<D>) many_rows_kernel(Kv4AttnArgs a) {
     using T = Tile<D, NG>;
+    constexpr int kManyWaves = kManyThreads<D> / 64;
     constexpr int kDeep = D / 16;                                // 16-channel products
     constexpr int kStageBytes = kStageRows * D * 2, kRing = 3;
-    constexpr int kCopies = kStageBytes / 1024 / kManyWaves;     // KiB of a stage that a wave copies
-    __shared__ __align__(16) uint8_t lds_raw[kRing * kStageBytes];
+    constexpr int kCopies = kStageBytes / 1024 < kManyWaves ? 1 : kStageBytes / 1024 / kManyWaves;   // KiB that a wave copies
+    constexpr int kHandover = kSplit<D> > 1 ? 4096 * kManyTiles : 0;
+    __shared__ __align__(16) uint8_t lds_raw[kRing * kStageBytes > kHandover ? kRing * kStageBytes : kHandover];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int kvh = a.c.kv_heads, G = a.q_heads / kvh;
     Work w;
     if (!work_of(a, blockIdx.z, blockIdx.y, 0, 0x3fffffff, &w)) return;
-    const int tile0 = w.t0 + (int)blockIdx.x * kManyWaves, tile = tile0 + wave;
+    const int tile0 = w.t0 + (int)blockIdx.x * kManyTiles, tile = tile0 + wave % kManyTiles;
     if (tile0 >= w.t1) return;
     const uint8_t *const p =
         tile < w.t1 ? tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, w.b, w.h, tile) : nullptr;
@@ -228,26 +237,55 @@ __global__ void __launch_bounds__(64 * kManyWaves) many_rows_kernel(Kv4AttnArgs 
     const int row_end = min((int64_t)i1 * G, (int64_t)w.rows);
     if (row_begin >= row_end) return;
 
+    // Where a row's q and lse lie, for one row a lane that advances by a stage at a time: no
+    // division in the loop.  A row past the last stands for the last.
+    const int step_token = kStageRows / G, step_head = kStageRows % G;
+    const uint16_t *const q0 = static_cast<const uint16_t *>(a.q) + (int64_t)w.first * a.q_stride + (int64_t)w.h * G * D;
+    const float *const lse0 = a.lse + (int64_t)w.first * a.q_heads + w.h * G;
+    struct Row {
+        int row, token, head;
+    };
+    auto row_at = [&](int row) { return Row{row, row / G, row % G}; };
+    auto advance = [&](Row &x) {
+        x.row += kStageRows;
+        x.token += step_token;
+        x.head += step_head;
+        if (x.head >= G) {
+            x.head -= G;
+            ++x.token;
+        }
+    };
+    const int last_token = w.n - 1, last_head = G - 1;
+    auto q_of = [&](const Row &x) {
+        const bool in = x.row < w.rows;
+        return q0 + (int64_t)(in ? x.token : last_token) * a.q_stride + (in ? x.head : last_head) * D;
+    };
+    auto lse_of = [&](const Row &x) {
+        const bool in = x.row < w.rows;
+        return lse0[(int64_t)(in ? x.token : last_token) * a.q_heads + (in ? x.head : last_head)];
+    };
+
     // a stage: 16-channel blocks of 32 rows, a KiB each, as matrix operands.  Copy i of this wave
-    // is block (wave + 8 i) % kDeep of the 32 rows (wave + 8 i) / kDeep.
-    auto copy = [&](int row0, int slot) {
+    // is block u % kDeep of the 32 rows u / kDeep, u = wave + waves * i.
+    Row copy_row[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+        copy_row[i] = row_at(row_begin + 32 * ((wave + kManyWaves * i) % (kStageBytes / 1024) / kDeep) + col);
+    auto copy = [&](int slot) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int unit = wave + kManyWaves * i, j = unit % kDeep;
-            const int row = min(row0 + 32 * (unit / kDeep) + col, w.rows - 1);
-            const int token = row / G;
-            const uint16_t *src = static_cast<const uint16_t *>(a.q) + (int64_t)(w.first + token) * a.q_stride +
-                                  (int64_t)(w.h * G + row - token * G) * D + 16 * j + 8 * half;
+            const int unit = (wave + kManyWaves * i) % (kStageBytes / 1024), j = unit % kDeep;
+            const uint16_t *src = q_of(copy_row[i]) + 16 * j + 8 * half;
             __builtin_amdgcn_global_load_lds(
                 reinterpret_cast<const __attribute__((address_space(1))) void *>(reinterpret_cast<uintptr_t>(src)),
                 (lds_void *)(lds + slot * kStageBytes + 1024 * unit), 16, 0, 0);
+            advance(copy_row[i]);
         }
     };
-    int copied = row_begin, slot_next = 0;
+    int slot_next = 0;
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) {
-        copy(copied, slot_next);                 // (past the last row: that row again)
-        copied += kStageRows;
+        copy(slot_next);
         slot_next = slot_next + 1 == kRing ? 0 : slot_next + 1;
     }
 
@@ -274,28 +312,39 @@ __global__ void __launch_bounds__(64 * kManyWaves) many_rows_kernel(Kv4AttnArgs 
     const f16v zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     f16v mass = zero;
     // lse of this lane's columns, loaded a stage ahead
-    float lse[2], lse_next[2];
-    auto load_lse = [&](int row0) {
+    constexpr int kLse = 2 / kSplit<D>;
+    float lse[kLse], lse_next[kLse];
+    Row lse_row[kLse];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int row = min(row0 + 32 * s + col, w.rows - 1), token = row / G;
-            lse_next[s] = a.lse[(int64_t)(w.first + token) * a.q_heads + w.h * G + row - token * G];
+    for (int step = 0; step < kLse; ++step)
+        lse_row[step] = row_at(row_begin + 32 * (kSplit<D> > 1 ? wave / kManyTiles : step) + col);
+    auto load_lse = [&]() {
+#pragma unroll
+        for (int step = 0; step < kLse; ++step) {
+            lse_next[step] = lse_of(lse_row[step]);
+            advance(lse_row[step]);
         }
     };
-    load_lse(row_begin);
+    load_lse();
+    // rows that see the whole tile: [all0, all1)
+    const int64_t first_all = a.causal ? max(0, 32 * tile + 31 - back) : 0;
+    const int64_t last_all = a.window > 0 ? min((int64_t)w.n, (int64_t)32 * tile + a.window - back) : w.n;
+    const bool any_all = 32 * tile + 32 <= w.len;
+    const int all0 = any_all ? (int)min(first_all * G, (int64_t)w.rows) : w.rows;
+    const int all1 = any_all ? (int)max(last_all * G, (int64_t)0) : 0;
     int at_slot = 0;
     for (int row0 = row_begin; row0 < row_end; row0 += kStageRows) {
-        lse[0] = lse_next[0];
-        lse[1] = lse_next[1];
-        load_lse(row0 + kStageRows);
-        copy(copied, slot_next);
-        copied += kStageRows;
+#pragma unroll
+        for (int step = 0; step < kLse; ++step) lse[step] = lse_next[step];
+        load_lse();
+        copy(slot_next);
         slot_next = slot_next + 1 == kRing ? 0 : slot_next + 1;
-        wait_loads<(kRing - 1) * kCopies + 2>();                 // this wave's share of the oldest stage is there
+        wait_loads<(kRing - 1) * kCopies + kLse>();              // this wave's share of the oldest stage is there
         lds_barrier();                                           // ... and the others'
         const lds_u8 *const at = lds + at_slot * kStageBytes + 16 * lane;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int step = 0; step < 2 / kSplit<D>; ++step) {
+            const int s = kSplit<D> > 1 ? wave / kManyTiles : step;
             const int ra = row0 + 32 * s, rb = ra + 31;          // the rows of this product
             f16v x = zero;
 #pragma unroll
@@ -304,11 +353,8 @@ __global__ void __launch_bounds__(64 * kManyWaves) many_rows_kernel(Kv4AttnArgs 
                 x = mfma32x32x16_t<BF>(high[j], q, x);
                 x = mfma32x32x16_t<BF>(low[j], q, x);
             }
-            const float shift = lse[s] == -__builtin_inff() ? lse[s] : -lse[s] * kLog2e;
-            // every row there and every slot seen by all of them?
-            const int ia = ra / G, ib = min(rb, w.rows - 1) / G;
-            const bool all = rb < w.rows && 32 * tile + 32 <= row_hi(ia, w.n, w.len, a.causal) &&
-                             32 * tile >= row_lo(ib, w.n, w.len, a.window);
+            const float shift = lse[step] == -__builtin_inff() ? lse[step] : -lse[step] * kLog2e;
+            const bool all = ra >= all0 && rb < all1;
             if (all) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mass[i] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c1, shift));
@@ -330,6 +376,23 @@ __global__ void __launch_bounds__(64 * kManyWaves) many_rows_kernel(Kv4AttnArgs 
         lds_barrier();                                           // the stage may be overwritten
     }
     wait_loads<0>();
+    // the tile's other wave hands its sums over in LDS, which the stages leave
+    if constexpr (kSplit<D> > 1) {
+        lds_barrier();
+        lds_u8 *const mine = lds + (wave % kManyTiles) * 4096 + 16 * lane;
+        if (wave >= kManyTiles)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds_put(mine + 1024 * i, f4{mass[4 * i], mass[4 * i + 1], mass[4 * i + 2], mass[4 * i + 3]});
+        lds_barrier();
+        if (wave >= kManyTiles) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f4 v = lds_get<f4>(mine + 1024 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mass[4 * i + e] += v[e];
+        }
+    }
     if (!p) return;
     // register e: slot 8 (e / 4) + 4 half + e % 4, summed over the 32 columns
 #pragma unroll
@@ -360,14 +423,15 @@ hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream) {
     if (a.window > 0) tiles = std::min<int64_t>(tiles, ((int64_t)a.window + a.max_q) / 32 + 2);
     const unsigned heads = (unsigned)a.c.kv_heads, batch = (unsigned)a.c.batch;
     if (rows > 64) {
-        const dim3 grid((unsigned)((tiles + kManyWaves - 1) / kManyWaves), heads, batch);
+        const dim3 grid((unsigned)((tiles + kManyTiles - 1) / kManyTiles), heads, batch);
         return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-            many_rows_kernel<bf(), d(), ng()><<<grid, 64 * kManyWaves, 0, stream>>>(a);
+            many_rows_kernel<bf(), d(), ng()><<<grid, kManyThreads<d()>, 0, stream>>>(a);
             return hipGetLastError();
         });
     }
-    // chunks as the attention's, within the page ids that a wave holds
-    const int64_t want = std::max<int64_t>(1, (batch <= 4 ? 768 : 2048) / ((int64_t)heads * batch));
+    // chunks as the attention's, within the page ids that a wave holds (8 sequences of 2000 to
+    // 16000 slots: 24.5 us with 512 workgroups, 18.3 with 1536, 22 with 2048)
+    const int64_t want = std::max<int64_t>(1, (batch <= 4 ? 768 : 1536) / ((int64_t)heads * batch));
     int64_t chunk = ((tiles + want - 1) / want + kWaves - 1) / kWaves * kWaves;
     if (a.c.tiles_per_page < (1 << 20)) chunk = std::min<int64_t>(chunk, 62 * (int64_t)a.c.tiles_per_page);
     chunk = std::max<int64_t>(kWaves, chunk / kWaves * kWaves);
