@@ -19,6 +19,10 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr float kNone = -3e38f;        // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
+// The activation type's largest number: m + 15 s may lie past it by the rounding of s, and an
+// infinite high part would make the low part, and the row, NaN.
+template <bool BF>
+constexpr float kLargest = BF ? 3.3895314e38f : 65504.0f;
 
 // What a workgroup works on: a tile of rows of one head of one sequence, and
 // a range of its slots.
@@ -60,7 +64,6 @@ template <typename T>
 __device__ __forceinline__ void lds_put(lds_u8 *p, T v) {
     *reinterpret_cast<__attribute__((address_space(3))) T *>(p) = v;
 }
-
 
 // One KiB from `base + at` to LDS without passing through registers, lane l's 16 bytes to 16 l; what
 // lies at or past base + bytes comes as zeros.

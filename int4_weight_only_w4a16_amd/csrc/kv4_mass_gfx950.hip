@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kManyThreads<D>) many_rows_kernel(Kv4AttnArgs 
         const float st = par_step<BF>(par), off = par_offset<BF>(par);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {            // channels 2 e and 2 e + 1: nibbles e and e + 4
-            const float k0 = __builtin_fmaf(st, (float)(word >> (4 * e) & 15u), off);
-            const float k1 = __builtin_fmaf(st, (float)(word >> (4 * e + 16) & 15u), off);
+            const float k0 = fminf(__builtin_fmaf(st, (float)(word >> (4 * e) & 15u), off), kLargest<BF>);
+            const float k1 = fminf(__builtin_fmaf(st, (float)(word >> (4 * e + 16) & 15u), off), kLargest<BF>);
             high[j][e] = pack2<BF>(k0, k1);
             low[j][e] = pack2<BF>(k0 - lo_f32<BF>(high[j][e]), k1 - hi_f32<BF>(high[j][e]));
         }

@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kManyThreads<D>)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {               // nibbles e and e + 4
                     const uint32_t src = e & 1 ? odd : even;
-                    const float v0 = __builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]);
-                    const float v1 = __builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]);
+                    const float v0 = fminf(__builtin_fmaf(st[e], ubyte_f32(src, e >> 1), off[e]), kLargest<BF>);
+                    const float v1 = fminf(__builtin_fmaf(st[4 + e], ubyte_f32(src, 2 + (e >> 1)), off[4 + e]), kLargest<BF>);
                     high[e] = pack2<BF>(v0, v1);
                     low[e] = pack2<BF>(v0 - lo_f32<BF>(high[e]), v1 - hi_f32<BF>(high[e]));
                 }

@@ -428,6 +428,29 @@ def test_attention_mass(dev, dtype, hq, hk, D, group, ns, lens, window, causal):
         assert torch.equal(got[b, :, lens[b]:], acc[b, :, lens[b]:].double())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("ns", [[4], [40]])
+def test_attention_and_mass_of_values_at_the_type_s_end(dev, dtype, ns):
+    """A group from the type's lowest to its highest number, whose m + 15 s lies past it: rows
+    that do not see it, or to which it adds nothing, are as they are without it."""
+    n, big = ns[0], torch.finfo(F16).max                 # (bfloat16: wide as well, without an overflow)
+    cache = ref.Cache([100], 2, 128, 64, 32, dtype, seed=9)
+    cache.fill()
+    k, v = randn(1, 2, 128), randn(2, 2, 128)
+    k[:, 0], k[:, 1], v[:, 70], v[:, 71] = -big, big, -big, big
+    cache.put(0, 99, k, v)                               # the last token's own slot
+    cache.put(0, 50, k, randn(3, 2, 128))
+    q = randn(5, n, 4, 128).to(dtype)
+    q[..., :64] = 0                                      # the keys' wide group
+    out, lse = attend(dev, cache, q, ns)
+    check_attention(out, lse, q, cache, ns)
+    acc = w4.kv4_attention_mass(q.to(dev), cache.pages(dev), ints(cache.table, dev), starts(ns, dev), ints([100], dev),
+                                lse, torch.zeros(1, 2, 100, device=dev), n, 100).cpu().double()
+    _, _, _, _, size, weights = ref.attention(cache, q, ns, 128 ** -0.5)
+    want = weights[0].sum((1, 2))
+    assert ((acc[0] - want).abs() <= (4 * E_LOGIT * max(1.0, float(size.max())) + 2.0 ** -22) * want).all()
+
+
 # ---- eviction ----
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
