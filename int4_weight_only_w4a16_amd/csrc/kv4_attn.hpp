@@ -2,6 +2,8 @@
 // slots, the plan of a launch, LDS access.
 #pragma once
 
+#include <algorithm>
+
 #include "kv4_device.hpp"
 
 namespace w4a16 {
@@ -52,6 +54,19 @@ __device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int 
     w->t0 = lo >> 5;
     w->t1 = hi > lo ? (hi + 31) >> 5 : w->t0;
     return true;
+}
+
+// Tiles of a workgroup that walks over one of about `want` equal parts of `tiles`, a whole number
+// for each wave.  The page ids of a part sit in the 64 lanes of a wave, 62 of them wherever it
+// begins; parts that this bounds stay equal (4000 slots of 64-slot pages, 192 rows, 32 sequences:
+// 287 us in two halves, 453 as 124 tiles and one).
+inline int chunk_of(const Kv4Cache &c, int tiles, int64_t want) {
+    if (c.tiles_per_page < (1 << 20)) {
+        const int64_t most = 62 * (int64_t)c.tiles_per_page / kWaves * kWaves;
+        want = std::max(want, (tiles + most - 1) / most);
+    }
+    const int64_t chunk = ((tiles + want - 1) / want + kWaves - 1) / kWaves * kWaves;
+    return (int)std::max<int64_t>(kWaves, chunk);
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;

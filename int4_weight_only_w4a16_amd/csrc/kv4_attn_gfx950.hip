@@ -38,28 +38,33 @@ __device__ __forceinline__ float mul_legacy(float a, float b) {
 // workgroup's start and end cost about as much as eight tiles (one sequence of 131071 slots, 8
 // heads: 36.6 us with 512 workgroups, 39 with 1024, 43.6 with 2048).  More sequences may differ
 // in length, and smaller chunks even that out (32 sequences of 1000 to 24000 slots: 136 us with
-// 512, 123 with 1024 to 3072).
-constexpr int kFewSlots = 512, kManySlots = 1536, kFewSequences = 4;
+// 512, 123 with 1024 to 3072; of 4000 slots each: 36 with 1024, 39 with 1536, 49 with 4096).
+constexpr int kFewSlots = 512, kManySlots = 1024, kFewSequences = 4;
 
-// Rows above which the kernel for many rows runs.
-constexpr int kFewRows = 64;
+// Rows above which the kernel for many rows runs, which keeps the matrix cores busier but works
+// on 256 rows however few there are.  Here and there, 8 heads of 128 channels, bfloat16, us:
+//   rows                            64           128          192          256          384
+//   1 sequence of 100000 slots   65 and 176   138 and 183  177 and 189  233 and 201  325 and 339
+//   8 of 4000                    43 and  76    63 and  88   83 and  97  105 and 107  152 and 167
+//   32 of 4000                  104 and 239   196 and 268  288 and 296  378 and 325  562 and 420
+constexpr int kFewRows = 192;
 int rows_of(const Kv4AttnArgs &a) { return a.q_heads / a.c.kv_heads * a.max_q; }
 
 Plan plan_of(const Kv4AttnArgs &a) {
     const int rows = rows_of(a);
     if (rows > kFewRows) return prefill_plan(a);
     Plan p;
-    p.rows = rows > 16 && a.c.head_dim <= 128 ? 32 : 16;   // (256 channels: 32 would not fit the registers)
+    // 32 rows a wave read the cache half as often as 16, at two waves a SIMD instead of three (32
+    // rows, 32 sequences of 16000 slots: 184 us, 221 with 16; 8 of 4000: 33 and 31; 256 channels:
+    // 32 would not fit the registers)
+    p.rows = rows > 16 && a.c.head_dim <= 128 ? 32 : 16;
     p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min(tiles, (a.window + a.max_q) / 32 + 2);
     const int64_t groups = (int64_t)a.c.batch * a.c.kv_heads * p.row_tiles;
     const int64_t want = std::max<int64_t>(
         1, (a.c.batch <= kFewSequences ? kFewSlots : kManySlots) / groups);
-    int64_t chunk = ((tiles + want - 1) / want + kWaves - 1) / kWaves * kWaves;
-    // page ids of a chunk sit in the 64 lanes of a wave
-    if (a.c.tiles_per_page < (1 << 20)) chunk = std::min<int64_t>(chunk, 62 * (int64_t)a.c.tiles_per_page);
-    p.chunk = (int)std::max<int64_t>(kWaves, chunk / kWaves * kWaves);
+    p.chunk = chunk_of(a.c, tiles, want);
     p.chunks = std::max(1, (tiles + p.chunk - 1) / p.chunk);
     return p;
 }
@@ -108,7 +113,7 @@ struct AttendShape {
 
 template <bool BF, int D, int NG, int NT>
 __global__ void __launch_bounds__(kThreads)
-    __attribute__((amdgpu_waves_per_eu(NT * D <= 128 ? 3 : 1, NT * D <= 128 ? 3 : 1))) attend_kernel(Kv4AttnArgs a, Plan plan) {
+    __attribute__((amdgpu_waves_per_eu(NT * D <= 128 ? 3 : 2, NT * D <= 128 ? 3 : 2))) attend_kernel(Kv4AttnArgs a, Plan plan) {
     using T = Tile<D, NG>;
     using Shape = AttendShape<D, NG, NT>;
     using Copy = TileCopy<D, NG>;

@@ -432,17 +432,15 @@ hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream) {
     // chunks as the attention's, within the page ids that a wave holds (8 sequences of 2000 to
     // 16000 slots: 24.5 us with 512 workgroups, 18.3 with 1536, 22 with 2048)
     const int64_t want = std::max<int64_t>(1, (batch <= 4 ? 768 : 1536) / ((int64_t)heads * batch));
-    int64_t chunk = ((tiles + want - 1) / want + kWaves - 1) / kWaves * kWaves;
-    if (a.c.tiles_per_page < (1 << 20)) chunk = std::min<int64_t>(chunk, 62 * (int64_t)a.c.tiles_per_page);
-    chunk = std::max<int64_t>(kWaves, chunk / kWaves * kWaves);
+    const int chunk = chunk_of(a.c, tiles, want);
     const dim3 grid((unsigned)((tiles + chunk - 1) / chunk), heads, batch);
     return by_shape(a.c, [&](auto bf, auto d, auto ng) {
         if (rows <= 16)
-            few_rows_kernel<bf(), d(), ng(), 1><<<grid, kThreads, 0, stream>>>(a, (int)chunk);
+            few_rows_kernel<bf(), d(), ng(), 1><<<grid, kThreads, 0, stream>>>(a, chunk);
         else if (rows <= 32)
-            few_rows_kernel<bf(), d(), ng(), 2><<<grid, kThreads, 0, stream>>>(a, (int)chunk);
+            few_rows_kernel<bf(), d(), ng(), 2><<<grid, kThreads, 0, stream>>>(a, chunk);
         else
-            few_rows_kernel<bf(), d(), ng(), 4><<<grid, kThreads, 0, stream>>>(a, (int)chunk);
+            few_rows_kernel<bf(), d(), ng(), 4><<<grid, kThreads, 0, stream>>>(a, chunk);
         return hipGetLastError();
     });
 }

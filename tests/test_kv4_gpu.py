@@ -320,6 +320,55 @@ def test_attention_what_a_row_does_not_see_does_not_reach_it(dev, dtype, ns):
     assert torch.isnan(out[-1]).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group", SHAPES)
+def test_attention_many_rows_every_shape(dev, dtype, D, group):
+    ns, lens = [70, 0, 3], [130, 20, 40]                  # 210 rows and 9
+    cache = ref.Cache(lens, 2, D, group, 64, dtype, seed=D)
+    cache.fill()
+    q = (1.5 * randn(7, sum(ns), 6, D)).to(dtype)
+    out, lse = attend(dev, cache, q, ns)
+    check_attention(out, lse, q, cache, ns)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("hq,hk,ns,lens,page,window,causal", [
+    (10, 2, [39, 20], [64, 20], 64, 0, True),
+    (8, 1, [25, 30], [3, 0], 32, 0, True),                 # more tokens than slots: empty rows
+    (8, 2, [50, 1], [150, 90], 32, 17, True),              # window inside a tile
+    (4, 1, [50], [100], 96, 1, True),                      # a window of one
+    (8, 2, [60, 49], [100, 5], 64, 0, False),              # every slot, from any token
+    (6, 1, [32], [4100], 32, 0, True),                     # 192 rows: the last that go a few at a time
+    (1, 1, [193], [193], 32, 0, True),
+])
+def test_attention_many_rows_masks_and_lengths(dev, dtype, hq, hk, ns, lens, page, window, causal):
+    cache = ref.Cache(lens, hk, 128, 64, page, dtype, seed=hq + page)
+    cache.fill()
+    q = (1.5 * randn(11, sum(ns), hq, 128)).to(dtype)
+    out, lse = attend(dev, cache, q, ns, window=window, causal=causal)
+    check_attention(out, lse, q, cache, ns, window=window, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_many_rows_what_a_row_does_not_see_does_not_reach_it(dev, dtype):
+    n, big = 110, torch.finfo(F16).max
+    cache = ref.Cache([200], 2, 128, 64, 32, dtype, seed=9)
+    cache.fill()
+    q = randn(5, n, 4, 128).to(dtype)
+    want, lse_want = attend(dev, cache, q, [n], window=60)
+    wide = randn(2, 2, 128)
+    wide[:, 70], wide[:, 71] = -big, big                   # (its m + 15 s lies past fp16's end)
+    cache.put(0, 199, randn(1, 2, 128), wide)
+    out, lse = attend(dev, cache, q, [n], window=60)
+    assert torch.equal(out[:-1], want[:-1])
+    check_attention(out, lse, q, cache, [n], window=60)
+    cache.poison(0, 199)                   # the last token's own slot
+    cache.poison(0, 200 - n + 1 - 60 - 1)  # just before the first token's window
+    out, lse = attend(dev, cache, q, [n], window=60)
+    assert torch.equal(out[:-1], want[:-1]) and torch.equal(lse[:-1], lse_want[:-1])
+    assert torch.isnan(out[-1]).all()
+
+
 def test_attention_scale_extremes_and_equal_logits(dev):
     cache = ref.Cache([77], 1, 128, 128, 32, F16, seed=2)
     cache.fill(scale_k=20.0)
