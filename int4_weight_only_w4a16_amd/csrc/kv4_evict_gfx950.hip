@@ -29,6 +29,9 @@ __device__ __forceinline__ uint32_t key_of(float f) {
     return (u & 0x80000000u) ? ((u & 0x7FFFFFFFu) > 0x7F800000u ? u | 0x80000000u : ~u) : u | 0x80000000u;
 }
 
+// kHeld: groups of 64 weights that a wave keeps in registers through the passes; 0: it reads them
+// from memory in each.
+template <int kHeld>
 __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
     const int h = blockIdx.x, b = blockIdx.y, kvh = a.c.kv_heads;
     const int64_t cap = (int64_t)a.c.table_stride * a.c.tiles_per_page * 32;
@@ -59,10 +62,34 @@ __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
     if (want == 0) return;
 
     constexpr int kBins = 2048, kWaves = kSelect / 64;
-    __shared__ unsigned hist[kBins];
+    __shared__ __align__(8) unsigned hist[kBins];
     __shared__ unsigned s_bin, s_left;
     __shared__ unsigned counts[kWaves], counts2[kWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // a part of the slots, whole groups of 64, for each wave
+    const int part = ((old + 63) / 64 + kWaves - 1) / kWaves * 64;
+    const int from = min(wave * part, old), to = min(from + part, old);
+    float held[kHeld > 0 ? kHeld : 8];
+    if constexpr (kHeld > 0)
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) held[j] = acc[min(from + 64 * j + lane, old - 1)];
+    // f(slot, weight) for the wave's groups of 64 in order, by all lanes (slots at or past `to` too)
+    auto each = [&](auto f) {
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                if (from + 64 * j >= to) break;
+                f(from + 64 * j + lane, held[j]);
+            }
+        } else {
+            for (int i0 = from; i0 < to; i0 += 8 * 64) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) held[j] = acc[min(i0 + 64 * j + lane, to - 1)];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f(i0 + 64 * j + lane, held[j]);
+            }
+        }
+    };
     uint32_t prefix = 0;                         // the threshold's known high bits
     unsigned left = want;                        // how many to take among those with that prefix
     for (int pass = 0; pass < 3; ++pass) {
@@ -70,21 +97,16 @@ __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
         const uint32_t digit = pass < 2 ? 2047u : 1023u;
         for (int i = threadIdx.x; i < kBins; i += kSelect) hist[i] = 0;
         __syncthreads();
-        for (int i0 = threadIdx.x; i0 < old; i0 += 8 * kSelect) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + j * kSelect, old - 1)];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t k = key_of(f[j]);
-                const uint32_t high = pass == 0 ? 0u : pass == 1 ? k >> 21 : k >> 10;
-                if (i0 + j * kSelect < old && high == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
-            }
-        }
+        each([&](int i, float f) {
+            const uint32_t k = key_of(f);
+            const uint32_t high = pass == 0 ? 0u : pass == 1 ? k >> 21 : k >> 10;
+            if (i < to && high == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+        });
         __syncthreads();
         // the bin, counted from the top, in which `left` is reached: thread t has bins 2047 - 2t
         // and 2046 - 2t, a scan over the workgroup the counts above them
-        const unsigned h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
+        const u2 pair = *reinterpret_cast<const u2 *>(&hist[kBins - 2 - 2 * threadIdx.x]);
+        const unsigned h0 = pair[1], h1 = pair[0];
         unsigned run = h0 + h1;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -94,7 +116,8 @@ __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
         if (lane == 63) counts[wave] = run;
         __syncthreads();
         unsigned above = run - h0 - h1;
-        for (int j = 0; j < wave; ++j) above += counts[j];
+#pragma unroll
+        for (int j = 0; j < kWaves; ++j) above += j < wave ? counts[j] : 0u;
         if (above < left && above + h0 >= left) {
             s_bin = kBins - 1 - 2 * threadIdx.x;
             s_left = left - above;
@@ -104,57 +127,40 @@ __global__ void __launch_bounds__(kSelect) select_kernel(Kv4EvictArgs a) {
         }
         __syncthreads();
         prefix = prefix << (pass < 2 ? 11 : 10) | s_bin;
-        left = s_left;
-        __syncthreads();
+        left = s_left;                           // (written again only after two more barriers)
     }
-    // slots above the threshold, and the first `left` equal to it: a part of the slots, whole
-    // groups of 64, for each wave
-    const int part = ((old + 63) / 64 + kWaves - 1) / kWaves * 64;
-    const int from = min(wave * part, old), to = min(from + part, old);
+    // slots above the threshold, and the first `left` equal to it
     const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
     unsigned na = 0, ne = 0;
-    for (int i0 = from; i0 < to; i0 += 8 * 64) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + 64 * j + lane, to - 1)];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool in = i0 + 64 * j + lane < to;
-            const uint32_t k = key_of(f[j]);
-            na += __popcll(__builtin_amdgcn_ballot_w64(in && k > prefix));
-            ne += __popcll(__builtin_amdgcn_ballot_w64(in && k == prefix));
-        }
-    }
+    each([&](int i, float f) {
+        const uint32_t k = key_of(f);
+        na += __popcll(__builtin_amdgcn_ballot_w64(i < to && k > prefix));
+        ne += __popcll(__builtin_amdgcn_ballot_w64(i < to && k == prefix));
+    });
     if (lane == 0) {
         counts[wave] = na;
         counts2[wave] = ne;
     }
     __syncthreads();
     na = ne = 0;
-    for (int j = 0; j < wave; ++j) {
-        na += counts[j];
-        ne += counts2[j];
+#pragma unroll
+    for (int j = 0; j < kWaves; ++j) {
+        na += j < wave ? counts[j] : 0u;
+        ne += j < wave ? counts2[j] : 0u;
     }
-    for (int i0 = from; i0 < to; i0 += 8 * 64) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = acc[min(i0 + 64 * j + lane, to - 1)];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + 64 * j + lane;
-            const uint32_t k = key_of(f[j]);
-            const bool above = i < to && k > prefix, equal = i < to && k == prefix;
-            const uint64_t ma = __builtin_amdgcn_ballot_w64(above), me = __builtin_amdgcn_ballot_w64(equal);
-            const unsigned a0 = na + __popcll(ma & below), e0 = ne + __popcll(me & below);
-            if (above || (equal && e0 < left)) {
-                const unsigned at = a0 + min(e0, left);
-                kept[at] = i;
-                out[at] = f[j];
-            }
-            na += __popcll(ma);
-            ne += __popcll(me);
+    each([&](int i, float f) {
+        const uint32_t k = key_of(f);
+        const bool above = i < to && k > prefix, equal = i < to && k == prefix;
+        const uint64_t ma = __builtin_amdgcn_ballot_w64(above), me = __builtin_amdgcn_ballot_w64(equal);
+        const unsigned a0 = na + __popcll(ma & below), e0 = ne + __popcll(me & below);
+        if (above || (equal && e0 < left)) {
+            const unsigned at = a0 + min(e0, left);
+            kept[at] = i;
+            out[at] = f;
         }
-    }
+        na += __popcll(ma);
+        ne += __popcll(me);
+    });
 }
 
 template <int D, int NG>
@@ -240,7 +246,14 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(Kv4EvictArgs a) {
 }  // namespace
 
 hipError_t launch_kv4_evict(const Kv4EvictArgs &a, hipStream_t stream) {
-    select_kernel<<<dim3((unsigned)a.c.kv_heads, (unsigned)a.c.batch), kSelect, 0, stream>>>(a);
+    // weights in registers where those of the longest sequence fit (one sequence of 8192 slots, 8
+    // heads: 12.7 us, 14.2 from memory; four times as many spill: 85 us instead of 36)
+    const int64_t most = (int64_t)a.max_kv - a.recent;
+    const dim3 heads((unsigned)a.c.kv_heads, (unsigned)a.c.batch);
+    if (most <= 8 * kSelect)
+        select_kernel<8><<<heads, kSelect, 0, stream>>>(a);
+    else
+        select_kernel<0><<<heads, kSelect, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((a.budget + 31) / 32), (unsigned)a.c.kv_heads, (unsigned)a.c.batch);

@@ -553,6 +553,26 @@ def test_evict(dev, dtype, D, group, lens, budget, recent):
     np.testing.assert_array_equal(after.words[~touched], cache.words[~touched])
 
 
+@pytest.mark.parametrize("lens,budget,recent", [([8200, 5000], 2048, 9), ([8193, 1], 100, 0), ([32768, 9001], 4000, 100),
+                                                ([33100, 32900], 1000, 50)])
+def test_evict_selects_of_long_sequences(dev, lens, budget, recent):
+    """Different weights, with runs of equal ones: what is kept and its weights."""
+    page, per = 128, -(-budget // 128)
+    rng = np.random.default_rng(budget)
+    acc = rng.random((len(lens), 1, max(lens) + 1)).astype(np.float32)
+    acc[:, :, 1000:1400] = acc[:, :, 2000:2400] = np.float32(0.9)
+    pages = w4.kv4_new_pages(len(lens) * per, 1, 64, 64, page, device=dev)
+    table = torch.full((len(lens), -(-max(lens) // page)), -1, dtype=torch.int32, device=dev)
+    dst = torch.arange(len(lens) * per, dtype=torch.int32, device=dev).view(len(lens), per)
+    kept, new, out = w4.kv4_evict(pages, table, ints(lens, dev), torch.from_numpy(acc).to(dev), budget, recent, dst, 64,
+                                  max(lens))
+    assert new.cpu().tolist() == [min(n, budget) for n in lens]
+    for b, n in enumerate(lens):
+        want = ref.evict_slots(acc[b, 0].tolist(), n, budget, recent)
+        assert kept[b, 0].cpu().tolist() == want + [-1] * (budget - len(want))
+        np.testing.assert_array_equal(out[b, 0].cpu().numpy()[:len(want)], acc[b, 0][want])
+
+
 def test_evicted_cache_attends_like_the_kept_slots(dev):
     """Attention and further appends go on from an evicted cache."""
     D, group, page, lens, budget = 128, 64, 32, [150], 70
