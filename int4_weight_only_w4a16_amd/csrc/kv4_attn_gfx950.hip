@@ -14,6 +14,11 @@
 // stored there: its product with a step is the one in which 0 x NaN is 0, and
 // a NaN offset is made finite (a group with a NaN has it in both, so that a
 // slot with weight still gives NaN).
+// Bound by memory while the rows are few, then by the vector ALUs (unpacking and weights): one
+// token, 40 heads on 8, 131071 slots 30 us (4.7 TB/s of 5.2) and 4.4 for the join of chunks; 32
+// sequences of 1000 to 24000 slots 115 us (4.4 TB/s) and 5.6; 64 rows instead of 4 over 32
+// sequences of 4000 slots 104 us instead of 36.  A wave's tile comes while the one before is
+// worked on; a third under way is slower (LDS for fewer waves: 9.1 -> 9.7 us at 2000 slots).
 // ref is a running reference per row, moved only when a tile's maximum
 // passes it by more than kSlack: p_t stays below 2^kSlack, and P_t below
 // 2^kSlack * (2 * 65504 / 15), which fp16 holds.

@@ -13,7 +13,10 @@
 // exponents alone would send a wave's adds to a handful of counters.  Then each
 // wave counts its part of the slots, and after one exchange of counts writes
 // them in order.  Bound by latency: five passes over weights that stay in L2.
-// copy_kernel: a workgroup per tile of the destination.
+// One sequence of 8192 slots, 8 heads: 12.7 us; 16 of 3000 to 33001: 36 us.
+// copy_kernel: a workgroup per tile of the destination, all of its loads before the
+// first store.  Bound by the source's cache lines, of which a kept slot's value codes touch
+// every one of its tile: 4096 slots of each of those 16 sequences 90 us, 2048 of the one 4.4.
 
 #include "kv4_device.hpp"
 

@@ -15,6 +15,10 @@
 // pass by in LDS, 64 at a time, shared by the waves of eight such tiles.  Two products a
 // channel block instead of one, but a weight then takes one fma, one
 // exponential and one add.  Bound by the matrix cores.
+//
+// Measured: 8 sequences of 2000 to 16000 slots, one token, 40 heads on 8: 17 us (2.7 TB/s of the
+// keys' half; the rest is the unpacking).  2048 tokens over 8191 slots, 32 heads on 8: 236 us, 490
+// TFLOP/s of the formula's product and twice that with the low parts.
 
 #include <algorithm>
 
@@ -422,6 +426,8 @@ hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream) {
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min<int64_t>(tiles, ((int64_t)a.window + a.max_q) / 32 + 2);
     const unsigned heads = (unsigned)a.c.kv_heads, batch = (unsigned)a.c.batch;
+    // up to 64 rows fit the registers of the kernel for few (32 sequences of 4000 slots, 8 heads: 64
+    // rows 57 us there and 174 here, of one sequence of 16000 slots 12 and 24)
     if (rows > 64) {
         const dim3 grid((unsigned)((tiles + kManyTiles - 1) / kManyTiles), heads, batch);
         return by_shape(a.c, [&](auto bf, auto d, auto ng) {

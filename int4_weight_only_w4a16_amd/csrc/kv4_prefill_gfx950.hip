@@ -19,6 +19,12 @@
 // of 2.4e-3 in bfloat16; the plain form's one rounding is 1.7e-3).  The
 // matrix cores have the time for the low parts.
 //
+// Bound by the matrix cores and the vector ALUs, which one wave does not keep busy together: two
+// prompts of 1500 and 2500 tokens over 12000 and 6000 slots, 40 heads on 8 (589 GFLOP of the
+// formula's products, 920 with the low parts and the offset term) 1008 us, 584 TFLOP/s of the
+// former.  A large product alone reaches 1280.  Fetching and unpacking, shared by the 8 waves, is
+// about a third of it.
+//
 // The transposed products K Q^T and V^T P^T put a row of the softmax in one
 // column: a lane's weights are the second product's operand as they stand,
 // if the 32 slots of a tile are the first operand's rows in the order
@@ -519,9 +525,25 @@ Plan prefill_plan(const Kv4AttnArgs &a) {
     p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min(tiles, (a.window + std::min(a.max_q, p.rows)) / 32 + 2);
-    // split the slots where there are too few tiles of rows for the chip's 256 CUs
+    // Split the slots where the tiles of rows alone leave some of the chip's 256 CUs without work (a
+    // workgroup fills one): the number of parts with the least time, in us, of a model fitted to
+    // 256 to 3200 rows over 2000 to 20000 slots.  A tile of slots is 1.5, a workgroup's start and
+    // end 10, a part's partial results and their join 0.15.  (4 sequences of 2000 slots, 1600 rows:
+    // 110 in one part, 203 in two; one of 20000: 964 in one, 281 in 4, 275 in 9, 300 in 18; 4800
+    // rows of it: 967 in one, 674 in three.)
     const int64_t groups = (int64_t)a.c.batch * a.c.kv_heads * p.row_tiles;
-    const int64_t want = std::max<int64_t>(1, 512 / groups);
+    int64_t want = 1;
+    if (groups < 512) {
+        double least = 0;
+        for (int64_t c = 1; c <= std::min<int64_t>(64, std::max(1, (tiles + 15) / 16)); ++c) {
+            const int64_t rounds = (groups * c + 255) / 256, part = (tiles + c - 1) / c;
+            const double time = (double)rounds * (1.5 * (double)part + 10) + (c > 1 ? 5 + 0.15 * (double)(groups * c) : 0);
+            if (c == 1 || time < least) {
+                least = time;
+                want = c;
+            }
+        }
+    }
     p.chunk = std::max<int>(16, (int)((tiles + want - 1) / want + 1) / 2 * 2);
     p.chunks = std::max(1, (tiles + p.chunk - 1) / p.chunk);
     return p;
