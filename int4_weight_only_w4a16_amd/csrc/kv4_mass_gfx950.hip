@@ -12,7 +12,7 @@
 //
 // Many rows (a prompt): a wave keeps the keys of 32 slots in registers, as
 // two 16-bit parts each (k = high + low to 2^-17 or better), and the rows
-// pass by in LDS, 64 at a time, shared by the waves of eight such tiles.  Two products a
+// pass by in LDS, 64 at a time, shared by the waves of up to eight such tiles.  Two products a
 // channel block instead of one, but a weight then takes one fma, one
 // exponential and one add.  Bound by the matrix cores.
 //
@@ -203,19 +203,21 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(Kv4AttnArgs a, int c
 
 // ---- many rows ----
 
-// A workgroup's eight tiles of slots, and how many waves share one: with two, each takes the
-// other 32 rows of a stage, so that four waves on a SIMD cover each other's exponentials and
-// products (256 channels: the keys' registers allow one).
-constexpr int kManyTiles = 8, kManySlots = 32 * kManyTiles, kStageRows = 64;
+// How many waves share a tile of slots: with two, each takes the other 32 rows of a stage, so that
+// the waves on a SIMD cover each other's exponentials and products (256 channels: the keys'
+// registers allow one).
+constexpr int kStageRows = 64;
 template <int D>
 constexpr int kSplit = D <= 128 ? 2 : 1;
-template <int D>
-constexpr int kManyThreads = 64 * kManyTiles * kSplit<D>;
+template <int D, int TILES>
+constexpr int kManyThreads = 64 * TILES * kSplit<D>;
 
-template <bool BF, int D, int NG>
-__global__ void __launch_bounds__(kManyThreads<D>) many_rows_kernel(Kv4AttnArgs a) {
+// TILES: tiles of slots of a workgroup.
+template <bool BF, int D, int NG, int TILES>
+__global__ void __launch_bounds__((kManyThreads<D, TILES>)) many_rows_kernel(Kv4AttnArgs a) {
     using T = Tile<D, NG>;
-    constexpr int kManyWaves = kManyThreads<D> / 64;
+    constexpr int kManyTiles = TILES, kManySlots = 32 * TILES;
+    constexpr int kManyWaves = kManyThreads<D, TILES> / 64;
     constexpr int kDeep = D / 16;                                // 16-channel products
     constexpr int kStageBytes = kStageRows * D * 2, kRing = 3;
     constexpr int kCopies = kStageBytes / 1024 < kManyWaves ? 1 : kStageBytes / 1024 / kManyWaves;   // KiB that a wave copies
@@ -295,20 +297,27 @@ __global__ void __launch_bounds__(kManyThreads<D>) many_rows_kernel(Kv4AttnArgs 
 
     // this wave's 32 keys in two parts: row `col` of the operands, channels 16 j + 8 half + 0..7
     u4 high[kDeep], low[kDeep];
-#pragma unroll
-    for (int j = 0; j < kDeep; ++j) {
-        uint32_t word = 0, par = 0;
+    {
+        uint32_t words[kDeep] = {}, pars[NG] = {};
         if (p) {
-            word = reinterpret_cast<const uint32_t *>(p)[key_word<D>(col, 2 * j + half)];
-            par = reinterpret_cast<const uint32_t *>(p + 2 * T::kCodes)[32 * (16 * j / T::kGroup) + col];
-        }
-        const float st = par_step<BF>(par), off = par_offset<BF>(par);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {            // channels 2 e and 2 e + 1: nibbles e and e + 4
-            const float k0 = fminf(__builtin_fmaf(st, (float)(word >> (4 * e) & 15u), off), kLargest<BF>);
-            const float k1 = fminf(__builtin_fmaf(st, (float)(word >> (4 * e + 16) & 15u), off), kLargest<BF>);
-            high[j][e] = pack2<BF>(k0, k1);
-            low[j][e] = pack2<BF>(k0 - lo_f32<BF>(high[j][e]), k1 - hi_f32<BF>(high[j][e]));
+            for (int j = 0; j < kDeep; ++j) words[j] = reinterpret_cast<const uint32_t *>(p)[key_word<D>(col, 2 * j + half)];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) pars[g] = reinterpret_cast<const uint32_t *>(p + 2 * T::kCodes)[32 * g + col];
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const float st = par_step<BF>(pars[16 * j / T::kGroup]), off = par_offset<BF>(pars[16 * j / T::kGroup]);
+            uint32_t even = words[j] & 0x0F0F0F0Fu, odd = (words[j] >> 4) & 0x0F0F0F0Fu;
+            asm("" : "+v"(even), "+v"(odd));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {        // channels 2 e and 2 e + 1: nibbles e and e + 4
+                const uint32_t src = e & 1 ? odd : even;
+                const float k0 = fminf(__builtin_fmaf(st, ubyte_f32(src, e >> 1), off), kLargest<BF>);
+                const float k1 = fminf(__builtin_fmaf(st, ubyte_f32(src, 2 + (e >> 1)), off), kLargest<BF>);
+                high[j][e] = pack2<BF>(k0, k1);
+                low[j][e] = pack2<BF>(k0 - lo_f32<BF>(high[j][e]), k1 - hi_f32<BF>(high[j][e]));
+            }
         }
     }
 
@@ -429,11 +438,20 @@ hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream) {
     // up to 64 rows fit the registers of the kernel for few (32 sequences of 4000 slots, 8 heads: 64
     // rows 57 us there and 174 here, of one sequence of 16000 slots 12 and 24)
     if (rows > 64) {
-        const dim3 grid((unsigned)((tiles + kManyTiles - 1) / kManyTiles), heads, batch);
-        return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-            many_rows_kernel<bf(), d(), ng()><<<grid, kManyThreads<d()>, 0, stream>>>(a);
-            return hipGetLastError();
-        });
+        // Eight tiles share a stage of rows, or fewer where half of the 256 CUs would be without
+        // work (1600 rows, 8 heads of 128 channels, us with 8, 4 and 2: 8000 slots 55, 66 and 86;
+        // 4000 slots 55, 38 and 39; 2000 slots 52, 35 and 31.  256 channels, 2000 slots: 83, 65, 78)
+        auto go = [&](auto n) {
+            const dim3 grid((unsigned)((tiles + n() - 1) / n()), heads, batch);
+            return by_shape(a.c, [&](auto bf, auto d, auto ng) {
+                many_rows_kernel<bf(), d(), ng(), n()><<<grid, kManyThreads<d(), n()>, 0, stream>>>(a);
+                return hipGetLastError();
+            });
+        };
+        const int64_t all = (int64_t)tiles * heads * batch;
+        return all > 8 * 128                              ? go(std::integral_constant<int, 8>{})
+               : all > 4 * 128 || a.c.head_dim > 128 ? go(std::integral_constant<int, 4>{})
+                                                          : go(std::integral_constant<int, 2>{});
     }
     // chunks as the attention's, within the page ids that a wave holds (8 sequences of 2000 to
     // 16000 slots: 24.5 us with 512 workgroups, 18.3 with 1536, 22 with 2048)

@@ -457,6 +457,10 @@ def test_attention_on_another_stream_and_replayed_from_a_graph(dev):
     (3, 1, 256, 32, [4, 5], [2, 70], 0, True),          # empty rows
     (4, 2, 128, 32, [33], [65], 0, False),
     (2, 2, 64, 64, [130], [300], 50, True),
+    (8, 8, 64, 64, [66, 70], [1100, 1200], 0, True),    # more slots: four and eight tiles together
+    (4, 4, 128, 64, [70], [4500], 0, True),
+    (2, 2, 256, 128, [70], [2100], 900, True),
+    (16, 16, 64, 32, [66, 66], [1400, 1300], 0, True),
 ])
 def test_attention_mass(dev, dtype, hq, hk, D, group, ns, lens, window, causal):
     cache = ref.Cache(lens, hk, D, group, 32, dtype, seed=8)
