@@ -238,9 +238,10 @@ py::object kv4_attention(const Tensor &q, const Tensor &pages, const Tensor &blo
     float *lse_ptr = l ? static_cast<float *>(plain("lse", *l, at::kFloat, q.device(), {T, hq})) : nullptr;
     const size_t need = w4a16_kv4_attention_workspace_bytes(s.batch, hq, g.heads, D, max_q, max_kv, window);
     Tensor ws;
-    if (workspace)
+    if (workspace) {
         ws = *workspace;
-    else if (need)
+        plain("workspace", ws, ws.scalar_type(), pages.device());     // (any type: bytes are what counts)
+    } else if (need)
         ws = at::empty({(int64_t)need}, pages.options());
     check(w4a16_kv4_attention(q.data_ptr(), qs, pages.data_ptr(), s.table, s.cu, s.kv_len, o.data_ptr(),
                               heads_stride("out", o, &q), lse_ptr, T, hq, g.heads, D, g.group, g.page, g.pages,
