@@ -11,9 +11,9 @@
 // from one more matrix product with ones, of the same rounded P_t, so that
 // B + 8 comes off exactly and only P_t (c_t - 8) feels their rounding.
 // A slot that a row does not see has p_t = 0 and adds nothing, whatever is
-// stored there: its product with a step is the one in which 0 x NaN is 0, and
-// a NaN offset is made finite (a group with a NaN has it in both, so that a
-// slot with weight still gives NaN).
+// stored there: its product with a step is the one in which 0 x anything is 0,
+// and m + 8 s is held between the type's ends (a group with a NaN has it in
+// both parameters, so that a slot with weight still gives NaN).
 // Bound by memory while the rows are few, then by the vector ALUs (unpacking and weights): one
 // token, 40 heads on 8, 131071 slots 30 us (4.7 TB/s of 5.2) and 4.4 for the join of chunks; 32
 // sequences of 1000 to 24000 slots 115 us (4.4 TB/s) and 5.6; 64 rows instead of 4 over 32
@@ -38,6 +38,9 @@ __device__ __forceinline__ float mul_legacy(float a, float b) {
     asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
 }
+
+// v held to [-most, most]; a NaN becomes -most.
+__device__ __forceinline__ float finite(float v, float most) { return __builtin_amdgcn_fmed3f(v, -most, most); }
 
 // Chunks.  A few sequences: two workgroups for each CU, all of them at work at once, since a
 // workgroup's start and end cost about as much as eight tiles (one sequence of 131071 slots, 8
@@ -352,12 +355,11 @@ __global__ void __launch_bounds__(kThreads)
             // operand holding group g: the rounded p_t with the middles in two parts
             const lds_u8 *mine = at + 2 * T::kCodes + 128 * (NG + (r < NG ? r : NG - 1)) + 16 * b4;
             const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
-            constexpr float kFloor = BF ? -3e38f : -65504.0f;        // in place of a NaN
             u4 high, low;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float m0 = fmaxf(__builtin_fmaf(8.0f, par_step<BF>(p0[e]), par_offset<BF>(p0[e])), kFloor);
-                const float m1 = fmaxf(__builtin_fmaf(8.0f, par_step<BF>(p1[e]), par_offset<BF>(p1[e])), kFloor);
+                const float m0 = finite(__builtin_fmaf(8.0f, par_step<BF>(p0[e]), par_offset<BF>(p0[e])), kLargest<BF>);
+                const float m1 = finite(__builtin_fmaf(8.0f, par_step<BF>(p1[e]), par_offset<BF>(p1[e])), kLargest<BF>);
                 high[e] = pack2<BF>(m0, m1);
                 low[e] = pack2<BF>(m0 - lo_f32<BF>(high[e]), m1 - hi_f32<BF>(high[e]));
             }
@@ -386,9 +388,9 @@ __global__ void __launch_bounds__(kThreads)
             if constexpr (!kMidRows) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    // (a NaN of an unseen slot becomes finite here; of a seen one, P_t is NaN)
-                    const float mid = fmaxf(
-                        __builtin_fmaf(8.0f, st[e], par_offset<BF>(e < 4 ? p0[e & 3] : p1[e & 3])), -3e38f);
+                    // (of a seen slot's NaN, P_t is NaN)
+                    const float mid = finite(
+                        __builtin_fmaf(8.0f, st[e], par_offset<BF>(e < 4 ? p0[e & 3] : p1[e & 3])), kLargest<true>);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mids[t][0] = __builtin_fmaf(x[t][e], mid, mids[t][0]);
                 }
