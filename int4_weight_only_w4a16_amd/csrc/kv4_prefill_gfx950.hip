@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
             for (int e = 0; e < 8; ++e) {
                 // NaN becomes a number here; the masks below bring it back
                 st[e] = fmaxf(par_step<BF>(p[e >> 2][e & 3]), 0.f);
-                off[e] = fmaxf(par_offset<BF>(p[e >> 2][e & 3]), BF ? -3e38f : -65504.0f);
+                off[e] = fmaxf(par_offset<BF>(p[e >> 2][e & 3]), -kLargest<BF>);
             }
 #pragma unroll
             for (int k = g * kWords / kValGroups; k < (g + 1) * kWords / kValGroups; ++k) {

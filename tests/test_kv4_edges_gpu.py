@@ -111,3 +111,16 @@ def test_slots_that_no_row_sees_may_hold_anything(dev, dtype, D, group, hq, n, w
     for plain, other in zip(*got):
         assert torch.isfinite(plain).all()
         assert torch.equal(plain, other)
+
+
+@pytest.mark.parametrize("group", [64, 128])
+@pytest.mark.parametrize("G", [1, 200])
+def test_attention_of_constant_groups_at_bfloat16_s_end(dev, group, G):
+    """One slot whose groups are all -3.3e38 or all 3.3e38: its value comes out as it is."""
+    cache = ref.Cache([1], 1, 128, group, 32, BF16, seed=3)
+    v = torch.full((1, 128), -3.3e38)
+    v[:, 64:] *= -1 if group == 64 else 1
+    cache.put(0, 0, randn(1, 1, 128), v)
+    out = w4.kv4_attention(torch.ones(1, G, 128, dtype=BF16, device=dev), cache.pages(dev), ints(cache.table, dev),
+                           starts([1], dev), ints([1], dev), 1, 1)
+    assert torch.equal(out.cpu(), v.to(BF16).expand(1, G, 128))
