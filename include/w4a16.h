@@ -489,7 +489,9 @@ int w4a16_kv4_read(const void *pages, const int32_t *table, const int32_t *cu_se
  * value step are rounded to the activation type before the second product,
  * with the sum of the rounded ones taken along (u = 2^-11 for fp16, 2^-8 for
  * bfloat16: |out - exact| <= u |exact| + 1.1 u sum_t p_t (s_t |c_t - 8| +
- * |m_t + 8 s_t|) and a few 2^-24 of the sums' magnitudes, sum_t p_t = 1). */
+ * |m_t + 8 s_t|) and a few 2^-24 of the sums' magnitudes, sum_t p_t = 1; with
+ * fp16, which has no numbers below 2^-25, also up to 2^-29 max(1, s) (1 +
+ * |m_t + 8 s_t|) for each slot, s the largest step that the query sees). */
 int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
                         const int32_t *cu_seqlens, const int32_t *kv_len, void *out,
                         int64_t out_stride, float *lse, int64_t T, int64_t q_heads,

@@ -20,8 +20,14 @@
 // sequences of 4000 slots 104 us instead of 36.  A wave's tile comes while the one before is
 // worked on; a third under way is slower (LDS for fewer waves: 9.1 -> 9.7 us at 2000 slots).
 // ref is a running reference per row, moved only when a tile's maximum
-// passes it by more than kSlack: p_t stays below 2^kSlack, and P_t below
-// 2^kSlack * (2 * 65504 / 15), which fp16 holds.
+// passes it by more than kSlack, and lies `lift` below the maximum: p_t stays
+// below 2^(lift + kSlack).  fp16 has few numbers below 2^-14 and none below
+// 2^-25, so there the weights start high: lift is 13, which rounds a P_t by at
+// most 2^-38 of the largest weight, and less for rows that have met a step of
+// 2 or more, so that P_t stays below 2^16.  (With 0 always, small values behind
+// a dominant logit lost their weights: 5000 slots of 0.02, 12.5 below it, came
+// out 0.29 % off, now 0.022 %, the output's rounding.)  bfloat16 has fp32's
+// range: 0.
 
 #include <algorithm>
 
@@ -31,12 +37,32 @@ namespace w4a16 {
 namespace {
 
 constexpr float kSlack = 2.0f;
+constexpr float kLift = 13.0f;         // the most
 
 // a * b with 0 * anything = 0.
 __device__ __forceinline__ float mul_legacy(float a, float b) {
     float r;
     asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
+}
+
+// The larger of the low halves, and of the high halves, as whole numbers.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+}
+
+// The largest of all lanes, in a scalar register.
+__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
+#define W4A16_MAX_ROR(N) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, true))
+    W4A16_MAX_ROR(8);
+    W4A16_MAX_ROR(4);
+    W4A16_MAX_ROR(2);
+    W4A16_MAX_ROR(1);
+#undef W4A16_MAX_ROR
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
 }
 
 // v held to [-most, most]; a NaN becomes -most.
@@ -236,12 +262,14 @@ __global__ void __launch_bounds__(kThreads)
     const CodeConsts cc = code_consts<BF>();
     const uint32_t one16 = BF ? 0x3F803F80u : 0x3C003C00u;
     const u4 ones = {one16, one16, one16, one16};
-    float ref[NT], sum[NT];
+    float ref[NT], sum[NT], lift[NT];
+    uint32_t step_limit = 0x3FFF;        // fp16: the largest step, as bits, below 2^(14 - lift) of every row
     f4 out[NT][kOut], psum[NT][NG], mids[NT];      // mids: sum_t p_t (m_t + 8 s_t)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         ref[t] = kNone;
         sum[t] = 0.f;
+        lift[t] = BF ? 0.f : kLift;
         mids[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < NG; ++g) psum[t][g] = f4{0.f, 0.f, 0.f, 0.f};
@@ -253,6 +281,15 @@ __global__ void __launch_bounds__(kThreads)
         // whether some row does not see some of the tile's slots; the same in every lane
         const bool masked = 32 * tile < all_lo || 32 * tile + 32 > all_hi;
         const lds_u8 *params = at + 2 * T::kCodes + 16 * b4;
+        // parameters of the values: eight slots of one group, group r in the lanes of column r
+        const lds_u8 *mine = params + 128 * (NG + (r < NG ? r : NG - 1));
+        uint32_t steps = 0;                      // fp16: the largest step of those, as bits
+        if constexpr (!BF) {
+            const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) steps = max_halves(max_halves(steps, p0[e]), p1[e]);
+            steps &= 0xFFFFu;
+        }
         float x[NT][8];
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
@@ -317,16 +354,50 @@ __global__ void __launch_bounds__(kThreads)
             float m = fmaxf(x[t][0], x[t][1]);
 #pragma unroll
             for (int e = 2; e < 8; ++e) m = fmaxf(m, x[t][e]);
-            top[t] = m * c1;
+            top[t] = BF ? m * c1 : __builtin_fmaf(m, c1, -lift[t]);
             move |= top[t] > ref[t] + kSlack;
         }
+        if constexpr (!BF) move |= steps > step_limit;
         if (__builtin_amdgcn_ballot_w64(move)) {
+            float met[NT];
+            if constexpr (!BF) {
+                if (!masked) {                   // (neither infinities nor NaN)
+                    const float all = lo_f32<BF>(max_lanes(steps < 0x7C00u ? steps : 0u));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) met[t] = all;
+                } else {                         // each row looks at the slots that it sees
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) met[t] = 0.f;
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float s = par_step<BF>(
+                                lds_get<uint32_t>(params + 128 * (NG + g) + 64 * (e >> 2) + 4 * (e & 3)));
+                            const int slot = 32 * tile + 16 * (e >> 2) + 4 * b4 + (e & 3);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                if ((slot >= lo[t]) & (slot < hi[t]) & (s < __builtin_inff())) met[t] = fmaxf(met[t], s);
+                        }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        met[t] = fmaxf(met[t], __shfl_xor(met[t], 16));
+                        met[t] = fmaxf(met[t], __shfl_xor(met[t], 32));
+                    }
+                }
+            }
+            float highest = 0.f;                 // the largest lift
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float m = fmaxf(top[t], __shfl_xor(top[t], 16));
                 m = fmaxf(m, __shfl_xor(m, 32));
                 // (an infinite maximum stays out of the reference: its weight becomes infinite)
                 m = fmaxf(ref[t], fminf(m, 3e38f));
+                if constexpr (!BF) {             // a step in [2^(e - 1), 2^e): lift at most 14 - e, at least 0
+                    const float to = fmaxf(fminf(lift[t], (float)(14 - __builtin_amdgcn_frexp_expf(met[t]))), 0.f);
+                    m += lift[t] - to;
+                    lift[t] = to;
+                    highest = fmaxf(highest, to);
+                }
                 const float f = __builtin_amdgcn_exp2f(ref[t] - m);
                 ref[t] = m;
                 sum[t] *= f;
@@ -336,6 +407,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int o = 0; o < kOut; ++o) out[t][o] *= f;
             }
+            if constexpr (!BF) step_limit = (29u - (uint32_t)__uint_as_float(max_lanes(__float_as_uint(highest)))) * 1024 - 1;
         }
         // weights, and their products with the values' steps as matrix operands
         u4 pr[NT];
@@ -353,7 +425,6 @@ __global__ void __launch_bounds__(kThreads)
         if constexpr (kMidRows) {
             // sum_t p_t (m_t + 8 s_t) of all groups in two matrix products, row g of the first
             // operand holding group g: the rounded p_t with the middles in two parts
-            const lds_u8 *mine = at + 2 * T::kCodes + 128 * (NG + (r < NG ? r : NG - 1)) + 16 * b4;
             const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
             u4 high, low;
 #pragma unroll

@@ -37,7 +37,12 @@
 namespace w4a16 {
 namespace {
 
-constexpr float kSlackMany = 8.0f;     // the weights stay below 2^8
+// The weights stay below 2^(kLiftMany + kSlackMany).  fp16 has few numbers below 2^-14 and none below
+// 2^-25, so there the reference lies below the maximum: a rounding is relative down to 2^-21 of
+// the largest weight instead of 2^-14.
+constexpr float kSlackMany = 8.0f;
+template <bool BF>
+constexpr float kLiftMany = BF ? 0.0f : 7.0f;
 constexpr int kPairs = 6;              // products of parts
 
 __device__ __forceinline__ int part_of_offset(int pair) { return (0x011002 >> (4 * (5 - pair))) & 15; }
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         top = fmaxf(top, __shfl_xor(top, 32));
         const bool unset = ref == kNone;
         // (an infinite maximum stays out of the reference: its weight becomes infinite)
-        float by = fminf(top, 3e38f);
+        float by = fminf(top, 3e38f) - kLiftMany<BF>;
         by = unset ? (top > -__builtin_inff() ? by : 0.f) : fmaxf(by, 0.f);
         const float f = unset ? 1.f : __builtin_amdgcn_exp2f(-by);
         ref = unset ? (top > -__builtin_inff() ? by : kNone) : ref + by;
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, x[t][i]);
-        if (__builtin_amdgcn_ballot_w64(top > kSlackMany || (ref == kNone && top > -__builtin_inff())))
+        if (__builtin_amdgcn_ballot_w64(top > kLiftMany<BF> + kSlackMany || (ref == kNone && top > -__builtin_inff())))
             move_reference(top, x);
         // a NaN that a row sees makes its group NaN
         if (__builtin_amdgcn_readfirstlane(lds_get<uint32_t>(at + Shape::kAtBad))) {

@@ -1,5 +1,5 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
-that nobody sees and that hold anything."""
+that nobody sees and that hold anything, weights and values far below the largest."""
 
 from __future__ import annotations
 
@@ -34,6 +34,23 @@ def ints(v, dev):
 
 def randn(seed, *shape):
     return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape)).float()
+
+
+def slots_of(cache, b):
+    """As cache.get for every slot of sequence b at once: (codes, s, m, value) of keys and of values,
+    each [heads, slots, D] in 64 bits."""
+    t, d = np.arange(cache.lens[b]), np.arange(cache.D)
+    words, r32 = cache.words[cache.table[b, t // cache.page], :, (t % cache.page) // 32], (t % 32)[:, None]
+    out = []
+    for value, place in ((False, cache.key_at), (True, cache.value_at)):
+        at, shift = (np.broadcast_to(x, (len(t), cache.D)) for x in place(r32, d[None, :]))
+        take = lambda index: np.take_along_axis(words, np.broadcast_to(index[:, None], (*words.shape[:2], cache.D)), 2)
+        par = take(cache.param_at(value, np.broadcast_to(d // cache.group, at.shape), r32))
+        s, m = (torch.from_numpy(((par >> np.uint32(i)) & np.uint32(0xFFFF)).astype(np.uint16).view(np.int16))
+                .view(cache.dtype).double().transpose(0, 1) for i in (0, 16))
+        c = torch.from_numpy(((take(at) >> shift[:, None].astype(np.uint32)) & 15).astype(np.int64)).double().transpose(0, 1)
+        out.append((c, s, m, m + s * c))
+    return out
 
 
 # ---- buffers that do not fit ----
@@ -124,3 +141,63 @@ def test_attention_of_constant_groups_at_bfloat16_s_end(dev, group, G):
     out = w4.kv4_attention(torch.ones(1, G, 128, dtype=BF16, device=dev), cache.pages(dev), ints(cache.table, dev),
                            starts([1], dev), ints([1], dev), 1, 1)
     assert torch.equal(out.cpu(), v.to(BF16).expand(1, G, 128))
+
+
+# ---- weights and values far below the largest ----
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (128, 32), (256, 64)])
+@pytest.mark.parametrize("G", [1, 20, 200])
+@pytest.mark.parametrize("gap,size,sink", [(12.5, 0.02, 0.001), (10.5, 0.001, 0.001), (17.0, 0.02, 1.0), (9.0, 1e-4, 0.0), (17.0, 0.02, 0.0)])
+def test_attention_small_values_behind_a_dominant_slot(dev, dtype, D, group, G, gap, size, sink):
+    """The first slot's logit lies `gap` above the rest, whose values are small: their share of the
+    output still has the type's precision.  512 sequences on the same pages, so that one workgroup
+    walks over all slots.
+
+    Only channel 0 of q is not zero, which leaves of the logits' error a few roundings of one
+    product: e = 2^-20 scale |q_0| max (s (2B + 15) + |m|), and 2^-20 for the exponent.  The weights'
+    products are summed as P (B + c): 2^-18 (B + 16) sum p s for that sum.  The rest is the header's
+    bound, u |o| + 1.1 u sum p (s |c - 8| + |m + 8 s|), and half a step of the output type's smallest
+    numbers."""
+    copies, heads, n_slots = 512, 2, 5001
+    cache = ref.Cache([n_slots], heads, D, group, 256, dtype, seed=D + group)
+    cache.rng = np.random.default_rng(11)
+    # values: a mean of each channel and as much around it
+    mean = torch.from_numpy(cache.rng.standard_normal((heads, 1, D))).float() * size
+    cache.fill(scale_k=0.7, scale_v=size)
+    for b, t0 in ((0, t) for t in range(0, n_slots, 32)):       # the means go onto the offsets
+        words, count = cache.tile(b, t0), min(32, n_slots - t0)
+        for g in range(cache.ng):
+            at = cache.param_at(True, g, np.arange(count))
+            m = torch.from_numpy((words[:, at] >> np.uint32(16)).astype(np.uint16).view(np.int16)).view(dtype).float()
+            m = (m + mean[:, 0, g * group].unsqueeze(1)).to(dtype)
+            m16 = m.view(torch.int16).numpy().astype(np.uint16).astype(np.uint32)
+            words[:, at] = (words[:, at] & np.uint32(0xFFFF)) | (m16 << np.uint32(16))
+    scale = D ** -0.5
+    q0 = 1.0 / scale / 0.7
+    first_k = randn(8, heads, D)
+    first_k[:, 0] = (gap + 2.0) * 0.7                           # the other logits: deviation 1
+    cache.put(0, 0, first_k, sink * randn(9, heads, D))
+    q = torch.zeros(1, G * heads, D)
+    q[0, :, 0] = q0 * torch.linspace(0.9, 1.0, G * heads)
+    q = q.to(dtype)
+    (_, ks, km, k), (vc, s, m, v) = slots_of(cache, 0)
+    ks0 = float(ks[..., 0].max()) * (2 * (128 if dtype == BF16 else 64) + 15) + float(km[..., 0].abs().max())
+    e = 2.0 ** -20 * (1 + scale * float(q[..., 0].abs().max()) * ks0)
+    u, base = ref.U[dtype], (128 if dtype == BF16 else 64) + 16
+    args = (ints(np.repeat(cache.table, copies, 0), dev), starts([1] * copies, dev), ints([n_slots] * copies, dev))
+    out, lse = w4.kv4_attention(q.expand(copies, -1, -1).contiguous().to(dev), cache.pages(dev), *args, 1, n_slots,
+                                return_lse=True)
+    assert torch.equal(out, out[:1].expand_as(out))
+    got, worst = out[0].cpu().double(), 0.0
+    for h in range(heads):
+        rows = slice(h * G, (h + 1) * G)
+        z = scale * (q[0, rows].double() @ k[h].T)
+        p = torch.softmax(z, -1)
+        want = p @ v[h]
+        bound = (1.01 * u * want.abs() + 1.1 * u * (p @ (s[h] * (vc[h] - 8).abs() + (m[h] + 8 * s[h]).abs()))
+                 + 2.2 * e * (p @ v[h].abs()) + 2.0 ** -18 * base * (p @ s[h]) + (2.0 ** -25 if dtype == F16 else 0))
+        ratio = ((got[rows] - want).abs() / bound).max()
+        worst = max(worst, float(ratio))
+        assert ((lse[0, rows].cpu().double() - torch.logsumexp(z, -1)).abs() <= e).all()
+    assert worst <= 1, worst
