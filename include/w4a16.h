@@ -480,7 +480,8 @@ int w4a16_kv4_read(const void *pages, const int32_t *table, const int32_t *cu_se
  *   q : [T, q_heads, D];  out : [T, q_heads, D]
  *   lse : [T, q_heads] log of the sum of exp(scale q . k), or null
  *   max_q, max_kv : at least the most new tokens and slots of any sequence
- *   (the work is laid out for them; further tokens and slots are not seen)
+ *   (the work is laid out for them: outputs of further tokens are not written,
+ *   further slots are not seen, and neither moves a token to another slot)
  *   scale : finite and positive
  *   workspace : w4a16_kv4_attention_workspace_bytes(...) bytes, caller-owned,
  *   no initial contents (null when that is 0); calls that overlap in time must

@@ -30,27 +30,30 @@ constexpr float kLargest = BF ? 3.3895314e38f : 65504.0f;
 // a range of its slots.
 struct Work {
     int b, h, len, n, first;      // sequence, head, slots, new tokens, row of q of the first new token
+    int start;                    // slot of the first new token
     int row0, rows;               // first row of the tile; rows of the sequence
     int t0, t1;                   // tiles of slots that any row of the tile sees
 };
 
 __device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int row0, int rows_per, Work *w) {
-    const int64_t first = a.cu[b];
-    const int64_t n64 = min((int64_t)a.cu[b + 1], a.T) - first;
+    const int64_t first = a.cu[b], end = a.cu[b + 1], kv_len = max(a.kv_len[b], 0);
+    const int64_t n64 = min(end, a.T) - first;
     if (first < 0 || n64 <= 0) return false;
     w->b = b;
     w->h = h;
     w->first = (int)first;
+    // the limits cut off rows and slots; where a token sits does not depend on them
     w->n = (int)min(n64, (int64_t)a.max_q);
+    w->start = (int)max(kv_len - (end - first), (int64_t)-0x3fffffff);
     const int64_t cap = (int64_t)a.c.table_stride * a.c.tiles_per_page * 32;
-    w->len = (int)min((int64_t)min(max(a.kv_len[b], 0), a.max_kv), cap);
+    w->len = (int)min(min(kv_len, (int64_t)a.max_kv), cap);
     const int G = a.q_heads / a.c.kv_heads;
     w->row0 = row0;
     w->rows = w->n * G;
     if (row0 >= w->rows) return false;
     const int last = min(row0 + rows_per, w->rows) - 1;
-    const int lo = row_lo(row0 / G, w->n, w->len, a.window);
-    const int hi = row_hi(last / G, w->n, w->len, a.causal);
+    const int lo = row_lo(row0 / G, w->start, a.window);
+    const int hi = row_hi(last / G, w->start, w->len, a.causal);
     w->t0 = lo >> 5;
     w->t1 = hi > lo ? (hi + 31) >> 5 : w->t0;
     return true;

@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kThreads)
         const int row = w.row0 + 16 * t + r;
         const bool in_seq = row < w.rows;
         const int i = in_seq ? row / G : 0;
-        lo[t] = in_seq ? row_lo(i, w.n, w.len, a.window) : 0;
-        hi[t] = in_seq ? row_hi(i, w.n, w.len, a.causal) : 0;
+        lo[t] = in_seq ? row_lo(i, w.start, a.window) : 0;
+        hi[t] = in_seq ? row_hi(i, w.start, w.len, a.causal) : 0;
         if (in_seq) {
             all_lo = max(all_lo, lo[t]);
             all_hi = min(all_hi, hi[t]);

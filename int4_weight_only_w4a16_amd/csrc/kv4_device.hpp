@@ -104,12 +104,13 @@ __device__ __forceinline__ float bf16_part(float v, int part) {
     return part == 1 ? b : round_act<true>(v - a - b);
 }
 
-// The slots that query row `i` of a sequence sees: [lo, hi).
-__device__ __forceinline__ int row_hi(int i, int n, int len, bool causal) {
-    return causal ? min(len, len - n + i + 1) : len;
+// The slots that new token `i` of a sequence sees, [lo, hi): `start` is the slot of the first
+// new one, and those from `len` on are not seen.
+__device__ __forceinline__ int row_hi(int i, int start, int len, bool causal) {
+    return causal ? min(len, start + i + 1) : len;
 }
-__device__ __forceinline__ int row_lo(int i, int n, int len, int window) {
-    return window > 0 ? max(0, len - n + i + 1 - window) : 0;
+__device__ __forceinline__ int row_lo(int i, int start, int window) {
+    return window > 0 ? max(0, start + i + 1 - window) : 0;
 }
 
 }  // namespace w4a16

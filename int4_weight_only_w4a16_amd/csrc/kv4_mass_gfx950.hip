@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(Kv4AttnArgs a, int c
         const float lse = a.lse[token * a.q_heads + head];
         // (a row that saw nothing adds nothing)
         const bool seen = in_seq && lse != -__builtin_inff();
-        lo[t] = seen ? row_lo(i, w.n, w.len, a.window) : 0;
-        hi[t] = seen ? row_hi(i, w.n, w.len, a.causal) : 0;
+        lo[t] = seen ? row_lo(i, w.start, a.window) : 0;
+        hi[t] = seen ? row_hi(i, w.start, w.len, a.causal) : 0;
         shift[t] = -lse * kLog2e;
         const uint16_t *src = static_cast<const uint16_t *>(a.q) + token * a.q_stride + (int64_t)head * D + 8 * b4;
 #pragma unroll
@@ -235,10 +235,9 @@ __global__ void __launch_bounds__((kManyThreads<D, TILES>)) many_rows_kernel(Kv4
         tile < w.t1 ? tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, w.b, w.h, tile) : nullptr;
 
     // the rows that see any of the workgroup's slots, in stages of kStageRows from a multiple of it
-    const int back = w.len - w.n;                                // slot of the first new token
-    const int i0 = a.causal ? max(0, 32 * tile0 - back) : 0;
+    const int i0 = a.causal ? max(0, 32 * tile0 - w.start) : 0;
     const int64_t last_slot = 32 * (int64_t)tile0 + kManySlots - 1;
-    const int i1 = a.window > 0 ? (int)min((int64_t)w.n, last_slot + a.window - back) : w.n;
+    const int i1 = a.window > 0 ? (int)min((int64_t)w.n, last_slot + a.window - w.start) : w.n;
     const int row_begin = i0 * G / kStageRows * kStageRows;
     const int row_end = min((int64_t)i1 * G, (int64_t)w.rows);
     if (row_begin >= row_end) return;
@@ -340,8 +339,8 @@ __global__ void __launch_bounds__((kManyThreads<D, TILES>)) many_rows_kernel(Kv4
     };
     load_lse();
     // rows that see the whole tile: [all0, all1)
-    const int64_t first_all = a.causal ? max(0, 32 * tile + 31 - back) : 0;
-    const int64_t last_all = a.window > 0 ? min((int64_t)w.n, (int64_t)32 * tile + a.window - back) : w.n;
+    const int64_t first_all = a.causal ? max(0, 32 * tile + 31 - w.start) : 0;
+    const int64_t last_all = a.window > 0 ? min((int64_t)w.n, (int64_t)32 * tile + a.window - w.start) : w.n;
     const bool any_all = 32 * tile + 32 <= w.len;
     const int all0 = any_all ? (int)min(first_all * G, (int64_t)w.rows) : w.rows;
     const int all1 = any_all ? (int)max(last_all * G, (int64_t)0) : 0;
@@ -374,8 +373,8 @@ __global__ void __launch_bounds__((kManyThreads<D, TILES>)) many_rows_kernel(Kv4
             } else {
                 const int row = ra + col, i = min(row, w.rows - 1) / G;
                 const bool in_seq = row < w.rows;
-                int lo = (in_seq ? row_lo(i, w.n, w.len, a.window) : 0) - 32 * tile - 4 * half;
-                int hi = (in_seq ? row_hi(i, w.n, w.len, a.causal) : 0) - 32 * tile - 4 * half;
+                int lo = (in_seq ? row_lo(i, w.start, a.window) : 0) - 32 * tile - 4 * half;
+                int hi = (in_seq ? row_hi(i, w.start, w.len, a.causal) : 0) - 32 * tile - 4 * half;
                 if (!in_seq) hi = lo;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {

@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     const int row = w.row0 + 32 * wave + col;
     const bool in_seq = row < w.rows;
     const int token = in_seq ? row / G : 0, head = w.h * G + (in_seq ? row - token * G : 0);
-    const int lo = in_seq ? row_lo(token, w.n, w.len, a.window) : 0;
-    const int hi = in_seq ? row_hi(token, w.n, w.len, a.causal) : 0;
+    const int lo = in_seq ? row_lo(token, w.start, a.window) : 0;
+    const int hi = in_seq ? row_hi(token, w.start, w.len, a.causal) : 0;
     u4 q[kDeep], sums[kTerms];
     {
         const uint16_t *src = static_cast<const uint16_t *>(a.q) + (int64_t)(w.first + token) * a.q_stride +

@@ -1,7 +1,10 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
-that nobody sees and that hold anything, weights and values far below the largest."""
+that nobody sees and that hold anything, weights and values far below the largest,
+lengths past the tables and the given maxima."""
 
 from __future__ import annotations
+
+import math
 
 import numpy as np
 import pytest
@@ -15,6 +18,7 @@ torch = pytest.importorskip("torch")
 import int4_weight_only_w4a16_amd as w4  # noqa: E402
 
 F16, BF16 = torch.float16, torch.bfloat16
+E_LOGIT = 2.0 ** -15
 
 
 @pytest.fixture(scope="module")
@@ -201,3 +205,75 @@ def test_attention_small_values_behind_a_dominant_slot(dev, dtype, D, group, G, 
         worst = max(worst, float(ratio))
         assert ((lse[0, rows].cpu().double() - torch.logsumexp(z, -1)).abs() <= e).all()
     assert worst <= 1, worst
+
+
+# ---- lengths past the tables and the given maxima ----
+
+def by_definition(cache, q, ns, lens, visible, scale, causal, window, rows):
+    """Attention of the first `rows` tokens of each sequence: token i of n sits in slot len - n + i, and
+    slots at or past visible[b] are not seen.  Returns out, lse, the bound's magnitudes and the weights."""
+    T, hq, D = q.shape
+    G = hq // cache.heads
+    out = torch.zeros(T, hq, D, dtype=torch.float64)
+    rough, mag = torch.zeros_like(out), torch.zeros_like(out)
+    lse = torch.full((T, hq), -math.inf, dtype=torch.float64)
+    size = torch.zeros(T, hq, dtype=torch.float64)
+    acc, at = [], 0
+    for b, n in enumerate(ns):
+        (_, _, _, k), (vc, s, _, v) = slots_of(cache, b)
+        c8 = vc - 8
+        total = torch.zeros(cache.heads, cache.lens[b], dtype=torch.float64)
+        for i in range(min(n, rows)):
+            lo, hi = ref.sees(i, n, lens[b], causal, window)
+            hi = min(hi, visible[b])
+            if hi <= lo:
+                continue
+            for h in range(cache.heads):
+                r = slice(h * G, (h + 1) * G)
+                qq = q[at + i, r].double()
+                z = scale * (qq @ k[h, lo:hi].T)
+                p = torch.softmax(z, -1)
+                out[at + i, r] = p @ v[h, lo:hi]
+                rough[at + i, r] = p @ (s[h, lo:hi] * c8[h, lo:hi].abs())
+                mag[at + i, r] = p @ (v[h, lo:hi].abs() + 24 * s[h, lo:hi])
+                lse[at + i, r] = torch.logsumexp(z, -1)
+                size[at + i, r] = scale * (qq.abs() @ k[h, lo:hi].abs().T).amax(-1)
+                total[h, lo:hi] += p.sum(0)
+        acc.append(total)
+        at += n
+    return out, lse, rough, mag, size, acc
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("hq,window,causal", [(4, 0, True), (4, 30, True), (4, 0, False), (48, 0, True), (48, 30, True)])
+@pytest.mark.parametrize("ns,lens,max_q,max_kv", [
+    ([3, 9, 4], [66, 100, 40], 9, 200),            # past the tables' 64 slots
+    ([7, 5, 12], [60, 64, 33], 5, 64),             # more tokens than max_q
+    ([6, 9, 2], [50, 64, 20], 9, 47),              # more slots than max_kv
+    ([6, 12, 1], [70, 200, 64], 4, 40),            # all of it; one whose tokens lie past the end
+])
+def test_positions_do_not_move_with_the_limits(dev, dtype, hq, window, causal, ns, lens, max_q, max_kv):
+    cache = ref.Cache([64, 64, 64], 2, 128, 64, 32, dtype, seed=4)
+    cache.fill()
+    q = (1.5 * randn(6, sum(ns), hq, 128)).to(dtype)
+    args = (cache.pages(dev), ints(cache.table, dev), starts(ns, dev), ints(lens, dev))
+    out = torch.full_like(q, 7.0, device=dev)
+    lse = torch.full(q.shape[:2], 7.0, device=dev)
+    w4.kv4_attention(q.to(dev), *args, max_q, max_kv, window=window, causal=causal, out=out, lse=lse)
+    visible = [min(n, 64, max_kv) for n in lens]
+    o, l, rough, mag, size, acc = by_definition(cache, q, ns, lens, visible, 128 ** -0.5, causal, window, max_q)
+    done = torch.cat([torch.arange(n) < max_q for n in ns])
+    assert (out.cpu()[~done] == 7).all() and (lse.cpu()[~done] == 7).all()      # further tokens are left alone
+    e = E_LOGIT * size.clamp(min=1.0)
+    bound = 1.01 * ref.U[dtype] * o.abs() + 1.1 * ref.U[dtype] * rough + 2.2 * e[..., None] * mag + 2.0 ** -24
+    assert ((out.cpu().double() - o).abs() <= bound)[done].all()
+    seen = torch.isfinite(l) & done[:, None]
+    got = lse.cpu().double()
+    assert ((got - l).abs()[seen] <= e[seen]).all() and (got[done[:, None] & ~seen] == -math.inf).all()
+    weights = w4.kv4_attention_mass(q.to(dev), *args, lse, torch.zeros(3, 2, max(64, max_kv), device=dev), max_q, max_kv,
+                                    window=window, causal=causal).cpu().double()
+    assert (weights[:, :, 64:] == 0).all()
+    weights = weights[:, :, :64]
+    e = 4 * E_LOGIT * max(1.0, float(size.max()))
+    for b, want in enumerate(acc):
+        assert ((weights[b] - want).abs() <= e * want + 2.0 ** -22 * want).all()
