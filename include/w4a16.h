@@ -451,7 +451,8 @@ int w4a16_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
 /* The call's keys and values into the cache, and in the same launch the norm
  * and rotation of keys (before they are quantised, from the fp32 values) and
  * of queries (to q_out).  q_heads = 0: keys and values only.  max_q: at least
- * the most tokens of any sequence.  Two calls that write the same tile must
+ * the most tokens of any sequence (of more, the first max_q are stored, in
+ * their slots).  Two calls that write the same tile must
  * not overlap in time; older slots of the tile are kept. */
 int w4a16_kv4_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, const float *q_weight,

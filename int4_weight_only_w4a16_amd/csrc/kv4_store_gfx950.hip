@@ -200,18 +200,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv4AppendArgs a, int t
     const int h = blockIdx.x % a.c.kv_heads;
     const int rest = blockIdx.x / a.c.kv_heads;
     const int b = rest / tiles;
-    const int64_t first = a.cu[b];
-    const int64_t n64 = min((int64_t)a.cu[b + 1], a.T) - first;
+    const int64_t first = a.cu[b], end = a.cu[b + 1];
+    const int64_t n64 = min(end, a.T) - first;
     if (first < 0 || n64 <= 0) return;
-    const int n = (int)min(n64, (int64_t)a.max_q);
-    const int len = a.kv_len[b];
-    const int start = len - n;                   // slot of the first new token
-    const int tile = (start >> 5) + rest % tiles;
-    const int base = 32 * tile;
-    if (base < 0 || base >= len) return;
+    // slots of the first new token, and after the last one that max_q leaves
+    const int64_t start64 = (int64_t)a.kv_len[b] - (end - first);
+    const int64_t base64 = 32 * ((start64 >> 5) + rest % tiles);
+    const int stop = (int)min(start64 + min(n64, (int64_t)a.max_q), (int64_t)0x7fffffff);
+    if (base64 < 0 || base64 >= stop) return;
+    const int start = (int)start64, base = (int)base64, tile = base >> 5;
     uint8_t *p = tile_at<D, NG>(a.c, a.c.table, a.c.table_stride, b, h, tile);
     if (!p) return;
-    const int lo = max(start - base, 0), hi = min(len - base, 32), count = hi - lo;
+    const int lo = max(start - base, 0), hi = min(stop - base, 32), count = hi - lo;
     uint32_t *words = reinterpret_cast<uint32_t *>(p);
     uint32_t *params = reinterpret_cast<uint32_t *>(p + 2 * T::kCodes);
     for (int idx = threadIdx.x; idx < 2 * count * kLanes; idx += kThreads) {

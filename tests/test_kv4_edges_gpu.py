@@ -277,3 +277,21 @@ def test_positions_do_not_move_with_the_limits(dev, dtype, hq, window, causal, n
     e = 4 * E_LOGIT * max(1.0, float(size.max()))
     for b, want in enumerate(acc):
         assert ((weights[b] - want).abs() <= e * want + 2.0 ** -22 * want).all()
+
+
+def test_append_of_more_tokens_than_max_q_stores_the_first_ones(dev):
+    """... in their own slots; the others' slots stay as they are."""
+    D, ns, lens, max_q = 64, [7, 3, 40], [50, 20, 41], 4
+    cache = ref.Cache(lens, 2, D, 32, 32, F16, seed=2)
+    cache.fill()
+    x = randn(3, sum(ns), 2, D).to(F16)
+    pages = cache.pages(dev)
+    w4.kv4_append(pages, x.to(dev), x.to(dev), ints(cache.table, dev), starts(ns, dev), ints(lens, dev), max_q)
+    at = 0
+    for b, n in enumerate(ns):
+        for i in range(min(n, max_q)):
+            cache.put(b, lens[b] - n + i, x[at + i], x[at + i])
+        at += n
+    got = ref.Cache(lens, 2, D, 32, 32, F16, seed=2)
+    got.back(pages)
+    np.testing.assert_array_equal(got.words, cache.words)
