@@ -484,6 +484,8 @@ int w4a16_kv4_read(const void *pages, const int32_t *table, const int32_t *cu_se
  *   (the work is laid out for them: outputs of further tokens are not written,
  *   further slots are not seen, and neither moves a token to another slot)
  *   scale : finite and positive
+ *   q_heads * max_q : up to about 16.7 million (8.3 with 256 channels; rows of
+ *   a head are counted in tiles of 256, or 128, of which there may be 65535)
  *   workspace : w4a16_kv4_attention_workspace_bytes(...) bytes, caller-owned,
  *   no initial contents (null when that is 0); calls that overlap in time must
  *   not share one.

@@ -106,7 +106,8 @@ __device__ __forceinline__ void wait_loads() {
 
 }  // namespace
 
-// The kernel for many rows, and its plan (kv4_prefill_gfx950.hip).
+// The kernel for many rows, the rows of its tiles and its plan (kv4_prefill_gfx950.hip).
+int prefill_rows(int head_dim);
 Plan prefill_plan(const Kv4AttnArgs &a);
 hipError_t launch_kv4_prefill(const Kv4AttnArgs &a, const Plan &p, hipStream_t stream);
 

@@ -84,14 +84,19 @@ constexpr int kFewSlots = 512, kManySlots = 1024, kFewSequences = 4;
 constexpr int kFewRows = 192;
 int rows_of(const Kv4AttnArgs &a) { return a.q_heads / a.c.kv_heads * a.max_q; }
 
+// 32 rows a wave read the cache half as often as 16, at two waves a SIMD instead of three (32
+// rows, 32 sequences of 16000 slots: 184 us, 221 with 16; 8 of 4000: 33 and 31; 256 channels:
+// 32 would not fit the registers)
+int tile_rows(const Kv4AttnArgs &a) {
+    if (rows_of(a) > kFewRows) return prefill_rows(a.c.head_dim);
+    return rows_of(a) > 16 && a.c.head_dim <= 128 ? 32 : 16;
+}
+
 Plan plan_of(const Kv4AttnArgs &a) {
     const int rows = rows_of(a);
     if (rows > kFewRows) return prefill_plan(a);
     Plan p;
-    // 32 rows a wave read the cache half as often as 16, at two waves a SIMD instead of three (32
-    // rows, 32 sequences of 16000 slots: 184 us, 221 with 16; 8 of 4000: 33 and 31; 256 channels:
-    // 32 would not fit the registers)
-    p.rows = rows > 16 && a.c.head_dim <= 128 ? 32 : 16;
+    p.rows = tile_rows(a);
     p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min(tiles, (a.window + a.max_q) / 32 + 2);
@@ -641,6 +646,10 @@ hipError_t by_shape(const Kv4Cache &c, F f) {
 }
 
 }  // namespace
+
+int64_t kv4_attention_row_tiles(const Kv4AttnArgs &a) {
+    return ((int64_t)rows_of(a) + tile_rows(a) - 1) / tile_rows(a);
+}
 
 size_t kv4_attention_workspace_bytes(const Kv4AttnArgs &a) {
     const Plan p = plan_of(a);

@@ -138,9 +138,8 @@ int check_attention(const CacheShape &s, int64_t T, int64_t q_heads, int64_t max
     if (!in_range(max_q, 0, 1 << 24) || !in_range(max_kv, 0, kMax - 64) || !in_range(window, 0, kMax / 2) ||
         !std::isfinite(scale) || !(scale > 0.f))
         return W4A16_ERR_SHAPE;
-    // rows of one sequence and the launch's second dimension
-    if (q_heads / s.kv_heads * max_q > kMax / 2 || (q_heads / s.kv_heads * max_q + 15) / 16 * s.kv_heads > 65535)
-        return W4A16_ERR_SHAPE;
+    // rows of one sequence and head
+    if (!in_range(q_heads, 1, 1 << 15) || q_heads / s.kv_heads * max_q > kMax / 2) return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
 
@@ -270,6 +269,11 @@ static w4a16::Kv4AttnArgs attention_args(const w4a16::Kv4Cache &c, const void *q
     return a;
 }
 
+// The attention's launch: heads and tiles of rows in its second dimension.
+static bool attention_fits(const w4a16::Kv4AttnArgs &a) {
+    return a.c.kv_heads * w4a16::kv4_attention_row_tiles(a) <= 65535;
+}
+
 extern "C" int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
                                    const int32_t *cu_seqlens, const int32_t *kv_len, void *out, int64_t out_stride,
                                    float *lse, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
@@ -280,12 +284,13 @@ extern "C" int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *
     int st = check_attention(s, T, q_heads, max_q, max_kv, window, scale, flags);
     if (st == W4A16_OK) st = check_queries(q, q_stride, out, out_stride, q_heads, kv_heads, head_dim, T);
     if (st != W4A16_OK) return st;
+    w4a16::Kv4AttnArgs a = attention_args(make_cache(pages, table, s, flags), q, q_stride, cu_seqlens, kv_len, T,
+                                          q_heads, max_q, max_kv, scale, window, flags);
+    if (!attention_fits(a)) return W4A16_ERR_SHAPE;
     if (!aligned(lse, 4)) return W4A16_ERR_ALIGN;
     if (T == 0 || batch == 0 || max_q == 0) return W4A16_OK;
     st = check_cache_pointers(pages, table, cu_seqlens, kv_len);
     if (st != W4A16_OK) return st;
-    w4a16::Kv4AttnArgs a = attention_args(make_cache(pages, table, s, flags), q, q_stride, cu_seqlens, kv_len, T,
-                                          q_heads, max_q, max_kv, scale, window, flags);
     a.out = out;
     a.out_stride = out_stride;
     a.lse = lse;
@@ -305,11 +310,11 @@ extern "C" size_t w4a16_kv4_attention_workspace_bytes(int64_t batch, int64_t q_h
                                                       int64_t window) {
     const CacheShape s{kv_heads, head_dim, 64, 32, 0, batch, 0};
     if (kv_heads <= 0 || check_attention(s, 0, q_heads, max_q, max_kv, window, 1.f, 0) != W4A16_OK ||
-        q_heads <= 0 || q_heads % kv_heads != 0 || batch == 0 || max_q == 0)
+        q_heads % kv_heads != 0 || batch == 0 || max_q == 0)
         return 0;
-    const w4a16::Kv4Cache c = make_cache(nullptr, nullptr, s, 0);
-    return w4a16::kv4_attention_workspace_bytes(
-        attention_args(c, nullptr, 0, nullptr, nullptr, 0, q_heads, max_q, max_kv, 1.f, window, 0));
+    const w4a16::Kv4AttnArgs a = attention_args(make_cache(nullptr, nullptr, s, 0), nullptr, 0, nullptr, nullptr, 0,
+                                                q_heads, max_q, max_kv, 1.f, window, 0);
+    return attention_fits(a) ? w4a16::kv4_attention_workspace_bytes(a) : 0;
 }
 
 extern "C" int w4a16_kv4_attention_mass(const void *q, int64_t q_stride, const void *pages, const int32_t *table,

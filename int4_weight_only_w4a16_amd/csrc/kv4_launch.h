@@ -98,6 +98,9 @@ struct Kv4AttnArgs {
     float scale = 1.f;
     void *workspace = nullptr;
 };
+// Tiles of rows that a head of one sequence is divided into (the attention's launch has them and
+// the heads in one dimension).
+int64_t kv4_attention_row_tiles(const Kv4AttnArgs &a);
 size_t kv4_attention_workspace_bytes(const Kv4AttnArgs &a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream);
 hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream);

@@ -523,10 +523,12 @@ hipError_t by_shape(const Kv4Cache &c, F f) {
 
 }  // namespace
 
+int prefill_rows(int head_dim) { return (head_dim <= 128 ? kManyThreads<128> : kManyThreads<256>) / 2; }
+
 Plan prefill_plan(const Kv4AttnArgs &a) {
     Plan p;
     const int rows = a.q_heads / a.c.kv_heads * a.max_q;
-    p.rows = (a.c.head_dim <= 128 ? kManyThreads<128> : kManyThreads<256>) / 2;
+    p.rows = prefill_rows(a.c.head_dim);
     p.row_tiles = (rows + p.rows - 1) / p.rows;
     int tiles = (a.max_kv + 31) / 32;
     if (a.window > 0) tiles = std::min(tiles, (a.window + std::min(a.max_q, p.rows)) / 32 + 2);

@@ -1,0 +1,41 @@
+"""What the 4-bit cache's entry points take and refuse at the edges, through the C ABI on the
+CPU: every check runs before any HIP call, and a call that passes them all ends here with
+W4A16_ERR_DEVICE, so the made-up addresses below are never touched."""
+
+import pytest
+
+import int4_weight_only_w4a16_amd as w4
+from test_kv4_boundary_cpu import append, attention, evict, lib, mass, norm_rope, read  # noqa: F401
+
+S = w4.W4A16_ERR_SHAPE
+
+
+@pytest.fixture(autouse=True)
+def no_gpu():
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+
+
+# ---- prompts of very many rows ----
+
+@pytest.mark.parametrize("hq,hk,D", [(40, 8, 128), (32, 8, 64), (128, 8, 128), (64, 64, 128), (16, 4, 256)])
+def test_attention_of_long_prompts(lib, hq, hk, D):  # noqa: F811
+    """Up to 65535 tiles of 256 rows (128 with 256 channels) over all heads; the weights have no such limit."""
+    kw = dict(hq=hq, hk=hk, D=D, qs=hq * D, os=hq * D, max_kv=1 << 20)
+    most = 65535 // hk * (256 if D <= 128 else 128) // (hq // hk)
+    assert most > 100000
+    for tokens in (4096, 8192, 16384, 32768, 100000, most):
+        assert attention(lib, **kw, max_q=tokens) == w4.W4A16_ERR_DEVICE
+        assert mass(lib, hq=hq, hk=hk, D=D, qs=hq * D, max_q=tokens) == w4.W4A16_ERR_DEVICE
+    assert attention(lib, **kw, max_q=most + 1) == S
+    assert attention(lib, **kw, max_q=most + 1, T=0) == S
+    assert mass(lib, hq=hq, hk=hk, D=D, qs=hq * D, max_q=most + 1) == w4.W4A16_ERR_DEVICE
+    assert w4.kv4_attention_workspace_bytes(1, hq, hk, D, most + 1, 1 << 20) == 0
+
+
+def test_rows_of_a_head_are_32_bits(lib):  # noqa: F811
+    assert mass(lib, hq=256, hk=1, qs=256 * 128, max_q=1 << 22) == S
+    assert mass(lib, hq=255, hk=1, qs=255 * 128, max_q=1 << 22) == w4.W4A16_ERR_DEVICE
+    for f in (attention, mass):
+        assert f(lib, hq=1 << 40) == S and f(lib, hq=-8) == S

@@ -1,6 +1,6 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
 that nobody sees and that hold anything, weights and values far below the largest,
-lengths past the tables and the given maxima."""
+lengths past the tables and the given maxima, prompts of very many rows."""
 
 from __future__ import annotations
 
@@ -295,3 +295,35 @@ def test_append_of_more_tokens_than_max_q_stores_the_first_ones(dev):
     got = ref.Cache(lens, 2, D, 32, 32, F16, seed=2)
     got.back(pages)
     np.testing.assert_array_equal(got.words, cache.words)
+
+
+# ---- prompts of very many rows ----
+
+@pytest.mark.parametrize("dtype,hq,D,n", [(F16, 2048, 64, 515), (BF16, 4096, 128, 260)])
+def test_attention_and_mass_of_a_million_rows(dev, dtype, hq, D, n):
+    """Every row against 64-bit products (on the GPU, a token at a time)."""
+    cache = ref.Cache([n + 5], 1, D, 64, 64, dtype, seed=7)
+    cache.fill()
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(3)
+    q = (1.5 * torch.randn(n, hq, D, generator=gen, device=dev)).to(dtype)
+    args = (cache.pages(dev), ints(cache.table, dev), starts([n], dev), ints([n + 5], dev))
+    out, lse = w4.kv4_attention(q, *args, n, n + 5, return_lse=True)
+    acc = w4.kv4_attention_mass(q, *args, lse, torch.zeros(1, 1, n + 5, device=dev), n, n + 5)[0, 0].double()
+    (_, _, _, k), (c, s, _, v) = ([t[0].to(dev) for t in part] for part in slots_of(cache, 0))
+    kt, rough, mag = k.T.contiguous(), s * (c - 8).abs(), v.abs() + 24 * s
+    u, total, worst = ref.U[dtype], torch.zeros_like(acc), 0.0
+    for i in range(n):
+        seen, qq = n + 5 - n + i + 1, q[i].double()
+        z = (qq @ kt)[:, :seen] * D ** -0.5
+        p = torch.softmax(z, -1)
+        total[:seen] += p.sum(0)
+        size = (qq.abs() @ kt.abs())[:, :seen].amax(-1, keepdim=True) * D ** -0.5
+        e = E_LOGIT * size.clamp(min=1.0)
+        want = p @ v[:seen]
+        bound = 1.01 * u * want.abs() + 1.1 * u * (p @ rough[:seen]) + 2.2 * e * (p @ mag[:seen]) + 2.0 ** -24
+        worst = max(worst, float(((out[i].double() - want).abs() / bound).max()))
+        assert ((lse[i].double() - torch.logsumexp(z, -1)).abs() <= e[:, 0]).all(), i
+    assert worst <= 1, worst
+    # (the sizes of the logits here are below 60; sums of up to a million weights in fp32)
+    assert ((acc - total).abs() <= 4 * E_LOGIT * 60 * total).all()
