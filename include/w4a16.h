@@ -531,7 +531,9 @@ int w4a16_kv4_attention_mass(const void *q, int64_t q_stride, const void *pages,
  * at most budget slots keep all.  What is kept is copied in its order to slots
  * 0 .. new_len - 1 of the pages in dst_table (same buffer; they must be none of
  * the pages that `table` names for slots in use), so heads no longer hold the
- * same tokens in a slot; the rotation of a key stays that of its token.
+ * same tokens in a slot; the rotation of a key stays that of its token.  Of
+ * slots on an unknown page the copies are NaN; slots past the table or past
+ * max_kv do not count as the sequence's.
  *   dst_table int32 [batch][dst_stride], dst_stride * page_size >= budget
  *   acc : fp32 [batch, kv_heads, acc_stride], acc_stride >= max_kv
  *   kept int32, acc_out fp32 : [batch, kv_heads, budget], the source slot and

@@ -15,7 +15,8 @@
 // them in order.  Bound by latency: five passes over weights that stay in L2.
 // One sequence of 8192 slots, 8 heads: 12.7 us; 16 of 3000 to 33001: 36 us.
 // copy_kernel: a workgroup per tile of the destination, all of its loads before the
-// first store.  Bound by the source's cache lines, of which a kept slot's value codes touch
+// first store.  A kept slot whose page is not there becomes NaN, as kv4_read gives it.  Bound
+// by the source's cache lines, of which a kept slot's value codes touch
 // every one of its tile: 4096 slots of each of those 16 sequences 90 us, 2048 of the one 4.4.
 
 #include "kv4_device.hpp"
@@ -196,7 +197,8 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(Kv4EvictArgs a) {
         if (threadIdx.x == 0) there_mask = (uint32_t)mask;
     }
     __syncthreads();
-    const uint32_t there = there_mask;
+    const uint32_t there = there_mask, used = len - base < 32 ? (1u << (len - base)) - 1 : ~0u;
+    constexpr uint32_t kNaNs = 0x7FC07FC0u;      // in either type
     uint32_t *words = reinterpret_cast<uint32_t *>(dst);
     constexpr int kCodeWords = T::kCodes / 4;
     constexpr int kKeyWords = 32 * (D / 8) / kCopy, kValueWords = 4 * D / kCopy ? 4 * D / kCopy : 1;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(Kv4EvictArgs a) {
 #pragma unroll
     for (int k = 0; k < kKeyWords; ++k) {
         const int idx = threadIdx.x + k * kCopy, r32 = idx / (D / 8);
-        if (there >> r32 & 1) words[key_word<D>(r32, idx % (D / 8))] = keys[k];
+        if (used >> r32 & 1) words[key_word<D>(r32, idx % (D / 8))] = there >> r32 & 1 ? keys[k] : 0u;
     }
 #pragma unroll
     for (int k = 0; k < kValueWords; ++k) {
@@ -242,7 +244,8 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(Kv4EvictArgs a) {
 #pragma unroll
     for (int k = 0; k < (64 * NG + kCopy - 1) / kCopy; ++k) {
         const int at = threadIdx.x + k * kCopy;
-        if (at < 64 * NG && (there >> (at & 31) & 1)) words[2 * kCodeWords + at] = params[k];
+        if (at < 64 * NG && (used >> (at & 31) & 1))
+            words[2 * kCodeWords + at] = there >> (at & 31) & 1 ? params[k] : kNaNs;
     }
 }
 

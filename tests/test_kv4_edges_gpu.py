@@ -1,6 +1,7 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
 that nobody sees and that hold anything, weights and values far below the largest,
-lengths past the tables and the given maxima, prompts of very many rows."""
+lengths past the tables and the given maxima, prompts of very many rows, pages that
+are not there."""
 
 from __future__ import annotations
 
@@ -327,3 +328,33 @@ def test_attention_and_mass_of_a_million_rows(dev, dtype, hq, D, n):
     assert worst <= 1, worst
     # (the sizes of the logits here are below 60; sums of up to a million weights in fp32)
     assert ((acc - total).abs() <= 4 * E_LOGIT * 60 * total).all()
+
+
+# ---- pages that are not there ----
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_evict_gives_nan_for_kept_slots_that_are_not_there(dev, dtype):
+    """As kv4_read does for such slots: what the destination held before does not show."""
+    D, lens, budget = 128, [96, 40], 70
+    cache = ref.Cache(lens, 2, D, 64, 32, dtype, seed=1, spare=6)
+    cache.fill()
+    dst = cache.free[:6].reshape(2, 3).astype(np.int32)
+    for page in dst.ravel():                               # old, valid contents
+        cache.words[page] = cache.words[cache.table[0, 0]]
+    table = cache.table.copy()
+    table[0, 1], table[1, 0] = cache.num_pages, -1         # slots 32..63 of the first, 0..31 of the second
+    pages = cache.pages(dev)
+    acc = torch.rand(2, 2, 96, device=dev)
+    kept, new, _ = w4.kv4_evict(pages, ints(table, dev), ints(lens, dev), acc, budget, 8, ints(dst, dev), D, 96)
+    k, v = (t.cpu() for t in w4.kv4_read(pages, ints(dst, dev), starts([70, 40], dev), new, 110, D, dtype))
+    for b, (first, count) in enumerate(((0, 70), (70, 40))):
+        for h in range(2):
+            for t in range(count):
+                slot = int(kept[b, h, t])
+                gone = 32 <= slot < 64 if b == 0 else slot < 32
+                if gone:
+                    assert torch.isnan(k[first + t, h]).all() and torch.isnan(v[first + t, h]).all()
+                else:
+                    want = cache.get(b, slot)
+                    assert torch.equal(k[first + t, h].double(), want[0][3][h].float().to(dtype).double())
+                    assert torch.equal(v[first + t, h].double(), want[1][3][h].float().to(dtype).double())
