@@ -434,7 +434,8 @@ size_t w4a16_kv4_page_bytes(int64_t kv_heads, int64_t head_dim, int64_t group_si
 /* Norm and rotation of queries and keys in one pass:
  *     y = x / sqrt(mean(x^2) + eps) * weight     over the D channels of a head
  *     (a, b) -> (a cos - b sin, b cos + a sin)   pairs of the first rot_dim
- * in fp32, rounded once to the activation type.
+ * in fp32 (the norm in 64 bits where squares leave fp32), rounded once to the
+ * activation type.
  *   q, k : [T, q_heads, D] and [T, kv_heads, D] (either may have no heads)
  *   q_weight, k_weight : [D], or null: no norm of those heads
  *   cos, sin : [max_pos, rot_dim / 2], or null (both): no rotation;

@@ -71,7 +71,18 @@ __device__ __forceinline__ void norm_rope(float (&x)[8], int i, const float *wei
                     (((x[4] * x[4] + x[5] * x[5]) + x[6] * x[6]) + x[7] * x[7]);
 #pragma unroll
         for (int d = 1; d < D / 8; d *= 2) sum += __shfl_xor(sum, d);
-        const float rstd = inverse_root(sum * (1.0f / D) + r.eps);
+        float rstd;
+        if (__builtin_expect(sum < 0x1p126f && sum + r.eps > 0x1p-90f, 1)) {
+            rstd = inverse_root(sum * (1.0f / D) + r.eps);
+        } else {
+            // squares that leave fp32 (bfloat16 beyond 1e19 or below 1e-14, or all zeros): in 64 bits
+            double squares = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) squares += (double)x[j] * x[j];
+#pragma unroll
+            for (int d = 1; d < D / 8; d *= 2) squares += __shfl_xor(squares, d);
+            rstd = (float)(1.0 / sqrt(squares * (1.0 / D) + (double)r.eps));
+        }
         float w[8];
         load8(weight + 8 * i, w);
 #pragma unroll

@@ -1,7 +1,7 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
 that nobody sees and that hold anything, weights and values far below the largest,
 lengths past the tables and the given maxima, prompts of very many rows, pages that
-are not there."""
+are not there, numbers near the types' ends."""
 
 from __future__ import annotations
 
@@ -358,3 +358,18 @@ def test_evict_gives_nan_for_kept_slots_that_are_not_there(dev, dtype):
                     want = cache.get(b, slot)
                     assert torch.equal(k[first + t, h].double(), want[0][3][h].float().to(dtype).double())
                     assert torch.equal(v[first + t, h].double(), want[1][3][h].float().to(dtype).double())
+
+
+# ---- numbers near the types' ends ----
+
+def test_norm_of_heads_whose_squares_leave_fp32(dev):
+    """bfloat16 numbers from 1e-30 to 3e38: the norm is as good as that of ordinary ones."""
+    x = randn(4, 6, 3, 128)
+    x *= torch.tensor([1.0, 1e19, 1e25, 1e38, 1e-22, 1e-30])[:, None, None] / x.abs().amax(-1, keepdim=True)
+    x = x.to(BF16)
+    w = 1 + 0.1 * randn(1, 128)
+    for eps in (0.0, 1e-6):
+        qo, ko = w4.qk_norm_rope(x.to(dev), x.to(dev), w.to(dev), w.to(dev), eps=eps)
+        want = ref.norm_rope(x, w, None, None, None, False, eps)
+        for y in (qo, ko):
+            assert ((y.cpu().double() - want).abs() <= ref.U[BF16] * want.abs() + 2.0 ** -17 * want.abs().amax(-1, keepdim=True)).all()
