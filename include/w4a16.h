@@ -395,7 +395,8 @@ int w4a16_read_probe(const void *data, int64_t bytes, void *sink, void *stream);
  * 0..15, and stands for m + s c:
  *     m = round(min), s = round((max - min) * (1/15)), c = rint((x - m) * (1/s))
  * in fp32 (both reciprocals rounded to fp32) from the unrounded x (a step below the smallest normal fp32 counts
- * as zero; a group with a value that is not finite is stored as NaN).  Words
+ * as zero; a group with a value that is not finite, or whose s or m the type
+ * does not hold, is stored as NaN).  Words
  * of a tile (lane = 16 b + r with b < 4, r < 16; nibble n):
  *     [D/64][64 lanes][4 words i]  key codes: w = 4 * first + i, slot
  *         16 (w / (D/32)) + r, channel 32 (w mod (D/32)) + 8 b + 2 (n mod 4) + n / 4

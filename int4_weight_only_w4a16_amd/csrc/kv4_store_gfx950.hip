@@ -7,8 +7,8 @@
 //                                             (2i, 2i + 1) when interleaved
 //   m = round(min), s = round((max - min) * (1/15)), c = rint((y - m) * (1/s))
 // per group of g channels, s and m in the activation type, everything else in
-// fp32; the stored value is m + s c.  A group with a value that is not finite
-// is stored as NaN (s = m = NaN).
+// fp32; the stored value is m + s c.  A group with a value that is not finite,
+// or whose s or m is not, is stored as NaN (s = m = NaN).
 //
 // All of it is bound by memory traffic (about 10 flops a channel).  A head is
 // spread over D/8 lanes with eight neighbouring channels each: one 16-byte
@@ -147,12 +147,13 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t (&cod
         hi = fmaxf(hi, __shfl_xor(hi, d));
         bad |= __shfl_xor((int)bad, d) != 0;
     }
-    // bad, or a range past fp32: NaN
-    float s = (hi - lo) * (1.0f / 15.0f), m = lo;
-    if (bad || !(s < __builtin_inff())) s = m = __builtin_nanf("");
-    const uint32_t par = pack2<BF>(s, m);
-    s = par_step<BF>(par);
-    m = par_offset<BF>(par);
+    uint32_t par = pack2<BF>((hi - lo) * (1.0f / 15.0f), lo);
+    float s = par_step<BF>(par), m = par_offset<BF>(par);
+    // a value that is not finite, or a step or offset that the type does not hold: NaN
+    if (bad || !(s < __builtin_inff()) || !(fabsf(m) < __builtin_inff())) {
+        s = m = __builtin_nanf("");
+        par = pack2<BF>(s, m);
+    }
     // a step below the normal range has no reciprocal: the group is its offset
     const float inv = s >= 1.17549435e-38f ? 1.0f / s : 0.0f;
 #pragma unroll

@@ -373,3 +373,25 @@ def test_norm_of_heads_whose_squares_leave_fp32(dev):
         want = ref.norm_rope(x, w, None, None, None, False, eps)
         for y in (qo, ko):
             assert ((y.cpu().double() - want).abs() <= ref.U[BF16] * want.abs() + 2.0 ** -17 * want.abs().amax(-1, keepdim=True)).all()
+
+
+def test_keys_past_the_type_s_end_are_stored_as_nan(dev):
+    """fp16 keys that the norm's weight takes past 65504, and bfloat16 groups wider than fp32 holds:
+    their parameters would be infinite.  Every reader gives NaN for them, and for them alone."""
+    for dtype in (F16, BF16):
+        cache = ref.Cache([40], 1, 64, 32, 32, dtype, seed=1)
+        cache.fill()
+        pages, args = cache.pages(dev), (ints(cache.table, dev), starts([1], dev), ints([40], dev))
+        k = randn(3, 1, 1, 64)
+        weight = torch.ones(64)
+        if dtype == F16:
+            weight[:32] = 1e5
+        else:
+            k[0, 0, 0], k[0, 0, 1] = 3.3e38, -3.3e38
+        v = randn(4, 1, 1, 64).to(dtype).to(dev)
+        w4.kv4_append(pages, k.to(dtype).to(dev), v, *args, 1, k_weight=weight.to(dev) if dtype == F16 else None)
+        rk, rv = w4.kv4_read(pages, *args, 1, 64, dtype)
+        assert torch.isnan(rk[0, 0, :32]).all() and torch.isfinite(rk[0, 0, 32:]).all() and torch.isfinite(rv).all()
+        for G in (1, 200):
+            out = w4.kv4_attention(torch.ones(1, G, 64, dtype=dtype, device=dev), pages, *args, 1, 40)
+            assert torch.isnan(out).all()
