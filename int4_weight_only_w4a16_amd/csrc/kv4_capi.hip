@@ -203,6 +203,7 @@ extern "C" int w4a16_kv4_append(const void *q, int64_t q_stride, const void *k, 
     const RopeIn rope{cos, sin, positions, rot_dim, max_pos, eps};
     st = check_rope(rope, head_dim);
     if (st != W4A16_OK) return st;
+    max_q = max_q < T ? max_q : T;               // (no sequence has more)
     if (!grid_ok(batch * ((max_q + 62) / 32) * kv_heads + T * q_heads / 8 + 1)) return W4A16_ERR_SHAPE;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
         return W4A16_ERR_ALIGN;

@@ -39,3 +39,9 @@ def test_rows_of_a_head_are_32_bits(lib):  # noqa: F811
     assert mass(lib, hq=255, hk=1, qs=255 * 128, max_q=1 << 22) == w4.W4A16_ERR_DEVICE
     for f in (attention, mass):
         assert f(lib, hq=1 << 40) == S and f(lib, hq=-8) == S
+
+
+def test_append_takes_any_bound_on_the_tokens_of_a_sequence(lib):  # noqa: F811
+    """max_q beyond the tokens that there are costs no workgroups: 512 sequences, a bound of 2^28."""
+    assert append(lib, batch=512, max_q=1 << 28) == w4.W4A16_ERR_DEVICE
+    assert append(lib, batch=512, max_q=(1 << 28) + 1) == S
