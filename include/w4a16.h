@@ -421,6 +421,9 @@ int w4a16_read_probe(const void *data, int64_t bytes, void *sink, void *stream);
  * 16-byte aligned (int32 arrays and lse: 4); flags W4A16_X_BF16 (q, k, v, the
  * outputs and the cache's parameters bfloat16, else fp16) and the ones named
  * at each call.  Weights, cos and sin, lse and accumulated weights are fp32.
+ * A launch counts threads in 32 bits: T * (q_heads + kv_heads) * D up to 2^35
+ * (norm and rotation), rows and budget up to 2^29, max_kv of the attention
+ * weights up to 2^30.
  * Every check runs before any HIP call; calls are asynchronous on `stream`,
  * allocate nothing, can be captured into a graph, and give the same bits for
  * the same inputs. */

@@ -118,8 +118,12 @@ int check_queries(const void *q, int64_t q_stride, const void *out, int64_t out_
     return aligned(q, 16) && aligned(out, 16) ? W4A16_OK : W4A16_ERR_ALIGN;
 }
 
-// A launch of `blocks` workgroups in one dimension.
-bool grid_ok(int64_t blocks) { return blocks <= kMax; }
+// A launch of `blocks` workgroups of `threads` in one dimension: it counts threads in 32 bits.
+bool grid_ok(int64_t blocks, int64_t threads) { return blocks * threads <= UINT32_MAX; }
+
+// Workgroups for `rows` rows of heads, eight channels a lane (norm and rotation).
+constexpr int64_t kRowThreads = 256;
+int64_t row_blocks(int64_t rows, int64_t D) { return (rows * (D / 8) + kRowThreads - 1) / kRowThreads; }
 
 int launched(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
 
@@ -170,7 +174,8 @@ extern "C" int w4a16_qk_norm_rope(const void *q, int64_t q_stride, const void *k
         if (T > 0 && !pointers[i]) return W4A16_ERR_NULL;
         if (!aligned(pointers[i], 16)) return W4A16_ERR_ALIGN;
     }
-    if (!in_range(T, 0, 1 << 28) || !grid_ok(T * (q_heads + kv_heads) / 8 + 1)) return W4A16_ERR_SHAPE;
+    if (!in_range(T, 0, 1 << 28) || !grid_ok(row_blocks(T * (q_heads + kv_heads), head_dim), kRowThreads))
+        return W4A16_ERR_SHAPE;
     if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return W4A16_ERR_ALIGN;
     const RopeIn rope{cos, sin, positions, rot_dim, max_pos, eps};
     const int st = check_rope(rope, head_dim);
@@ -204,7 +209,8 @@ extern "C" int w4a16_kv4_append(const void *q, int64_t q_stride, const void *k, 
     st = check_rope(rope, head_dim);
     if (st != W4A16_OK) return st;
     max_q = max_q < T ? max_q : T;               // (no sequence has more)
-    if (!grid_ok(batch * ((max_q + 62) / 32) * kv_heads + T * q_heads / 8 + 1)) return W4A16_ERR_SHAPE;
+    if (!grid_ok(batch * ((max_q + 62) / 32) * kv_heads + row_blocks(T * q_heads, head_dim), kRowThreads))
+        return W4A16_ERR_SHAPE;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
         return W4A16_ERR_ALIGN;
     if (T == 0) return W4A16_OK;
@@ -233,7 +239,7 @@ extern "C" int w4a16_kv4_read(const void *pages, const int32_t *table, const int
     const CacheShape s{kv_heads, head_dim, group_size, page_size, num_pages, batch, table_stride};
     int st = check_cache(s);
     if (st != W4A16_OK) return st;
-    if (!in_range(rows, 0, kMax - 32)) return W4A16_ERR_SHAPE;
+    if (!in_range(rows, 0, kMax - 32) || !grid_ok((rows + 31) / 32, kRowThreads)) return W4A16_ERR_SHAPE;
     if (rows == 0) return W4A16_OK;
     if (!k || !v) return W4A16_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16)) return W4A16_ERR_ALIGN;
@@ -328,7 +334,8 @@ extern "C" int w4a16_kv4_attention_mass(const void *q, int64_t q_stride, const v
     int st = check_attention(s, T, q_heads, max_q, max_kv, window, scale, flags);
     if (st == W4A16_OK) st = check_queries(q, q_stride, q, q_stride, q_heads, kv_heads, head_dim, T);
     if (st != W4A16_OK) return st;
-    if (acc_stride < max_kv) return W4A16_ERR_SHAPE;
+    // (many rows: 128 threads a tile, up to eight tiles a workgroup)
+    if (acc_stride < max_kv || !grid_ok((max_kv + 255) / 256, 1024)) return W4A16_ERR_SHAPE;
     if (!aligned(lse, 4) || !aligned(acc, 4)) return W4A16_ERR_ALIGN;
     if (T == 0 || batch == 0 || max_q == 0 || max_kv == 0) return W4A16_OK;
     if (!lse || !acc) return W4A16_ERR_NULL;
@@ -354,7 +361,8 @@ extern "C" int w4a16_kv4_evict(void *pages, const int32_t *table, const int32_t 
     int st = check_cache(s);
     if (st != W4A16_OK) return st;
     if (!in_range(budget, 1, kMax - 64) || recent < 0 || recent > budget || !in_range(max_kv, 0, kMax - 64) ||
-        acc_stride < max_kv || !in_range(dst_stride, 1, kMax / page_size) || dst_stride * page_size < budget)
+        acc_stride < max_kv || !in_range(dst_stride, 1, kMax / page_size) || dst_stride * page_size < budget ||
+        !grid_ok((budget + 31) / 32, 256))
         return W4A16_ERR_SHAPE;
     if (batch == 0) return W4A16_OK;
     st = check_cache_pointers(pages, table, kv_len, kv_len);

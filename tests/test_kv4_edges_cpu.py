@@ -41,6 +41,24 @@ def test_rows_of_a_head_are_32_bits(lib):  # noqa: F811
         assert f(lib, hq=1 << 40) == S and f(lib, hq=-8) == S
 
 
+# ---- launches count threads in 32 bits ----
+
+def test_launches_of_more_threads_are_refused_before_them(lib):  # noqa: F811
+    taken = w4.W4A16_ERR_DEVICE
+    rope = dict(hq=32, hk=0, qs=4096, qos=4096)
+    assert norm_rope(lib, T=(1 << 23) - 1, **rope) == taken and norm_rope(lib, T=1 << 23, **rope) == S
+    wide = dict(hq=16, hk=0, D=256, rot=64, qs=4096, qos=4096)
+    assert norm_rope(lib, T=(1 << 23) - 1, **wide) == taken and norm_rope(lib, T=1 << 23, **wide) == S
+    # (eight more workgroups for the tiles)
+    assert append(lib, T=(1 << 23) - 5, batch=1, max_q=1, hq=32, qs=4096, qos=4096) == taken
+    assert append(lib, T=1 << 23, batch=1, max_q=1, hq=32, qs=4096, qos=4096) == S
+    assert read(lib, rows=(1 << 29) - 32) == taken and read(lib, rows=1 << 29) == S
+    long = dict(acc_stride=1 << 31)
+    assert mass(lib, max_kv=(1 << 30) - 256, **long) == taken and mass(lib, max_kv=1 << 30, **long) == S
+    pages = dict(dst_stride=1 << 24, recent=0)
+    assert evict(lib, budget=(1 << 29) - 32, **pages) == taken and evict(lib, budget=1 << 29, **pages) == S
+
+
 def test_append_takes_any_bound_on_the_tokens_of_a_sequence(lib):  # noqa: F811
     """max_q beyond the tokens that there are costs no workgroups: 512 sequences, a bound of 2^28."""
     assert append(lib, batch=512, max_q=1 << 28) == w4.W4A16_ERR_DEVICE
