@@ -63,6 +63,8 @@ class AttentionBlock:
         """x [sum(counts), hidden]: counts[b] new tokens of each sequence, in order."""
         if max(n + c for n, c in zip(self.lengths, counts)) > self.budget + self.room:
             raise ValueError("more tokens than the cache has room for: call evict() in between")
+        if max(p + c for p, c in zip(self.positions, counts)) > self.cos.shape[0]:
+            raise ValueError("a sequence is longer than the rotation's tables")
         dev, D = x.device, self.head_dim
         new = torch.tensor(counts, dtype=torch.int32, device=dev)
         cu = torch.zeros(len(counts) + 1, dtype=torch.int32, device=dev)

@@ -63,3 +63,23 @@ def test_append_takes_any_bound_on_the_tokens_of_a_sequence(lib):  # noqa: F811
     """max_q beyond the tokens that there are costs no workgroups: 512 sequences, a bound of 2^28."""
     assert append(lib, batch=512, max_q=1 << 28) == w4.W4A16_ERR_DEVICE
     assert append(lib, batch=512, max_q=(1 << 28) + 1) == S
+
+
+# ---- the example ----
+
+def test_example_refuses_positions_past_its_tables():
+    """Evictions keep a cache small for any number of tokens; the rotation's tables end."""
+    import importlib.util
+    import os
+
+    import torch
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_block.py")
+    spec = importlib.util.spec_from_file_location("attention_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    block = example.AttentionBlock(hidden=128, q_heads=2, kv_heads=1, head_dim=64, group=32, page=32, batch=2, budget=64,
+                                   recent=16, room=64, device="cpu")
+    block.positions, block.lengths = [100, (1 << 14) - 2], [64, 64]
+    with pytest.raises(ValueError, match="tables"):
+        block(torch.zeros(4, 128, dtype=torch.bfloat16), [1, 3])
+    assert block.positions == [100, (1 << 14) - 2] and block.kv_len.tolist() == [0, 0]
