@@ -1,7 +1,8 @@
 """The 4-bit cache's operators where a call leaves the ordinary: buffers that do not fit, slots
 that nobody sees and that hold anything, weights and values far below the largest,
 lengths past the tables and the given maxima, prompts of very many rows, pages that
-are not there, numbers near the types' ends."""
+are not there, numbers near the types' ends; and the paths that only long sequences
+take."""
 
 from __future__ import annotations
 
@@ -395,3 +396,58 @@ def test_keys_past_the_type_s_end_are_stored_as_nan(dev):
         for G in (1, 200):
             out = w4.kv4_attention(torch.ones(1, G, 64, dtype=dtype, device=dev), pages, *args, 1, 40)
             assert torch.isnan(out).all()
+
+
+# ---- slots split over workgroups, windows over several of them, many pages ----
+
+@pytest.mark.parametrize("dtype,D,group,hq,hk,ns,lens,page,window", [
+    # few rows: several chunks with 256 channels, and windows that begin inside one
+    (F16, 256, 32, 2, 1, [1], [3001], 32, 0),
+    (BF16, 256, 128, 3, 1, [2, 1], [2777, 1500], 96, 0),
+    (BF16, 128, 64, 5, 1, [3], [4099], 64, 1001),
+    (F16, 128, 32, 10, 2, [1, 4], [5000, 2345], 32, 1500),
+    (F16, 256, 64, 1, 1, [1], [4001], 64, 999),
+    (BF16, 64, 32, 30, 1, [4], [3333], 32, 1111),
+    # many rows: parts with 128 and 256 channels, and windows over several
+    (BF16, 128, 64, 2, 1, [110], [3210], 64, 0),
+    (F16, 128, 32, 4, 1, [60, 7], [2500, 2100], 32, 0),
+    (BF16, 128, 128, 2, 1, [130], [4000], 128, 1700),
+    (F16, 256, 32, 2, 1, [120], [2600], 64, 0),
+    (BF16, 256, 64, 1, 1, [200, 100], [2222, 1999], 32, 1400),
+    (F16, 64, 64, 3, 1, [150], [5000], 32, 2500),
+])
+def test_split_slots_and_windows(dev, dtype, D, group, hq, hk, ns, lens, page, window):
+    cache = ref.Cache(lens, hk, D, group, page, dtype, seed=D + hq)
+    cache.fill()
+    q = (1.5 * randn(8, sum(ns), hq, D)).to(dtype)
+    args = (cache.pages(dev), ints(cache.table, dev), starts(ns, dev), ints(lens, dev))
+    out, lse = w4.kv4_attention(q.to(dev), *args, max(ns), max(lens), window=window, return_lse=True)
+    o, l, rough, mag, size, acc = by_definition(cache, q, ns, lens, lens, D ** -0.5, True, window, max(ns))
+    e, u = E_LOGIT * size.clamp(min=1.0), ref.U[dtype]
+    assert ((out.cpu().double() - o).abs() <= 1.01 * u * o.abs() + 1.1 * u * rough + 2.2 * e[..., None] * mag + 2.0 ** -24).all()
+    assert ((lse.cpu().double() - l).abs() <= e).all()
+    before = torch.rand(len(ns), hk, max(lens))
+    got = w4.kv4_attention_mass(q.to(dev), *args, lse, before.to(dev), max(ns), max(lens), window=window).cpu().double()
+    e = 4 * E_LOGIT * max(1.0, float(size.max()))
+    for b, add in enumerate(acc):
+        want = before[b, :, :lens[b]].double() + add
+        assert ((got[b, :, :lens[b]] - want).abs() <= e * add + 2.0 ** -22 * want).all()
+        assert torch.equal(got[b, :, lens[b]:], before[b, :, lens[b]:].double())
+
+
+@pytest.mark.parametrize("dtype,D,group,page", [(BF16, 128, 64, 32), (F16, 64, 32, 32), (F16, 256, 128, 64)])
+def test_many_rows_in_one_part_over_more_than_64_pages(dev, dtype, D, group, page):
+    """512 sequences on the same pages, so that one workgroup walks over all of them: the page ids
+    that a wave holds are loaded again on the way, twice for the longest."""
+    lens, copies, G = [page * 140 + 5], 512, 200
+    cache = ref.Cache(lens, 1, D, group, page, dtype, seed=5)
+    cache.fill()
+    q = (1.5 * randn(6, 1, G, D)).to(dtype)
+    out, lse = w4.kv4_attention(q.expand(copies, -1, -1).contiguous().to(dev), cache.pages(dev),
+                                ints(np.repeat(cache.table, copies, 0), dev), starts([1] * copies, dev),
+                                ints(lens * copies, dev), 1, lens[0], return_lse=True)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    o, l, rough, mag, size, _ = by_definition(cache, q, [1], lens, lens, D ** -0.5, True, 0, 1)
+    e, u = E_LOGIT * size.clamp(min=1.0), ref.U[dtype]
+    assert ((out[:1].cpu().double() - o).abs() <= 1.01 * u * o.abs() + 1.1 * u * rough + 2.2 * e[..., None] * mag + 2.0 ** -24).all()
+    assert ((lse[:1].cpu().double() - l).abs() <= e).all()
