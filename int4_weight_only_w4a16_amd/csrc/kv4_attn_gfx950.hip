@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads)
     // Offsets of the values: with one group 24 operations in every lane, with more a matrix
     // product whose rows are the groups (about 36, whatever the number of groups).
     constexpr bool kMidRows = NG > 1;
+    constexpr int kShare = NG > 1 ? NG / 2 : 1;       // of a tile's 32 NG value parameters, a lane's share
     __shared__ __align__(16) uint8_t lds_raw[Shape::kLds];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
@@ -286,13 +287,12 @@ __global__ void __launch_bounds__(kThreads)
         // whether some row does not see some of the tile's slots; the same in every lane
         const bool masked = 32 * tile < all_lo || 32 * tile + 32 > all_hi;
         const lds_u8 *params = at + 2 * T::kCodes + 16 * b4;
-        // parameters of the values: eight slots of one group, group r in the lanes of column r
-        const lds_u8 *mine = params + 128 * (NG + (r < NG ? r : NG - 1));
-        uint32_t steps = 0;                      // fp16: the largest step of those, as bits
+        // fp16: the largest step of the values, as bits, of the tile's parameters that fall to this lane
+        uint32_t steps = 0;
         if constexpr (!BF) {
-            const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
+            const lds_u8 *all = at + 2 * T::kCodes + 128 * NG + 4 * kShare * (NG > 1 ? lane : lane & 31);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) steps = max_halves(max_halves(steps, p0[e]), p1[e]);
+            for (int i = 0; i < kShare; ++i) steps = max_halves(steps, lds_get<uint32_t>(all + 4 * i));
             steps &= 0xFFFFu;
         }
         float x[NT][8];
@@ -362,10 +362,11 @@ __global__ void __launch_bounds__(kThreads)
             top[t] = BF ? m * c1 : __builtin_fmaf(m, c1, -lift[t]);
             move |= top[t] > ref[t] + kSlack;
         }
-        if constexpr (!BF) move |= steps > step_limit;
-        if (__builtin_amdgcn_ballot_w64(move)) {
-            float met[NT];
-            if constexpr (!BF) {
+        const bool wide = !BF && __builtin_amdgcn_ballot_w64(steps > step_limit);
+        if (__builtin_amdgcn_ballot_w64(move) || wide) {
+            float by[NT] = {};                   // what each row's lift goes down by
+            if (wide) {
+                float met[NT];
                 if (!masked) {                   // (neither infinities nor NaN)
                     const float all = lo_f32<BF>(max_lanes(steps < 0x7C00u ? steps : 0u));
 #pragma unroll
@@ -389,20 +390,23 @@ __global__ void __launch_bounds__(kThreads)
                         met[t] = fmaxf(met[t], __shfl_xor(met[t], 32));
                     }
                 }
+                float highest = 0.f;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {   // a step in [2^(e - 1), 2^e): lift at most 14 - e, at least 0
+                    const float to = fmaxf(fminf(lift[t], (float)(14 - __builtin_amdgcn_frexp_expf(met[t]))), 0.f);
+                    by[t] = lift[t] - to;
+                    lift[t] = to;
+                    highest = fmaxf(highest, to);
+                }
+                step_limit = (29u - (uint32_t)__uint_as_float(max_lanes(__float_as_uint(highest)))) * 1024 - 1;
             }
-            float highest = 0.f;                 // the largest lift
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float m = fmaxf(top[t], __shfl_xor(top[t], 16));
                 m = fmaxf(m, __shfl_xor(m, 32));
                 // (an infinite maximum stays out of the reference: its weight becomes infinite)
                 m = fmaxf(ref[t], fminf(m, 3e38f));
-                if constexpr (!BF) {             // a step in [2^(e - 1), 2^e): lift at most 14 - e, at least 0
-                    const float to = fmaxf(fminf(lift[t], (float)(14 - __builtin_amdgcn_frexp_expf(met[t]))), 0.f);
-                    m += lift[t] - to;
-                    lift[t] = to;
-                    highest = fmaxf(highest, to);
-                }
+                if constexpr (!BF) m += by[t];
                 const float f = __builtin_amdgcn_exp2f(ref[t] - m);
                 ref[t] = m;
                 sum[t] *= f;
@@ -412,7 +416,6 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int o = 0; o < kOut; ++o) out[t][o] *= f;
             }
-            if constexpr (!BF) step_limit = (29u - (uint32_t)__uint_as_float(max_lanes(__float_as_uint(highest)))) * 1024 - 1;
         }
         // weights, and their products with the values' steps as matrix operands
         u4 pr[NT];
@@ -430,6 +433,7 @@ __global__ void __launch_bounds__(kThreads)
         if constexpr (kMidRows) {
             // sum_t p_t (m_t + 8 s_t) of all groups in two matrix products, row g of the first
             // operand holding group g: the rounded p_t with the middles in two parts
+            const lds_u8 *mine = at + 2 * T::kCodes + 128 * (NG + (r < NG ? r : NG - 1)) + 16 * b4;
             const u4 p0 = lds_get<u4>(mine), p1 = lds_get<u4>(mine + 64);
             u4 high, low;
 #pragma unroll

@@ -398,6 +398,26 @@ def test_keys_past_the_type_s_end_are_stored_as_nan(dev):
             assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("hq,n", [(1, 1), (5, 6), (20, 1), (50, 6)])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32)])
+def test_attention_of_values_that_grow(dev, dtype, hq, n, D, group):
+    """Values from 1 to thousands, slot after slot, the new tokens' own the largest: steps beyond 2 in
+    every tile, and rows that do not see the last ones."""
+    lens = [190]
+    cache = ref.Cache(lens, 1, D, group, 64, dtype, seed=2)
+    k, v = randn(3, 190, 1, D), randn(4, 190, 1, D) * 2.0 ** (torch.arange(190) / 15.0)[:, None, None]
+    for t in range(190):
+        cache.put(0, t, k[t], v[t])
+    q = (1.5 * randn(5, n, hq, D)).to(dtype)
+    args = (cache.pages(dev), ints(cache.table, dev), starts([n], dev), ints(lens, dev))
+    out, lse = w4.kv4_attention(q.to(dev), *args, n, 190, return_lse=True)
+    o, l, rough, mag, size, _ = by_definition(cache, q, [n], lens, lens, D ** -0.5, True, 0, n)
+    e, u = E_LOGIT * size.clamp(min=1.0), ref.U[dtype]
+    assert ((out.cpu().double() - o).abs() <= 1.01 * u * o.abs() + 1.1 * u * rough + 2.2 * e[..., None] * mag).all()
+    assert ((lse.cpu().double() - l).abs() <= e).all()
+
+
 # ---- slots split over workgroups, windows over several of them, many pages ----
 
 @pytest.mark.parametrize("dtype,D,group,hq,hk,ns,lens,page,window", [
