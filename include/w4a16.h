@@ -487,7 +487,9 @@ int w4a16_kv4_read(const void *pages, const int32_t *table, const int32_t *cu_se
  *   lse : [T, q_heads] log of the sum of exp(scale q . k), or null
  *   max_q, max_kv : at least the most new tokens and slots of any sequence
  *   (the work is laid out for them: outputs of further tokens are not written,
- *   further slots are not seen, and neither moves a token to another slot)
+ *   further slots are not seen, and neither moves a token to another slot);
+ *   where q_heads / kv_heads * max_q is above 192 all sequences go to a kernel
+ *   for many rows, so that a prompt and single tokens are faster in two calls
  *   scale : finite and positive
  *   q_heads * max_q : up to about 16.7 million (8.3 with 256 channels; rows of
  *   a head are counted in tiles of 256, or 128, of which there may be 65535)

@@ -15,9 +15,10 @@
 // and m + 8 s is held between the type's ends (a group with a NaN has it in
 // both parameters, so that a slot with weight still gives NaN).
 // Bound by memory while the rows are few, then by the vector ALUs (unpacking and weights): one
-// token, 40 heads on 8, 131071 slots 30 us (4.7 TB/s of 5.2) and 4.4 for the join of chunks; 32
-// sequences of 1000 to 24000 slots 115 us (4.4 TB/s) and 5.6; 64 rows instead of 4 over 32
-// sequences of 4000 slots 104 us instead of 36.  A wave's tile comes while the one before is
+// token, 40 heads on 8, 131071 slots 30 us (4.7 TB/s of 5.2) and 4.6 for the join of chunks; 32
+// sequences of 1000 to 24000 slots in groups of 32 119 us with a join of 5.6 (a call among others;
+// the kernel by itself between pauses 125); 64 rows instead of 4 over 32 sequences of 4000 slots
+// 104 us instead of 36.  A wave's tile comes while the one before is
 // worked on; a third under way is slower (LDS for fewer waves: 9.1 -> 9.7 us at 2000 slots).
 // ref is a running reference per row, moved only when a tile's maximum
 // passes it by more than kSlack, and lies `lift` below the maximum: p_t stays
@@ -81,6 +82,10 @@ constexpr int kFewSlots = 512, kManySlots = 1024, kFewSequences = 4;
 //   1 sequence of 100000 slots   65 and 176   138 and 183  177 and 189  233 and 201  325 and 339
 //   8 of 4000                    43 and  76    63 and  88   83 and  97  105 and 107  152 and 167
 //   32 of 4000                  104 and 239   196 and 268  288 and 296  378 and 325  562 and 420
+// With 64 channels both meet near there too: at 192 rows 135 and 133, 68 and 70, 232 and 160; at
+// 128 rows 107 and 131, 52 and 63, 160 and 159.  With 256 the kernel for many rows gains less (its
+// tiles have 128 rows): at 192 rows 418 and 636, 150 and 238, 562 and 806; at 256 rows 551 and 638,
+// 195 and 243, 743 and 808.
 constexpr int kFewRows = 192;
 int rows_of(const Kv4AttnArgs &a) { return a.q_heads / a.c.kv_heads * a.max_q; }
 

@@ -15,9 +15,9 @@
 // load, the sum of squares and the group's extremes by shuffles within those
 // lanes, and a lane's eight codes are exactly one key word of the cache.
 // Measured (fp16 or bfloat16): norm and rotation of the 170 MB of a prompt in and
-// out 39 us (4.3 TB/s; a copy reaches 5.2), of one token 2.9; into the cache one
-// token of each of 64 sequences 6.3 us (a chain of four loads), three chunks of
-// prompts 24.8 and their rows back 10.7 (95 MB together, 2.7 TB/s).
+// out 40 us (4.3 TB/s; a copy reaches 5.2), of one token 2.9; into the cache one
+// token of each of 64 sequences 6.5 us (a chain of four loads), three chunks of
+// prompts 25.2 and their rows back 10.9 (95 MB together, 2.6 TB/s).
 
 #include "kv4_device.hpp"
 
