@@ -518,6 +518,33 @@ size_t w4a16_kv4_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64
                                            int64_t head_dim, int64_t max_q, int64_t max_kv,
                                            int64_t window);
 
+/* w4a16_kv4_attention for new tokens that are a tree of drafts, several
+ * continuations that are checked in one call.  Their keys and values are in
+ * the cache's last slots, token i of the n of a sequence in slot len - n + i as
+ * there (w4a16_kv4_append; the rotation by each token's depth).  Token i sees
+ * the slots before the new tokens', its own and those of the earlier new tokens
+ * that its word names:
+ *   tree : int64 [T], bit j of a token's word: it descends from token j of its
+ *     sequence's new ones (j < i; bits from i on mean nothing).  A token comes
+ *     after those that it descends from; with bits 0 .. i - 1 set everywhere it is
+ *     w4a16_kv4_attention (fp16: up to the rounding of the weights).
+ *   max_q : at most W4A16_TREE_MAX
+ *   window : 0, or at least W4A16_TREE_MAX; a token of depth d (how many it
+ *     descends from) stands at slot len - n + d for it, and its path is in it.
+ * Everything else, the workspace too, as for w4a16_kv4_attention (no
+ * W4A16_NONCAUSAL).  To keep the accepted path, append its tokens' keys and
+ * values again over the drafts' slots, with kv_len as it then is. */
+#define W4A16_TREE_MAX 64
+int w4a16_kv4_tree_attention(const void *q, int64_t q_stride, const void *pages,
+                             const int32_t *table, const int32_t *cu_seqlens,
+                             const int32_t *kv_len, const int64_t *tree, void *out,
+                             int64_t out_stride, float *lse, int64_t T, int64_t q_heads,
+                             int64_t kv_heads, int64_t head_dim, int64_t group_size,
+                             int64_t page_size, int64_t num_pages, int64_t batch,
+                             int64_t table_stride, int64_t max_q, int64_t max_kv, float scale,
+                             int64_t window, unsigned flags, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* acc[b][h][t] += sum of exp(scale q . k_t - lse) over the new tokens of
  * sequence b that see slot t and the query heads of key/value head h: the
  * attention weight that slot t got.  q, lse, scale, window and flags as the

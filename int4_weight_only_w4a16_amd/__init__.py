@@ -63,7 +63,7 @@ EXPORTS = ("w4a16_linear", "w4a16_linear_noalloc", "w4a16_linear_ex", "w4a16_lin
            "pack_gptq_v2", "unpack_gptq_v2",
            "w4a16_read_probe", "w4a16_kv4_page_bytes", "w4a16_qk_norm_rope", "w4a16_kv4_append",
            "w4a16_kv4_read", "w4a16_kv4_attention", "w4a16_kv4_attention_workspace_bytes",
-           "w4a16_kv4_attention_mass", "w4a16_kv4_evict", "w4a16_status_string")
+           "w4a16_kv4_tree_attention", "w4a16_kv4_attention_mass", "w4a16_kv4_evict", "w4a16_status_string")
 
 _lib: Optional[ctypes.CDLL] = None
 

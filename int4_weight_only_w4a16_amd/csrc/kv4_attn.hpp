@@ -52,11 +52,25 @@ __device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int 
     w->rows = w->n * G;
     if (row0 >= w->rows) return false;
     const int last = min(row0 + rows_per, w->rows) - 1;
-    const int lo = row_lo(row0 / G, w->start, a.window);
+    // (in a tree a later token may lie less deep and see earlier slots)
+    const int lo = row_lo(a.tree ? 0 : row0 / G, w->start, a.window);
     const int hi = row_hi(last / G, w->start, w->len, a.causal);
     w->t0 = lo >> 5;
     w->t1 = hi > lo ? (hi + 31) >> 5 : w->t0;
     return true;
+}
+
+// What drafted token i of a tree sees of the new tokens: bit j for token j, the earlier ones that it
+// descends from and its own.  (Bits from i on that the word may hold mean nothing.)
+__device__ __forceinline__ uint64_t kin_of(uint64_t word, int i) { return (word & ((1ull << i) - 1)) | 1ull << i; }
+
+// Bit s: a row with the bounds [lo, hi) sees slot first + s of a tile's 32; `start` is the slot of the
+// first new token, and hi at most 64 after it.
+__device__ __forceinline__ uint32_t seen_bits(uint64_t kin, int lo, int hi, int start, int first) {
+    const int from = min(max(lo - first, 0), 32), to = min(max(hi - first, from), 32);
+    const int before = min(max(start - first, 0), 32), past = min(max(first - start, 0), 63);
+    const uint32_t in_tree = (uint32_t)((1ull << before) - 1) | (uint32_t)((kin >> past) << before);
+    return (uint32_t)((1ull << to) - (1ull << from)) & in_tree;
 }
 
 // Tiles of a workgroup that walks over one of about `want` equal parts of `tiles`, a whole number

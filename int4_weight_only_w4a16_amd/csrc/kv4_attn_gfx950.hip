@@ -157,7 +157,9 @@ struct AttendShape {
     static constexpr int kLds = kStats + 2 * kWaves * kRows * 4;
 };
 
-template <bool BF, int D, int NG, int NT>
+// TREE: the new tokens are a tree of drafts (up to 64): a row sees the slots before them and those
+// that its token's word names.
+template <bool BF, int D, int NG, int NT, bool TREE>
 __global__ void __launch_bounds__(kThreads)
     __attribute__((amdgpu_waves_per_eu(NT * D <= 128 ? 3 : 2, NT * D <= 128 ? 3 : 2))) attend_kernel(Kv4AttnArgs a, Plan plan) {
     using T = Tile<D, NG>;
@@ -220,13 +222,19 @@ __global__ void __launch_bounds__(kThreads)
     float qsum[NT][NG];
     f4 init[NT][NG];                          // -B sum(q_g)
     int lo[NT], hi[NT];
-    int all_lo = 0, all_hi = 0x7fffffff;
+    uint64_t kin[TREE ? NT : 1];
+    int all_lo = 0, all_hi = TREE ? w.start : 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int row = w.row0 + 16 * t + r;
         const bool in_seq = row < w.rows;
         const int i = in_seq ? row / G : 0;
-        lo[t] = in_seq ? row_lo(i, w.start, a.window) : 0;
+        int depth = i;
+        if constexpr (TREE) {
+            kin[t] = in_seq ? kin_of(a.tree[w.first + i], i) : 0;
+            depth = __popcll(kin[t]) - 1;
+        }
+        lo[t] = in_seq ? row_lo(depth, w.start, a.window) : 0;
         hi[t] = in_seq ? row_hi(i, w.start, w.len, a.causal) : 0;
         if (in_seq) {
             all_lo = max(all_lo, lo[t]);
@@ -288,6 +296,10 @@ __global__ void __launch_bounds__(kThreads)
         for (int o = 0; o < kOut; ++o) out[t][o] = f4{0.f, 0.f, 0.f, 0.f};
     }
 
+    // (of a tile's 32 slots this lane's eight are 16 (e / 4) + 4 b4 + e % 4)
+    auto tree_bits = [&](int t, int tile) {
+        return seen_bits(kin[TREE ? t : 0], lo[t], hi[t], w.start, 32 * tile) >> (4 * b4);
+    };
     auto step = [&](int tile, const lds_u8 *at) {
         // whether some row does not see some of the tile's slots; the same in every lane
         const bool masked = 32 * tile < all_lo || 32 * tile + 32 > all_hi;
@@ -350,12 +362,20 @@ __global__ void __launch_bounds__(kThreads)
         if (masked) {
             asm volatile("");                    // (a branch, not sixteen selects in every tile)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                if constexpr (TREE) {
+                    const uint32_t bits = tree_bits(t, tile);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[t][e] = bits >> (16 * (e >> 2) + (e & 3)) & 1 ? x[t][e] : -__builtin_inff();
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int slot = 32 * tile + 16 * (e >> 2) + 4 * b4 + (e & 3);
                     if (!((slot >= lo[t]) & (slot < hi[t]))) x[t][e] = -__builtin_inff();
                 }
+            }
         }
         float top[NT];
         bool move = false;
@@ -368,7 +388,8 @@ __global__ void __launch_bounds__(kThreads)
             move |= top[t] > ref[t] + kSlack;
         }
         const bool wide = !BF && __builtin_amdgcn_ballot_w64(steps > step_limit);
-        if (__builtin_amdgcn_ballot_w64(move) || wide) {
+        const bool moves = __builtin_amdgcn_ballot_w64(move);
+        if (moves || wide) {
             float by[NT] = {};                   // what each row's lift goes down by
             if (wide) {
                 float met[NT];
@@ -386,8 +407,11 @@ __global__ void __launch_bounds__(kThreads)
                                 lds_get<uint32_t>(params + 128 * (NG + g) + 64 * (e >> 2) + 4 * (e & 3)));
                             const int slot = 32 * tile + 16 * (e >> 2) + 4 * b4 + (e & 3);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                if ((slot >= lo[t]) & (slot < hi[t]) & (s < __builtin_inff())) met[t] = fmaxf(met[t], s);
+                            for (int t = 0; t < NT; ++t) {
+                                bool seen = (slot >= lo[t]) & (slot < hi[t]);
+                                if constexpr (TREE) seen = tree_bits(t, tile) >> (16 * (e >> 2) + (e & 3)) & 1;
+                                if (seen & (s < __builtin_inff())) met[t] = fmaxf(met[t], s);
+                            }
                         }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
@@ -411,6 +435,8 @@ __global__ void __launch_bounds__(kThreads)
                 m = fmaxf(m, __shfl_xor(m, 32));
                 // (an infinite maximum stays out of the reference: its weight becomes infinite)
                 m = fmaxf(ref[t], fminf(m, 3e38f));
+                // (steps that a row does not see leave its last bits as they are)
+                if (TREE && !moves) m = ref[t];
                 if constexpr (!BF) m += by[t];
                 const float f = __builtin_amdgcn_exp2f(ref[t] - m);
                 ref[t] = m;
@@ -673,10 +699,17 @@ hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
         if (rows_of(a) > kFewRows) {
             const hipError_t e = launch_kv4_prefill(a, p, stream);
             if (e != hipSuccess) return e;
-        } else if (p.rows == 16)
-            attend_kernel<bf(), d(), ng(), 1><<<grid, kThreads, 0, stream>>>(a, p);
-        else if constexpr (d() <= 128)
-            attend_kernel<bf(), d(), ng(), 2><<<grid, kThreads, 0, stream>>>(a, p);
+        } else if (p.rows == 16) {
+            if (a.tree)
+                attend_kernel<bf(), d(), ng(), 1, true><<<grid, kThreads, 0, stream>>>(a, p);
+            else
+                attend_kernel<bf(), d(), ng(), 1, false><<<grid, kThreads, 0, stream>>>(a, p);
+        } else if constexpr (d() <= 128) {
+            if (a.tree)
+                attend_kernel<bf(), d(), ng(), 2, true><<<grid, kThreads, 0, stream>>>(a, p);
+            else
+                attend_kernel<bf(), d(), ng(), 2, false><<<grid, kThreads, 0, stream>>>(a, p);
+        }
         hipError_t e = hipGetLastError();
         if (e == hipSuccess && p.chunks > 1) {
             join_kernel<bf(), d()><<<dim3(std::min(p.rows, rows_of(a)), grid.y, grid.z), kJoin, 0, stream>>>(a, p);

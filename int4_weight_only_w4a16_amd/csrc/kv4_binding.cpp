@@ -222,10 +222,11 @@ float scale_of(std::optional<double> scale, int64_t D) {
     return (float)(scale ? *scale : 1.0 / std::sqrt((double)D));
 }
 
-py::object kv4_attention(const Tensor &q, const Tensor &pages, const Tensor &block_table, const Tensor &cu_seqlens,
-                         const Tensor &kv_len, int64_t max_q, int64_t max_kv, std::optional<double> scale,
-                         bool causal, int64_t window, const MaybeTensor &out, bool return_lse,
-                         const MaybeTensor &lse, const MaybeTensor &workspace, const py::object &stream) {
+// Attention of tokens in a row, or of a tree.
+py::object attend(const Tensor &q, const Tensor &pages, const Tensor &block_table, const Tensor &cu_seqlens,
+                  const Tensor &kv_len, const Tensor *tree, int64_t max_q, int64_t max_kv,
+                  std::optional<double> scale, bool causal, int64_t window, const MaybeTensor &out, bool return_lse,
+                  const MaybeTensor &lse, const MaybeTensor &workspace, const py::object &stream) {
     const int64_t qs = heads_stride("q", q);
     const Geometry g = attention_geometry(q, pages);
     const Sequences s = sequences_of(pages, block_table, &cu_seqlens, kv_len);
@@ -243,12 +244,40 @@ py::object kv4_attention(const Tensor &q, const Tensor &pages, const Tensor &blo
         plain("workspace", ws, ws.scalar_type(), pages.device());     // (any type: bytes are what counts)
     } else if (need)
         ws = at::empty({(int64_t)need}, pages.options());
-    check(w4a16_kv4_attention(q.data_ptr(), qs, pages.data_ptr(), s.table, s.cu, s.kv_len, o.data_ptr(),
-                              heads_stride("out", o, &q), lse_ptr, T, hq, g.heads, D, g.group, g.page, g.pages,
-                              s.batch, s.stride, max_q, max_kv, scale_of(scale, D), window, flags,
-                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, on.stream()),
-          "w4a16_kv4_attention");
+    const int64_t os = heads_stride("out", o, &q);
+    void *ws_ptr = ws.defined() ? ws.data_ptr() : nullptr;
+    const size_t ws_bytes = ws.defined() ? ws.nbytes() : 0;
+    if (tree) {
+        const auto *words = static_cast<int64_t *>(plain("tree", *tree, at::kLong, q.device(), {T}));
+        check(w4a16_kv4_tree_attention(q.data_ptr(), qs, pages.data_ptr(), s.table, s.cu, s.kv_len, words,
+                                       o.data_ptr(), os, lse_ptr, T, hq, g.heads, D, g.group, g.page, g.pages,
+                                       s.batch, s.stride, max_q, max_kv, scale_of(scale, D), window, flags, ws_ptr,
+                                       ws_bytes, on.stream()),
+              "w4a16_kv4_tree_attention");
+    } else {
+        check(w4a16_kv4_attention(q.data_ptr(), qs, pages.data_ptr(), s.table, s.cu, s.kv_len, o.data_ptr(), os,
+                                  lse_ptr, T, hq, g.heads, D, g.group, g.page, g.pages, s.batch, s.stride, max_q,
+                                  max_kv, scale_of(scale, D), window, flags, ws_ptr, ws_bytes, on.stream()),
+              "w4a16_kv4_attention");
+    }
     return return_lse ? py::cast(std::make_tuple(o, *l)) : py::cast(o);
+}
+
+py::object kv4_attention(const Tensor &q, const Tensor &pages, const Tensor &block_table, const Tensor &cu_seqlens,
+                         const Tensor &kv_len, int64_t max_q, int64_t max_kv, std::optional<double> scale,
+                         bool causal, int64_t window, const MaybeTensor &out, bool return_lse,
+                         const MaybeTensor &lse, const MaybeTensor &workspace, const py::object &stream) {
+    return attend(q, pages, block_table, cu_seqlens, kv_len, nullptr, max_q, max_kv, scale, causal, window, out,
+                  return_lse, lse, workspace, stream);
+}
+
+py::object kv4_tree_attention(const Tensor &q, const Tensor &pages, const Tensor &block_table,
+                              const Tensor &cu_seqlens, const Tensor &kv_len, const Tensor &tree, int64_t max_q,
+                              int64_t max_kv, std::optional<double> scale, int64_t window, const MaybeTensor &out,
+                              bool return_lse, const MaybeTensor &lse, const MaybeTensor &workspace,
+                              const py::object &stream) {
+    return attend(q, pages, block_table, cu_seqlens, kv_len, &tree, max_q, max_kv, scale, true, window, out,
+                  return_lse, lse, workspace, stream);
 }
 
 float *weights_of(const Tensor &acc, const at::Device &device, int64_t batch, int64_t heads) {
@@ -332,6 +361,14 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
           "last ones); one that sees none gets zeros.  max_q, max_kv: at least the most new tokens and slots of\n"
           "any sequence.  Returns out, or (out, lse) with return_lse (lse fp32 [T, q_heads], -inf where nothing\n"
           "is seen).");
+    m.def("kv4_tree_attention", &kv4_tree_attention, py::arg("q"), py::arg("pages"), py::arg("block_table"),
+          py::arg("cu_seqlens"), py::arg("kv_len"), py::arg("tree"), py::arg("max_q"), py::arg("max_kv"),
+          py::arg("scale") = none, py::arg("window") = 0, py::arg("out") = none, py::arg("return_lse") = false,
+          py::arg("lse") = none, py::arg("workspace") = none, py::arg("stream") = none,
+          "kv4_attention for new tokens that are a tree of drafts, up to 64 a sequence: bit j of a token's word in\n"
+          "tree (int64 [T]) says that it descends from its sequence's new token j, an earlier one.  A token sees the\n"
+          "slots before the new ones, those of the tokens that it descends from, and its own.  window: 0, or at\n"
+          "least 64, counted along a token's path.");
     m.def("kv4_attention_mass", &kv4_attention_mass, py::arg("q"), py::arg("pages"), py::arg("block_table"),
           py::arg("cu_seqlens"), py::arg("kv_len"), py::arg("lse"), py::arg("acc"), py::arg("max_q"),
           py::arg("max_kv"), py::arg("scale") = none, py::arg("causal") = true, py::arg("window") = 0,

@@ -281,23 +281,30 @@ static bool attention_fits(const w4a16::Kv4AttnArgs &a) {
     return a.c.kv_heads * w4a16::kv4_attention_row_tiles(a) <= 65535;
 }
 
-extern "C" int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
-                                   const int32_t *cu_seqlens, const int32_t *kv_len, void *out, int64_t out_stride,
-                                   float *lse, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                                   int64_t group_size, int64_t page_size, int64_t num_pages, int64_t batch,
-                                   int64_t table_stride, int64_t max_q, int64_t max_kv, float scale, int64_t window,
-                                   unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
-    const CacheShape s{kv_heads, head_dim, group_size, page_size, num_pages, batch, table_stride};
+// Attention of tokens in a row, or with `is_tree` of a tree.
+static int attend(const CacheShape &s, const void *q, int64_t q_stride, const void *pages, const int32_t *table,
+                  const int32_t *cu_seqlens, const int32_t *kv_len, bool is_tree, const int64_t *tree, void *out,
+                  int64_t out_stride, float *lse, int64_t T, int64_t q_heads, int64_t max_q, int64_t max_kv,
+                  float scale, int64_t window, unsigned flags, void *workspace, size_t workspace_bytes,
+                  void *stream) {
+    const int64_t kv_heads = s.kv_heads, head_dim = s.head_dim, batch = s.batch;
     int st = check_attention(s, T, q_heads, max_q, max_kv, window, scale, flags);
+    if (st == W4A16_OK && is_tree) {
+        if (flags & W4A16_NONCAUSAL) return W4A16_ERR_FLAGS;
+        // (a window that a path of drafts could leave is not taken)
+        if (max_q > W4A16_TREE_MAX || (window > 0 && window < W4A16_TREE_MAX)) return W4A16_ERR_SHAPE;
+    }
     if (st == W4A16_OK) st = check_queries(q, q_stride, out, out_stride, q_heads, kv_heads, head_dim, T);
     if (st != W4A16_OK) return st;
     w4a16::Kv4AttnArgs a = attention_args(make_cache(pages, table, s, flags), q, q_stride, cu_seqlens, kv_len, T,
                                           q_heads, max_q, max_kv, scale, window, flags);
     if (!attention_fits(a)) return W4A16_ERR_SHAPE;
-    if (!aligned(lse, 4)) return W4A16_ERR_ALIGN;
+    if (!aligned(lse, 4) || !aligned(tree, 8)) return W4A16_ERR_ALIGN;
     if (T == 0 || batch == 0 || max_q == 0) return W4A16_OK;
+    if (is_tree && !tree) return W4A16_ERR_NULL;
     st = check_cache_pointers(pages, table, cu_seqlens, kv_len);
     if (st != W4A16_OK) return st;
+    a.tree = tree;
     a.out = out;
     a.out_stride = out_stride;
     a.lse = lse;
@@ -310,6 +317,29 @@ extern "C" int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *
     }
     if (device_ok() != W4A16_OK) return W4A16_ERR_DEVICE;
     return launched(w4a16::launch_kv4_attention(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+extern "C" int w4a16_kv4_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
+                                   const int32_t *cu_seqlens, const int32_t *kv_len, void *out, int64_t out_stride,
+                                   float *lse, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                   int64_t group_size, int64_t page_size, int64_t num_pages, int64_t batch,
+                                   int64_t table_stride, int64_t max_q, int64_t max_kv, float scale, int64_t window,
+                                   unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
+    const CacheShape s{kv_heads, head_dim, group_size, page_size, num_pages, batch, table_stride};
+    return attend(s, q, q_stride, pages, table, cu_seqlens, kv_len, false, nullptr, out, out_stride, lse, T, q_heads,
+                  max_q, max_kv, scale, window, flags, workspace, workspace_bytes, stream);
+}
+
+extern "C" int w4a16_kv4_tree_attention(const void *q, int64_t q_stride, const void *pages, const int32_t *table,
+                                        const int32_t *cu_seqlens, const int32_t *kv_len, const int64_t *tree,
+                                        void *out, int64_t out_stride, float *lse, int64_t T, int64_t q_heads,
+                                        int64_t kv_heads, int64_t head_dim, int64_t group_size, int64_t page_size,
+                                        int64_t num_pages, int64_t batch, int64_t table_stride, int64_t max_q,
+                                        int64_t max_kv, float scale, int64_t window, unsigned flags,
+                                        void *workspace, size_t workspace_bytes, void *stream) {
+    const CacheShape s{kv_heads, head_dim, group_size, page_size, num_pages, batch, table_stride};
+    return attend(s, q, q_stride, pages, table, cu_seqlens, kv_len, true, tree, out, out_stride, lse, T, q_heads,
+                  max_q, max_kv, scale, window, flags, workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t w4a16_kv4_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads,

@@ -95,6 +95,7 @@ struct Kv4AttnArgs {
     int64_t T = 0;
     int q_heads = 0, max_q = 0, max_kv = 0, window = 0;    // window 0: none
     bool causal = true;
+    const int64_t *tree = nullptr;     // [T]: bit j: the token descends from new token j; or null
     float scale = 1.f;
     void *workspace = nullptr;
 };

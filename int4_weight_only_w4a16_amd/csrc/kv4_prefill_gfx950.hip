@@ -79,7 +79,8 @@ struct ManyShape {
 
 __device__ __forceinline__ int row_of_slot(int s) { return (s & 7) | (s & 8) << 1 | (s & 16) >> 1; }
 
-template <bool BF, int D, int NG>
+// TREE: the new tokens are a tree of drafts, as in the kernel for few rows.
+template <bool BF, int D, int NG, bool TREE>
 __global__ void __launch_bounds__(kManyThreads<D>)
     __attribute__((amdgpu_waves_per_eu(D <= 128 ? 2 : 1, D <= 128 ? 2 : 1))) prefill_kernel(Kv4AttnArgs a, Plan plan) {
     using T = Tile<D, NG>;
@@ -111,7 +112,13 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     const int row = w.row0 + 32 * wave + col;
     const bool in_seq = row < w.rows;
     const int token = in_seq ? row / G : 0, head = w.h * G + (in_seq ? row - token * G : 0);
-    const int lo = in_seq ? row_lo(token, w.start, a.window) : 0;
+    uint64_t kin = 0;
+    int depth = token;
+    if constexpr (TREE) {
+        kin = in_seq ? kin_of(a.tree[w.first + token], token) : 0;
+        depth = __popcll(kin) - 1;
+    }
+    const int lo = in_seq ? row_lo(depth, w.start, a.window) : 0;
     const int hi = in_seq ? row_hi(token, w.start, w.len, a.causal) : 0;
     u4 q[kDeep], sums[kTerms];
     {
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     }
     // the slots that every row of the wave sees
     int all_lo = in_seq ? lo : 0, all_hi = in_seq ? hi : 0x7fffffff;
+    if constexpr (TREE) all_hi = min(all_hi, w.start);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         all_lo = max(all_lo, __shfl_xor(all_lo, d));
@@ -430,12 +438,21 @@ __global__ void __launch_bounds__(kManyThreads<D>)
             int from = lo - 32 * tile - 4 * half, to_slot = hi - 32 * tile - 4 * half;
             asm volatile("" : "+v"(from), "+v"(to_slot));
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
+            for (int t = 0; t < kTiles; ++t) {
+                if constexpr (TREE) {            // (selects: there are no branches for a lane's slots here)
+                    const uint32_t there = found >> t & 1 ? ~0u : 0u;
+                    const uint32_t bits = (seen_bits(kin, lo, hi, w.start, 32 * (tile + t)) & there) >> (4 * half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[t][i] = bits >> (16 * ((i >> 2) & 1) + 8 * (i >> 3) + (i & 3)) & 1 ? x[t][i] : -__builtin_inff();
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int slot = 32 * t + 16 * ((i >> 2) & 1) + 8 * (i >> 3) + (i & 3);
                     if (!((found >> t & 1) & (slot >= from) & (slot < to_slot))) x[t][i] = -__builtin_inff();
                 }
+            }
         }
         float top = x[0][0];
 #pragma unroll
@@ -559,7 +576,10 @@ Plan prefill_plan(const Kv4AttnArgs &a) {
 hipError_t launch_kv4_prefill(const Kv4AttnArgs &a, const Plan &p, hipStream_t stream) {
     const dim3 grid((unsigned)p.chunks, (unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)a.c.batch);
     return by_shape(a.c, [&](auto bf, auto d, auto ng) {
-        prefill_kernel<bf(), d(), ng()><<<grid, kManyThreads<d()>, 0, stream>>>(a, p);
+        if (a.tree)
+            prefill_kernel<bf(), d(), ng(), true><<<grid, kManyThreads<d()>, 0, stream>>>(a, p);
+        else
+            prefill_kernel<bf(), d(), ng(), false><<<grid, kManyThreads<d()>, 0, stream>>>(a, p);
         return hipGetLastError();
     });
 }

@@ -5,10 +5,11 @@ Names match the C ABI in ``include/w4a16.h`` without its prefix:
   kv4_append          the same, and keys and values quantised into the cache
   kv4_read            the values a cache holds
   kv4_attention       softmax attention over the cache
+  kv4_tree_attention  the same for a tree of drafted tokens
   kv4_attention_mass  the attention weight every cached slot got, accumulated
   kv4_evict           the slots with most weight and the recent ones kept
 plus ``kv4_new_pages``, ``kv4_page_bytes`` and ``kv4_attention_workspace_bytes``.
-The six operators are bound in C++ (``csrc/kv4_binding.cpp``, built to
+The operators are bound in C++ (``csrc/kv4_binding.cpp``, built to
 ``_kv4.so``; see their docstrings): they run once for each layer and token,
 where a decode step waits for launches.
 
@@ -29,7 +30,8 @@ from . import load_library
 W4A16_ROPE_INTERLEAVED = 0x10
 W4A16_NONCAUSAL = 0x20
 
-OPERATORS = ("qk_norm_rope", "kv4_append", "kv4_read", "kv4_attention", "kv4_attention_mass", "kv4_evict")
+OPERATORS = ("qk_norm_rope", "kv4_append", "kv4_read", "kv4_attention", "kv4_tree_attention", "kv4_attention_mass",
+             "kv4_evict")
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kv4.so")
 
 
@@ -59,6 +61,8 @@ def declare(lib: ctypes.CDLL) -> None:
              + [i64] * 12 + [u32, p]),
             ("w4a16_kv4_read", [p] * 6 + [i64] * 8 + [u32, p]),
             ("w4a16_kv4_attention", [p, i64, p, p, p, p, p, i64, p] + [i64] * 11
+             + [f32, i64, u32, p, sz, p]),
+            ("w4a16_kv4_tree_attention", [p, i64, p, p, p, p, p, p, i64, p] + [i64] * 11
              + [f32, i64, u32, p, sz, p]),
             ("w4a16_kv4_attention_mass", [p, i64, p, p, p, p, p, p, i64] + [i64] * 11 + [f32, i64, u32, p]),
             ("w4a16_kv4_evict", [p, p, p, p, i64, i64, i64, p, i64, p, p, p] + [i64] * 8 + [u32, p])):
