@@ -579,6 +579,82 @@ int w4a16_kv4_evict(void *pages, const int32_t *table, const int32_t *kv_len, co
                     int64_t num_pages, int64_t batch, int64_t table_stride, int64_t max_kv,
                     unsigned flags, void *stream);
 
+/* ---- Layers that mix tokens through a state: short convolution, gated delta rule ----
+ *
+ * Beside attention layers a decoder may have layers whose merged projection goes
+ * through a short causal convolution and whose heads then mix tokens by the
+ * gated delta rule, on a state of fixed size for each sequence instead of a
+ * cache.
+ *
+ * Sequences.  As for the cache, the call's tokens of sequence b are rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [batch + 1]) of the inputs.
+ * state_index int32 [batch] names its state in a pool of num_states (an index
+ * outside the pool: none; zeros are taken and nothing is kept), which the call
+ * moves on in place; seen int32 [batch], or null, says how many tokens the
+ * state holds: for 0 it is taken as zeros, whatever is there.  Two sequences
+ * with tokens must not name one state.  A sequence without tokens keeps its
+ * state.  All are read on the device, so a captured graph may be replayed with
+ * other contents; max_q is at least the most tokens of any sequence (of more,
+ * the first max_q count), and other rows of the output are not written.
+ * tree int64 [T], or null: the new tokens are a tree of drafts, as for
+ * w4a16_kv4_tree_attention (max_q at most W4A16_TREE_MAX): what comes before a
+ * token is the state and the tokens that it descends from (its word names all of
+ * them), and the states stay as they are.  To keep the accepted path, make the call
+ * again with its tokens alone.
+ *
+ * Common rules: strides in elements, multiples of 8 and at least a row;
+ * pointers 16-byte aligned (int32, fp32 vectors of heads: 4, tree: 8; a and b by their
+ * type); flags W4A16_X_BF16 (activations bfloat16, else fp16) and the ones named
+ * at each call; T up to 2^28, batch up to 65535.  Every check runs before any
+ * HIP call; calls are asynchronous on `stream`, allocate nothing, can be captured
+ * into a graph, and give the same bits for the same inputs. */
+#define W4A16_SILU 0x40u      /* silu(z) = z / (1 + e^-z) of each result */
+#define W4A16_UNIT_QK 0x80u   /* q and k heads to unit length: x / sqrt(sum x^2 + eps) */
+
+/* Causal convolution of each channel:
+ *     out[t][c] = act(bias[c] + sum_j weight[c][j] x[t - (width - 1) + j][c])
+ * summed in fp32 and rounded once.
+ *   x, out : [T, channels] (not overlapping), channels a multiple of 8
+ *   weight : fp32 [channels, width], width 2, 3 or 4;  bias : fp32 [channels], or null
+ *   state : [num_states, width - 1, channels] of x's type: the rows before a
+ *     sequence's first token, oldest first; afterwards the last width - 1 rows. */
+int w4a16_short_conv(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                     void *state, const int32_t *state_index, const int32_t *seen,
+                     const int32_t *cu_seqlens, const int64_t *tree, void *out,
+                     int64_t out_stride, int64_t T, int64_t channels, int64_t width,
+                     int64_t num_states, int64_t batch, int64_t max_q, unsigned flags,
+                     void *stream);
+
+/* The gated delta rule, for each token and value head h (with key head
+ * h / (v_heads / k_heads)):
+ *     S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
+ *   q, k : [T, k_heads, key_dim], key_dim 64 or 128
+ *   v, out : [T, v_heads, value_dim], value_dim 64, 128, 192 or 256
+ *   a_log, dt_bias : fp32 [v_heads]: g = -exp(a_log) softplus(a + dt_bias) and
+ *     beta = sigmoid(b), a and b [T, v_heads] of the activation type; or both
+ *     null: a is g and b is beta, fp32.  g is not positive.  (a_stride, b_stride
+ *     any number of at least v_heads.)
+ *   state : fp32 [num_states, v_heads, key_dim, value_dim]
+ *   scale : finite and positive
+ *   workspace : w4a16_delta_rule_workspace_bytes(...) bytes, caller-owned, no
+ *     initial contents (null when that is 0); calls that overlap in time must
+ *     not share one. */
+int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const void *a, int64_t a_stride,
+                     const void *b, int64_t b_stride, const float *a_log, const float *dt_bias,
+                     float *state, const int32_t *state_index, const int32_t *seen,
+                     const int32_t *cu_seqlens, const int64_t *tree, void *out,
+                     int64_t out_stride, int64_t T, int64_t k_heads, int64_t v_heads,
+                     int64_t key_dim, int64_t value_dim, int64_t num_states, int64_t batch,
+                     int64_t max_q, float scale, float eps, unsigned flags, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of w4a16_delta_rule (tree: whether one is given); 0 also for
+ * arguments it rejects. */
+size_t w4a16_delta_rule_workspace_bytes(int64_t batch, int64_t T, int64_t k_heads,
+                                        int64_t v_heads, int64_t key_dim, int64_t value_dim,
+                                        int64_t max_q, int tree);
+
 /* Static, human-readable name of a status code (never null). */
 const char *w4a16_status_string(int status);
 

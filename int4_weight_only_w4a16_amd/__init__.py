@@ -15,7 +15,8 @@ Names match the C ABI in ``include/w4a16.h``:
 plus ``linear``, ``gate_up_silu``, ``linear_lora`` and ``linear_zp`` (allocate
 y, and a workspace, with torch, then call the entry point of x's and the
 scales' dtypes).  The attention block on a 4-bit key/value cache (``kv4_*``,
-``qk_norm_rope``) is bound in ``kv4``.
+``qk_norm_rope``) is bound in ``kv4``, layers that mix tokens through a state
+(``short_conv``, ``gated_delta_rule``) in ``delta``.
 """
 
 from __future__ import annotations
@@ -63,7 +64,8 @@ EXPORTS = ("w4a16_linear", "w4a16_linear_noalloc", "w4a16_linear_ex", "w4a16_lin
            "pack_gptq_v2", "unpack_gptq_v2",
            "w4a16_read_probe", "w4a16_kv4_page_bytes", "w4a16_qk_norm_rope", "w4a16_kv4_append",
            "w4a16_kv4_read", "w4a16_kv4_attention", "w4a16_kv4_attention_workspace_bytes",
-           "w4a16_kv4_tree_attention", "w4a16_kv4_attention_mass", "w4a16_kv4_evict", "w4a16_status_string")
+           "w4a16_kv4_tree_attention", "w4a16_kv4_attention_mass", "w4a16_kv4_evict", "w4a16_short_conv",
+           "w4a16_delta_rule", "w4a16_delta_rule_workspace_bytes", "w4a16_status_string")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -126,6 +128,7 @@ def load_library() -> ctypes.CDLL:
     lib.w4a16_status_string.argtypes = [i32]
     lib.w4a16_status_string.restype = ctypes.c_char_p
     kv4.declare(lib)
+    delta.declare(lib)
     _lib = lib
     return lib
 
@@ -479,14 +482,15 @@ def linear(x, qweight, scales, group_size: int, out=None, stream=None,
     return out
 
 
-from . import kv4  # noqa: E402  (needs the names above)
+from . import delta, kv4  # noqa: E402  (need the names above)
+from .delta import W4A16_SILU, W4A16_UNIT_QK, delta_rule_workspace_bytes  # noqa: E402,F401
 from .kv4 import (W4A16_NONCAUSAL, W4A16_ROPE_INTERLEAVED, kv4_attention_workspace_bytes,  # noqa: E402,F401
                   kv4_new_pages, kv4_page_bytes)
 
 
 def __getattr__(name: str):
-    """The operators of kv4, loaded with their binding when first used."""
-    if name not in kv4.OPERATORS:
+    """The operators of kv4 and delta, loaded with their binding when first used."""
+    if name not in kv4.OPERATORS + delta.OPERATORS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     globals()[name] = kv4.operator(name)
     return globals()[name]

@@ -17,7 +17,8 @@ BINDING_PATH = os.path.join(PKG_DIR, "_kv4.so")
 SOURCES = ("w4a16_capi.hip", "decode_gfx950.hip", "prefill_gfx950.hip", "lora_gfx950.hip",
            "probe_gfx950.hip", "kv4_capi.hip", "kv4_store_gfx950.hip", "kv4_attn_gfx950.hip",
            "kv4_prefill_gfx950.hip", "kv4_mass_gfx950.hip",
-           "kv4_evict_gfx950.hip")
+           "kv4_evict_gfx950.hip", "delta_capi.hip", "short_conv_gfx950.hip", "delta_step_gfx950.hip")
+BINDINGS = ("kv4_binding.cpp", "delta_binding.cpp")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -42,31 +43,31 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-def _compile_binding() -> str:
-    """The object of csrc/kv4_binding.cpp: host code against the installed torch's headers."""
+def _compile_binding(src: str) -> str:
+    """The object of a source in BINDINGS: host code against the installed torch's headers."""
     import sysconfig
 
     import torch
     include = os.path.join(os.path.dirname(torch.__file__), "include")
-    obj = os.path.join(BUILD_DIR, "kv4_binding.o")
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            "-DTORCH_EXTENSION_NAME=_kv4", "-DTORCH_API_INCLUDE_EXTENSION_H",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
-           "-c", os.path.join(CSRC, "kv4_binding.cpp"), "-o", obj]
+           "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed on kv4_binding.cpp")
+        raise RuntimeError(f"g++ failed on {src}")
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs: list[str]) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
-    subprocess.run(["g++", "-shared", "-fPIC", obj, "-o", tmp, "-L", PKG_DIR, "-l:libw4a16.so", "-L", lib, "-lc10",
+    subprocess.run(["g++", "-shared", "-fPIC", *objs, "-o", tmp, "-L", PKG_DIR, "-l:libw4a16.so", "-L", lib, "-lc10",
                     "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"],
                    check=True)
     os.replace(tmp, BINDING_PATH)
@@ -77,15 +78,15 @@ def build(resource_usage: bool = False) -> str:
     operators' Python binding against it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Rpass-analysis=kernel-resource-usage"] if resource_usage else []
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + len(BINDINGS)) as ex:
+        bindings = [ex.submit(_compile_binding, s) for s in BINDINGS]
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
-        binding = binding.result()
+        bindings = [b.result() for b in bindings]
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding)
+    _link_binding(bindings)
     return LIB_PATH
 
 

@@ -36,7 +36,7 @@ BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kv4.so
 
 
 def operator(name: str):
-    """One of OPERATORS, from the built binding."""
+    """An operator of the built binding (OPERATORS here and in delta)."""
     load_library()                      # torch first, then the library that the binding calls
     if not os.path.exists(BINDING_PATH):
         raise RuntimeError(f"{BINDING_PATH} is not built; run __graft_entry__.build() first")

@@ -1,0 +1,101 @@
+"""What short_conv and delta_rule refuse, through the C ABI on the CPU: every check runs before
+any HIP call, so the made-up addresses below are never touched.  And the references' own forms."""
+
+import ctypes
+
+import pytest
+
+import int4_weight_only_w4a16_amd as w4
+from test_kv4_boundary_cpu import call, lib  # noqa: F401
+
+
+def conv(lib, **kw):  # noqa: F811
+    d = dict(x=0x1000, xs=512, weight=0x2000, bias=0x3000, state=0x4000, index=0x5000, seen=0x6000, cu=0x7000,
+             tree=None, out=0x8000, os=512, T=4, C=512, W=4, states=9, batch=2, max_q=3, flags=0, stream=None)
+    return call(lib.w4a16_short_conv, d, kw)
+
+
+def delta(lib, **kw):  # noqa: F811
+    d = dict(q=0x1000, qs=256, k=0x2000, ks=256, v=0x3000, vs=512, a=0x4000, as_=4, b=0x5000, bs=4, a_log=0x6000,
+             dt=0x7000, state=0x8000, index=0x9000, seen=0xa000, cu=0xb000, tree=None, out=0xc000, os=512, T=4, hk=2,
+             hv=4, dk=128, dv=128, states=9, batch=2, max_q=3, scale=ctypes.c_float(0.1), eps=ctypes.c_float(1e-6),
+             flags=0, ws=0xd0000, wsb=1 << 40, stream=None)
+    return call(lib.w4a16_delta_rule, d, kw)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), w4.W4A16_ERR_NULL), (dict(weight=None), w4.W4A16_ERR_NULL), (dict(state=None), w4.W4A16_ERR_NULL),
+    (dict(out=None), w4.W4A16_ERR_NULL), (dict(index=None), w4.W4A16_ERR_NULL), (dict(cu=None), w4.W4A16_ERR_NULL),
+    (dict(x=0x1008), w4.W4A16_ERR_ALIGN), (dict(weight=0x2004), w4.W4A16_ERR_ALIGN),
+    (dict(bias=0x3004), w4.W4A16_ERR_ALIGN), (dict(state=0x4002), w4.W4A16_ERR_ALIGN),
+    (dict(out=0x8004), w4.W4A16_ERR_ALIGN), (dict(index=0x5002), w4.W4A16_ERR_ALIGN),
+    (dict(seen=0x6001), w4.W4A16_ERR_ALIGN), (dict(tree=0x9004), w4.W4A16_ERR_ALIGN),
+    (dict(C=0), w4.W4A16_ERR_SHAPE), (dict(C=12, xs=16, os=16), w4.W4A16_ERR_SHAPE), (dict(xs=504), w4.W4A16_ERR_SHAPE),
+    (dict(os=516), w4.W4A16_ERR_SHAPE), (dict(W=1), w4.W4A16_ERR_SHAPE), (dict(W=5), w4.W4A16_ERR_SHAPE),
+    (dict(T=-1), w4.W4A16_ERR_SHAPE), (dict(T=(1 << 28) + 1), w4.W4A16_ERR_SHAPE), (dict(batch=65536), w4.W4A16_ERR_SHAPE),
+    (dict(max_q=-1), w4.W4A16_ERR_SHAPE), (dict(tree=0x9000, max_q=65), w4.W4A16_ERR_SHAPE),
+    (dict(states=-1), w4.W4A16_ERR_SHAPE), (dict(C=1 << 24, xs=1 << 24, os=1 << 24, T=1 << 28, max_q=1 << 28), w4.W4A16_ERR_SHAPE),
+    (dict(flags=0x2), w4.W4A16_ERR_FLAGS), (dict(flags=w4.W4A16_UNIT_QK), w4.W4A16_ERR_FLAGS),
+    (dict(T=0, x=None), w4.W4A16_OK), (dict(batch=0, cu=None), w4.W4A16_OK), (dict(max_q=0), w4.W4A16_OK)])
+def test_conv_refusals(lib, kw, status):  # noqa: F811
+    assert conv(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    *[(dict([(n, None)]), w4.W4A16_ERR_NULL) for n in ("q", "k", "v", "a", "b", "state", "index", "cu", "out", "dt")],
+    (dict(a_log=None), w4.W4A16_ERR_NULL),
+    *[(dict([(n, 0x1008)]), w4.W4A16_ERR_ALIGN) for n in ("q", "k", "v", "state", "out")],
+    (dict(a=0x4001), w4.W4A16_ERR_ALIGN), (dict(a_log=None, dt=None, a=0x4002), w4.W4A16_ERR_ALIGN),
+    (dict(b=0x5001), w4.W4A16_ERR_ALIGN), (dict(dt=0x7002), w4.W4A16_ERR_ALIGN), (dict(tree=0x1004), w4.W4A16_ERR_ALIGN),
+    (dict(index=0x9002), w4.W4A16_ERR_ALIGN),
+    (dict(dk=96), w4.W4A16_ERR_SHAPE), (dict(dk=256, qs=512, ks=512), w4.W4A16_ERR_SHAPE), (dict(dv=32), w4.W4A16_ERR_SHAPE),
+    (dict(dv=320, vs=1280, os=1280), w4.W4A16_ERR_SHAPE), (dict(hk=3), w4.W4A16_ERR_SHAPE), (dict(hk=0), w4.W4A16_ERR_SHAPE),
+    (dict(hv=0), w4.W4A16_ERR_SHAPE), (dict(qs=248), w4.W4A16_ERR_SHAPE), (dict(ks=260), w4.W4A16_ERR_SHAPE),
+    (dict(vs=504), w4.W4A16_ERR_SHAPE), (dict(os=0), w4.W4A16_ERR_SHAPE), (dict(as_=3), w4.W4A16_ERR_SHAPE),
+    (dict(bs=0), w4.W4A16_ERR_SHAPE), (dict(T=-1), w4.W4A16_ERR_SHAPE), (dict(batch=70000), w4.W4A16_ERR_SHAPE),
+    (dict(max_q=-2), w4.W4A16_ERR_SHAPE), (dict(tree=0x1000, max_q=65), w4.W4A16_ERR_SHAPE),
+    (dict(scale=ctypes.c_float(0)), w4.W4A16_ERR_SHAPE), (dict(scale=ctypes.c_float(float("nan"))), w4.W4A16_ERR_SHAPE),
+    (dict(eps=ctypes.c_float(-1)), w4.W4A16_ERR_SHAPE), (dict(eps=ctypes.c_float(float("inf"))), w4.W4A16_ERR_SHAPE),
+    (dict(flags=w4.W4A16_SILU), w4.W4A16_ERR_FLAGS), (dict(flags=0x100), w4.W4A16_ERR_FLAGS),
+    (dict(T=0, q=None), w4.W4A16_OK), (dict(batch=0), w4.W4A16_OK), (dict(max_q=0, cu=None), w4.W4A16_OK)])
+def test_delta_refusals(lib, kw, status):  # noqa: F811
+    assert delta(lib, **kw) == status
+
+
+def test_valid_calls_reach_the_device_check(lib):  # noqa: F811
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    for kw in (dict(), dict(bias=None, seen=None), dict(tree=0xe000, max_q=64), dict(flags=w4.W4A16_X_BF16 | w4.W4A16_SILU)):
+        assert conv(lib, **kw) == w4.W4A16_ERR_DEVICE
+    for kw in (dict(), dict(a_log=None, dt=None, seen=None), dict(tree=0xe000, max_q=64), dict(T=900, max_q=700),
+               dict(flags=w4.W4A16_X_BF16 | w4.W4A16_UNIT_QK), dict(dv=192, vs=768, os=768)):
+        assert delta(lib, **kw) == w4.W4A16_ERR_DEVICE
+
+
+def test_a_chunk_s_triangular_form_is_the_recurrence():
+    """The form that long calls are computed in, against the definition: U = T (V - e^G K S)."""
+    import torch
+
+    import delta_ref as ref
+    import tree_ref as tr
+    g = torch.Generator().manual_seed(0)
+    n, d = 30, 16
+    for parents in (tr.chain(n), tr.random_tree(n, __import__("random").Random(1), 2)):
+        q, k = (torch.randn(n, 1, d, generator=g, dtype=torch.float64) for _ in range(2))
+        v, S = torch.randn(n, 1, 8, generator=g, dtype=torch.float64), torch.randn(1, d, 8, generator=g, dtype=torch.float64)
+        lg, beta = -torch.rand(n, 1, generator=g, dtype=torch.float64), torch.rand(n, 1, generator=g, dtype=torch.float64)
+        out, size, last = ref.delta(q, k, v, lg, beta, S, 0.3, True, 0.0, parents)
+        kin = torch.zeros(n, n, dtype=torch.float64)
+        for i in range(n):
+            kin[i, tr.path(parents, i)] = 1
+        G = kin @ lg[:, 0]
+        decay = torch.where(kin > 0, torch.exp(G[:, None] - G[None]), torch.zeros_like(kin))
+        qn, kn = (x[:, 0] / x[:, 0].norm(dim=-1, keepdim=True) for x in (q, k))
+        A = torch.tril(beta * (kn @ kn.T) * decay, -1)
+        U = torch.linalg.solve(torch.eye(n, dtype=torch.float64) + A, beta * (v[:, 0] - torch.exp(G)[:, None] * (kn @ S[0])))
+        o = 0.3 * (torch.exp(G)[:, None] * (qn @ S[0]) + (decay * (qn @ kn.T)) @ U)
+        assert (o - out[:, 0]).abs().max() < 1e-12 and (out.abs() <= size + 1e-12).all()
+        if parents == tr.chain(n):
+            end = torch.exp(G[-1]) * S[0] + (torch.exp(G[-1] - G)[:, None] * kn).T @ U
+            assert (end - last[0]).abs().max() < 1e-12
