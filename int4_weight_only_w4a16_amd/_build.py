@@ -17,7 +17,8 @@ BINDING_PATH = os.path.join(PKG_DIR, "_kv4.so")
 SOURCES = ("w4a16_capi.hip", "decode_gfx950.hip", "prefill_gfx950.hip", "lora_gfx950.hip",
            "probe_gfx950.hip", "kv4_capi.hip", "kv4_store_gfx950.hip", "kv4_attn_gfx950.hip",
            "kv4_prefill_gfx950.hip", "kv4_mass_gfx950.hip",
-           "kv4_evict_gfx950.hip", "delta_capi.hip", "short_conv_gfx950.hip", "delta_step_gfx950.hip")
+           "kv4_evict_gfx950.hip", "delta_capi.hip", "short_conv_gfx950.hip", "delta_step_gfx950.hip",
+           "delta_chunk_gfx950.hip")
 BINDINGS = ("kv4_binding.cpp", "delta_binding.cpp")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -90,6 +90,19 @@ extern "C" int w4a16_short_conv(const void *x, int64_t x_stride, const float *we
     return launched(w4a16::launch_short_conv(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// Most tokens of a sequence that go token by token.
+static constexpr int64_t kStepTokens = 8;
+
+static bool in_chunks(const w4a16::DeltaArgs &d) { return d.s.tree || d.s.max_q > kStepTokens; }
+
+static int check_delta(int64_t T, int64_t k_heads, int64_t v_heads, int64_t key_dim, int64_t value_dim,
+                       int64_t num_states, int64_t batch, int64_t max_q, bool tree) {
+    if ((key_dim != 64 && key_dim != 128) || !in_range(value_dim, 64, 256) || value_dim % 64 != 0 ||
+        !in_range(k_heads, 1, 1 << 12) || !in_range(v_heads, 1, 1 << 12) || v_heads % k_heads != 0)
+        return W4A16_ERR_SHAPE;
+    return check_sizes(T, batch, max_q, num_states, tree);
+}
+
 extern "C" int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                 int64_t v_stride, const void *a, int64_t a_stride, const void *b, int64_t b_stride,
                                 const float *a_log, const float *dt_bias, float *state, const int32_t *state_index,
@@ -97,13 +110,8 @@ extern "C" int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, 
                                 int64_t out_stride, int64_t T, int64_t k_heads, int64_t v_heads, int64_t key_dim,
                                 int64_t value_dim, int64_t num_states, int64_t batch, int64_t max_q, float scale,
                                 float eps, unsigned flags, void *workspace, size_t workspace_bytes, void *stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if ((flags & ~(W4A16_X_BF16 | W4A16_UNIT_QK)) != 0) return W4A16_ERR_FLAGS;
-    if ((key_dim != 64 && key_dim != 128) || !in_range(value_dim, 64, 256) || value_dim % 64 != 0 ||
-        !in_range(k_heads, 1, 1 << 12) || !in_range(v_heads, 1, 1 << 12) || v_heads % k_heads != 0)
-        return W4A16_ERR_SHAPE;
-    int st = check_sizes(T, batch, max_q, num_states, tree != nullptr);
+    int st = check_delta(T, k_heads, v_heads, key_dim, value_dim, num_states, batch, max_q, tree != nullptr);
     if (st == W4A16_OK) st = check_stride(q_stride, k_heads * key_dim);
     if (st == W4A16_OK) st = check_stride(k_stride, k_heads * key_dim);
     if (st == W4A16_OK) st = check_stride(v_stride, v_heads * value_dim);
@@ -146,12 +154,28 @@ extern "C" int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, 
     d.eps = eps;
     d.bf16 = (flags & W4A16_X_BF16) != 0;
     d.unit = (flags & W4A16_UNIT_QK) != 0;
+    d.workspace = workspace;
+    if (in_chunks(d)) {
+        if (!workspace) return W4A16_ERR_NULL;
+        if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+        if (workspace_bytes < w4a16::delta_chunk_workspace_bytes(d)) return W4A16_ERR_WORKSPACE;
+    }
     if (device_ok() != W4A16_OK) return W4A16_ERR_DEVICE;
-    return launched(w4a16::launch_delta_step(d, reinterpret_cast<hipStream_t>(stream)));
+    const hipStream_t on = reinterpret_cast<hipStream_t>(stream);
+    return launched(in_chunks(d) ? w4a16::launch_delta_chunk(d, on) : w4a16::launch_delta_step(d, on));
 }
 
 extern "C" size_t w4a16_delta_rule_workspace_bytes(int64_t batch, int64_t T, int64_t k_heads, int64_t v_heads,
                                                    int64_t key_dim, int64_t value_dim, int64_t max_q, int tree) {
-    (void)batch; (void)T; (void)k_heads; (void)v_heads; (void)key_dim; (void)value_dim; (void)max_q; (void)tree;
-    return 0;
+    if (check_delta(T, k_heads, v_heads, key_dim, value_dim, 0, batch, max_q, tree != 0) != W4A16_OK || T == 0 ||
+        batch == 0 || max_q == 0)
+        return 0;
+    static const int64_t some = 0;
+    w4a16::DeltaArgs d;
+    d.s = make_sequences(nullptr, nullptr, nullptr, tree ? &some : nullptr, T, batch, max_q, 0);
+    d.k_heads = (int)k_heads;
+    d.v_heads = (int)v_heads;
+    d.key_dim = (int)key_dim;
+    d.value_dim = (int)value_dim;
+    return in_chunks(d) ? w4a16::delta_chunk_workspace_bytes(d) : 0;
 }

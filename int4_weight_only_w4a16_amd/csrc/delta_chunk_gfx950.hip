@@ -1,0 +1,671 @@
+// The gated delta rule for prompts, and for trees of drafted tokens, 64 tokens at a time.
+//
+// In a chunk with G_i the sum of g up to token i, from the state S at its start (K, Q, V its rows,
+// each key and query of unit length if asked for):
+//   A_ij = beta_i e^(G_i - G_j) k_i . k_j  (j < i),   T = (I + A)^-1 diag(beta)
+//   U = T (V - e^G K S)                               the rows that the tokens write
+//   O = scale (e^G Q S + [e^(G_i - G_j) q_i . k_j]_(j <= i) U)
+//   S <- e^G_last S + (e^(G_last - G) K)^T U
+// For a tree "j < i" is "i descends from j", G_i the sum along the path, and S stays.
+//
+// chunk_prep_kernel makes what does not depend on S, for all chunks at once: T, the triangle of
+// products with the queries, and keys and queries as operands.  chunk_scan_kernel walks over the
+// chunks of one head with sixteen columns of S in each wave (columns do not depend on each other):
+// the state stays in the accumulators of the matrix instructions, and what one product leaves in
+// a lane is the next one's operand as it stands, if the depth (channels, or tokens) is taken in
+// the order slot 8 b + e = place 4 b + e of the first 16, 16 + 4 b + e - 4 of the next.  So waves
+// exchange nothing.
+//
+// The state is fp32, and its sums keep that: each factor that is not an input enters in two
+// 16-bit parts of eleven bits (S, the rows V - e^G K S, T, the rows e^(G_last - G) U), three
+// products for a pair of such factors, lo x lo left out (2^-22).  Inputs are exact as they are, bfloat16
+// ones too, once a power of two for each row brings them into fp16's range; so do powers of
+// two for each row of T and each column of S and of the rows.  What goes into the output
+// alone has one part (2^-12).  Powers of two come off in fp32.
+//
+// What is not finite (in a key, a gate, a value) would reach earlier rows, or a tree's other
+// branches, through products with zero.  Its row is taken out as zeros and marked, and the rows
+// that come after it, and S, become NaN.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "delta_device.hpp"
+#include "lds.hpp"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kChunk = 64;
+constexpr int kTop = 14;               // operands lie below 2^kTop
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Workspace of one chunk: for each key head K, K^T and Q as operands (tiles of 1 KiB: 64 lanes x 16
+// bytes), for each value head T in two parts, the products with the queries (the six tiles of 16 x 32
+// that are not above the diagonal), and what goes by rows.
+template <int DK>
+struct Chunk {
+    static constexpr int kTiles = DK / 8;                      // of K, K^T and Q each
+    static constexpr int kKey = 3 * kTiles * 1024;
+    static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRows = 18 * 1024;
+    static constexpr int kValue = 20 * 1024;
+    // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
+    // output of S and of U; words of a tree; e^G_last and the power of two in the second of them
+    static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kKin = 1024, kLast = 1536;
+    static constexpr int kUnits = (kKey + kValue) / 1024;
+};
+
+// The part of a call that one launch works on: `chunks` chunks from the first_chunk-th of `batch`
+// sequences from the first_seq-th.
+struct Segment {
+    int first_seq, batch, first_chunk, chunks;
+    uint8_t *keys, *values;            // [batch][chunks][heads][bytes]
+    float *carry;                      // [batch][v_heads][DK][value_dim]: states that are not in the pool
+};
+
+__device__ __forceinline__ int exponent(float v) { return __builtin_amdgcn_frexp_expf(v); }
+__device__ __forceinline__ float times2(float v, int e) { return __builtin_amdgcn_ldexpf(v, e); }
+__device__ __forceinline__ float exp_f32(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
+// Row (or column) r of what lane (r, b) holds as operand s: places 4 b .. of two tiles of 16.
+__device__ __forceinline__ int place(int s, int b, int e) { return 32 * s + 16 * (e >> 2) + 4 * b + (e & 3); }
+
+// First tile of row tile mt among those that are not above the diagonal.
+__device__ __forceinline__ constexpr int tile_of(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
+
+// x by and y by rounded to fp16, and what that leaves, rounded too.  (The first parts are pinned: made
+// twice, by instructions that round ties to different sides, they would not go with the second.)
+__device__ __forceinline__ void split2(float x, float y, float by, uint32_t *hi, uint32_t *lo) {
+    *hi = pack2<false>(x * by, y * by);
+    asm("" : "+v"(*hi));
+    *lo = pack2<false>(__builtin_fmaf(x, by, -lo_f32<false>(*hi)), __builtin_fmaf(y, by, -hi_f32<false>(*hi)));
+}
+
+// Two operands of eleven bits each from eight fp32 values times `by`.
+struct Split {
+    h8 hi, lo;
+};
+__device__ __forceinline__ Split split(const f4 &x, const f4 &y, float by) {
+    u4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t h, l;
+        split2(x[2 * e], x[2 * e + 1], by, &h, &l);
+        hi[e] = h;
+        lo[e] = l;
+        split2(y[2 * e], y[2 * e + 1], by, &h, &l);
+        hi[2 + e] = h;
+        lo[2 + e] = l;
+    }
+    return {__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
+}
+
+template <bool BF, int DK, bool TREE>
+__global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment seg) {
+    using C = Chunk<DK>;
+    constexpr int kStride = DK + 8, kA = 68, kP = 72;
+    __shared__ __align__(16) _Float16 K[kChunk][kStride], Q[kChunk][kStride];
+    __shared__ __align__(16) float A[kChunk][kA], X[kChunk][kA];
+    __shared__ double G[kChunk];
+    __shared__ float beta[kChunk], kf[kChunk], qf[kChunk];
+    __shared__ int tau[kChunk];
+    __shared__ uint64_t kin[kChunk];
+    __shared__ uint32_t bad[kChunk];           // 1: the key or a gate, 2: the query is not finite
+    __shared__ float within_scale[kChunk];
+
+    const int ci = blockIdx.x, h = blockIdx.y, r = a.v_heads / a.k_heads, hk = h / r;
+    Seq s;
+    if (!seq_of(a.s, seg.first_seq + blockIdx.z, &s)) return;
+    if (TREE) s.n = min(s.n, kChunk);
+    const int t0 = kChunk * (seg.first_chunk + ci);
+    if (t0 >= s.n) return;
+    const int n = min(kChunk, s.n - t0);
+    const int64_t slot = (int64_t)blockIdx.z * seg.chunks + ci;
+    uint8_t *const to_key = seg.keys + (slot * a.k_heads + hk) * C::kKey;
+    uint8_t *const to = seg.values + (slot * a.v_heads + h) * C::kValue;
+
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, b = lane >> 4;
+
+    // ---- keys and queries as fp16 rows of about 2^14 at most, and what came off them ----
+    if (tid < kChunk) bad[tid] = 0;
+    __syncthreads();
+    {
+        const int row = tid >> 2, part = (tid & 3) * (DK / 4);
+        const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint16_t *const src = (which ? static_cast<const uint16_t *>(a.q) + (s.first + t0 + row) * a.q_stride
+                                               : static_cast<const uint16_t *>(a.k) + (s.first + t0 + row) * a.k_stride) +
+                                        hk * DK + part;
+            u4 raw[DK / 32];
+#pragma unroll
+            for (int i = 0; i < DK / 32; ++i) raw[i] = row < n ? *reinterpret_cast<const u4 *>(src + 8 * i) : u4{0u, 0u, 0u, 0u};
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < DK / 32; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(raw[i][e] & 0x7FFFu, raw[i][e] >> 16 & 0x7FFFu));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+            const bool fine = top < limit;
+            const int up = fine && top ? kTop - exponent(lo_f32<BF>(top)) : 0;
+            float sum = 0.f;
+            _Float16 *const dst = (which ? Q[row] : K[row]) + part;
+#pragma unroll
+            for (int i = 0; i < DK / 32; ++i) {
+                h8 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = fine ? times2(lo_f32<BF>(raw[i][e]), up) : 0.f;
+                    const float x1 = fine ? times2(hi_f32<BF>(raw[i][e]), up) : 0.f;
+                    sum = __builtin_fmaf(x0, x0, sum);
+                    sum = __builtin_fmaf(x1, x1, sum);
+                    v[2 * e] = (_Float16)x0;
+                    v[2 * e + 1] = (_Float16)x1;
+                }
+                *reinterpret_cast<h8 *>(dst + 8 * i) = v;
+            }
+            sum += __shfl_xor(sum, 1);
+            sum += __shfl_xor(sum, 2);
+            if (part == 0) {
+                // (rows past the sequence's are zeros and count for nothing)
+                float f = a.unit ? 1.0f / sqrtf(sum + times2(a.eps, 2 * up)) : times2(1.0f, -up);
+                if (row >= n) f = 0.f;
+                const bool ok = fine && f < __builtin_inff();
+                (which ? qf : kf)[row] = ok ? f : 0.f;
+                if (!ok) atomicOr(&bad[row], 1u + which);
+            }
+        }
+    }
+    // ---- gates, and their sums in 64 bits: differences of far sums keep their precision ----
+    if (tid < kChunk) {
+        Gates gate{0.f, 0.f};
+        if (tid < n)
+            gate = gates_of<BF>(a, s.first + t0 + tid, h, a.a_log ? expf(a.a_log[h]) : 0.f, a.a_log ? a.dt_bias[h] : 0.f);
+        const bool ok = gate.g < __builtin_inff() && __builtin_fabsf(gate.beta) < __builtin_inff();
+        if (!ok) atomicOr(&bad[tid], 1u);
+        // (e^-256 is 0 in fp32, as is all that it multiplies)
+        const double g = ok ? (double)fmaxf(gate.g, -256.f) : 0.0;
+        beta[tid] = ok ? gate.beta : 0.f;
+        double sum = g;
+        uint64_t word = (2ull << tid) - 1;
+        if constexpr (TREE) {
+            word = tid < n ? ((uint64_t)a.s.tree[s.first + tid] & ((1ull << tid) - 1)) | 1ull << tid : 0;
+            sum = 0;
+            for (int j = 0; j < kChunk; ++j) {
+                const double gj = __shfl(g, j);
+                if (word >> j & 1) sum += gj;
+            }
+        } else {
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const double below = __shfl_up(sum, d);
+                if (tid >= d) sum += below;
+            }
+        }
+        G[tid] = sum;
+        kin[tid] = word;
+    }
+    __syncthreads();
+
+    // ---- products of keys with keys and queries; lane (m, b): rows 16 wave + 4 b + j, column 16 nt + m ----
+    f4 p[4];
+    {
+        f4 kk[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) kk[nt] = p[nt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < DK / 32; ++d) {
+            const h8 ka = *reinterpret_cast<const h8 *>(&K[16 * wave + m][32 * d + 8 * b]);
+            const h8 qa = *reinterpret_cast<const h8 *>(&Q[16 * wave + m][32 * d + 8 * b]);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                if (nt > wave) continue;
+                const h8 kb = *reinterpret_cast<const h8 *>(&K[16 * nt + m][32 * d + 8 * b]);
+                kk[nt] = mfma16x16x32(ka, kb, kk[nt]);
+                p[nt] = mfma16x16x32(qa, kb, p[nt]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt > wave) continue;
+            const int col = 16 * nt + m;
+            const double gc = G[col];
+            const float kc = kf[col];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * wave + 4 * b + j;
+                const bool sees = TREE ? kin[row] >> col & 1 : col <= row;
+                const float w = sees ? exp_f32((float)(G[row] - gc)) * kc : 0.f;
+                A[row][col] = col < row ? beta[row] * (kf[row] * kk[nt][j] * w) : 0.f;
+                p[nt][j] = a.scale * (qf[row] * p[nt][j] * w);
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- X = (I + A)^-1: blocks of 16 on the diagonal by substitution, the others from them ----
+    {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == m ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v = __builtin_fmaf(-A[16 * wave + i][16 * wave + j], x[j], v);
+            x[i] = v;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (b == i / 4) X[16 * wave + i][16 * wave + m] = x[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+        __syncthreads();
+        const int i = wave + d, j = wave;
+        if (i < 4) {
+            f4 acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
+            for (int mid = j; mid < i; ++mid) {
+                const f4 left = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * mid + 4 * b]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], X[16 * mid + 4 * b + e][16 * j + m], acc, 0, 0, 0);
+            }
+            const f4 left = *reinterpret_cast<const f4 *>(&X[16 * i + m][16 * i + 4 * b]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], acc[e], out, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[16 * i + 4 * b + e][16 * j + m] = -out[e];
+        }
+    }
+    __syncthreads();
+
+    // ---- T = X diag(beta) as operands; lane (m, b): row 16 wave + m ----
+    {
+        const int row = 16 * wave + m;
+        float t[2][8], top = 0.f;
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const int col = place(d, b, e);
+                const bool in = 2 * d + (e >> 2) <= wave;
+                f4 v = {0.f, 0.f, 0.f, 0.f};
+                if (in) v = *reinterpret_cast<const f4 *>(&X[row][col]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t[d][e + i] = in ? v[i] * beta[col + i] : 0.f;
+                    top = fmaxf(top, __builtin_fabsf(t[d][e + i]));
+                }
+            }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const int up = kTop - max(exponent(top), -60);
+        if (b == 0) tau[row] = up;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            if (2 * d > wave) continue;
+            const Split x = split(f4{t[d][0], t[d][1], t[d][2], t[d][3]}, f4{t[d][4], t[d][5], t[d][6], t[d][7]}, times2(1.0f, up));
+            const int tile = tile_of(wave, d);
+            *reinterpret_cast<h8 *>(to + C::kHigh + 1024 * tile + 16 * lane) = x.hi;
+            *reinterpret_cast<h8 *>(to + C::kLow + 1024 * tile + 16 * lane) = x.lo;
+        }
+    }
+    __syncthreads();
+
+    // ---- products with the queries: by what the rows of U carry, through LDS into operands ----
+    _Float16 *const P = reinterpret_cast<_Float16 *>(&A[0][0]);      // [64][kP]
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 16 * wave + 4 * b + j;
+        float top = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt > wave) continue;
+            p[nt][j] = times2(p[nt][j], -tau[16 * nt + m]);
+            top = fmaxf(top, __builtin_fabsf(p[nt][j]));
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        const int up = kTop - max(exponent(top), -100);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)times2(p[nt][j], up);
+        if (m == 0) within_scale[row] = times2(1.0f, -up);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        if (2 * d > wave) continue;
+        const _Float16 *const from = P + (16 * wave + m) * kP + 32 * d + 4 * b;
+        const h4 lo = *reinterpret_cast<const h4 *>(from), hi = *reinterpret_cast<const h4 *>(from + 16);
+        *reinterpret_cast<h8 *>(to + C::kWithin + 1024 * tile_of(wave, d) + 16 * lane) =
+            __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+
+    // ---- what goes by rows ----
+    if (tid < kChunk) {
+        float *const rows = reinterpret_cast<float *>(to + C::kRows);
+        const float grow = exp_f32((float)G[tid]), nan = __builtin_nanf("");
+        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], -tau[tid]);
+        float top = weigh;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        const int up = -20 - max(exponent(top), -120);
+        rows[C::kOff / 4 + tid] = bad[tid] & 1 ? nan : grow * kf[tid];
+        rows[C::kWeigh / 4 + tid] = times2(weigh, up);
+        rows[C::kFromS / 4 + tid] = bad[tid] & 2 ? nan : a.scale * qf[tid] * grow;
+        rows[C::kFromU / 4 + tid] = within_scale[tid];
+        reinterpret_cast<uint64_t *>(to + C::kRows + C::kKin)[tid] = kin[tid];
+        if (tid == 0) {
+            rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
+            reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
+        }
+    }
+
+    // ---- keys and queries as operands, once for each key head ----
+    if (h % r != 0) return;
+#pragma unroll
+    for (int i = 0; i < C::kTiles / 4; ++i) {
+        const int tile = 4 * i + wave;                     // of K and Q: [row tile][DK / 32]
+        const int row = 16 * (tile / (DK / 32)) + m, ch = 32 * (tile % (DK / 32)) + 4 * b;
+        const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
+        const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
+        *reinterpret_cast<h8 *>(to_key + 1024 * tile + 16 * lane) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
+        *reinterpret_cast<h8 *>(to_key + 1024 * (2 * C::kTiles + tile) + 16 * lane) =
+            __builtin_shufflevector(q0, q1, 0, 1, 2, 3, 4, 5, 6, 7);
+        h8 kt;                                             // of K^T: [16 channels][32 tokens]
+#pragma unroll
+        for (int e = 0; e < 8; ++e) kt[e] = K[place(tile & 1, b, e)][16 * (tile >> 1) + m];
+        *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) = kt;
+    }
+}
+
+// The largest size in a column's lanes; NaN if there is one.
+__device__ __forceinline__ float top_of_column(float v) {
+    v = __builtin_elementwise_maximum(v, __shfl_xor(v, 16));
+    return __builtin_elementwise_maximum(v, __shfl_xor(v, 32));
+}
+
+template <bool BF, int DK, bool TREE, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Segment seg) {
+    using C = Chunk<DK>;
+    constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
+    __shared__ __align__(16) uint8_t lds_raw[2 * (C::kKey + C::kValue)];     // two chunks
+    lds_u8 *const lds = (lds_u8 *)lds_raw;
+
+    const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
+    Seq s;
+    if (!seq_of(a.s, seg.first_seq + blockIdx.z, &s)) return;
+    if (TREE) s.n = min(s.n, kChunk);
+    const int first = kChunk * seg.first_chunk;
+    if (first >= s.n) return;
+    const int count = min(seg.chunks, (s.n - first + kChunk - 1) / kChunk);
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
+    const int col = 16 * (blockIdx.x * WAVES + wave) + m;
+    const int64_t slot = (int64_t)blockIdx.z * seg.chunks;
+    auto copy = [&](int ci) {
+        const uint8_t *const key = seg.keys + ((slot + ci) * a.k_heads + hk) * C::kKey;
+        const uint8_t *const value = seg.values + ((slot + ci) * a.v_heads + h) * C::kValue;
+        lds_u8 *const to = lds + (ci & 1) * (C::kKey + C::kValue);
+#pragma unroll
+        for (int u = 0; u < C::kUnits; u += WAVES) {
+            const int unit = u + wave;
+            if (unit < C::kKey / 1024)
+                copy_kib(key, C::kKey, 1024 * unit, to + 1024 * unit, lane);
+            else if (unit < C::kUnits)
+                copy_kib(value, C::kValue, 1024 * unit - C::kKey, to + 1024 * unit, lane);
+        }
+    };
+    copy(0);
+
+    // S 2^power, lane (m, b): rows 16 t + 4 b + j of its column
+    f4 S[kRowTiles];
+    int power = 0;
+    float *const pool = s.state < 0 ? seg.carry + ((int64_t)blockIdx.z * a.v_heads + h) * DK * a.value_dim
+                                    : a.state + (s.state * a.v_heads + h) * DK * a.value_dim;
+    {
+        const bool zero = seg.first_chunk == 0 && s.fresh;
+        const float *const from = pool + (int64_t)(4 * b) * a.value_dim + col;
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][j] = zero ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
+    }
+    const uint16_t *const values = static_cast<const uint16_t *>(a.v) + (s.first + first) * a.v_stride +
+                                   (int64_t)h * a.value_dim + col;
+    uint16_t *const outs = static_cast<uint16_t *>(a.out) + (s.first + first) * a.out_stride +
+                           (int64_t)h * a.value_dim + col;
+
+    for (int ci = 0; ci < count; ++ci) {
+        const int n = min(kChunk, s.n - first - kChunk * ci);
+        wait_loads<0>();
+        lds_barrier();                         // this chunk is there, and the other one is done with
+        if (ci + 1 < count) copy(ci + 1);
+        const lds_u8 *const at = lds + (ci & 1) * (C::kKey + C::kValue), *const mine = at + 16 * lane;
+        const lds_u8 *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
+        f4 V[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * t + 4 * b + j;
+                V[t][j] = row < n ? lo_f32<BF>(values[(int64_t)(kChunk * ci + row) * a.v_stride]) : 0.f;
+            }
+
+        // ---- K S and Q S ----
+        float top = 0.f;
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = __builtin_elementwise_maximum(top, __builtin_fabsf(S[t][j]));
+        top = top_of_column(top);
+        const int top_s = max(exponent(top), -100);
+        const float by_s = times2(1.0f, kTop - top_s);
+        f4 ks[4], qs[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[t] = qs[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) {
+            const Split x = split(S[2 * d], S[2 * d + 1], by_s);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const h8 k = lds_get<h8>(mine + 1024 * (t * kSteps + d));
+                const h8 q = lds_get<h8>(mine + 1024 * (2 * C::kTiles + t * kSteps + d));
+                ks[t] = mfma16x16x32(k, x.hi, ks[t]);
+                ks[t] = mfma16x16x32(k, x.lo, ks[t]);
+                qs[t] = mfma16x16x32(q, x.hi, qs[t]);
+            }
+        }
+        const int from_s = top_s - kTop - power;           // S's own power of two
+
+        // ---- R = V - e^G K S, its rows as operands ----
+        f4 R[4];
+        float top_r = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f4 off = lds_get<f4>(rows + C::kOff + 64 * t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                R[t][j] = V[t][j] - times2(off[j] * ks[t][j], from_s);
+                top_r = __builtin_elementwise_maximum(top_r, __builtin_fabsf(R[t][j]));
+            }
+        }
+        top_r = top_of_column(top_r);
+        uint64_t lost = 0;                     // rows that come after one that is not finite
+        if (__builtin_amdgcn_ballot_w64(!(top_r < __builtin_inff()))) {
+            uint64_t found = 0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    found |= __builtin_fabsf(R[t][j]) < __builtin_inff() ? 0ull : 1ull << (16 * t + 4 * b + j);
+            found |= __shfl_xor(found, 16);
+            found |= __shfl_xor(found, 32);
+            if constexpr (TREE) {
+                for (int row = 0; row < kChunk; ++row)
+                    if (lds_get<uint64_t>(val + C::kRows + C::kKin + 8 * row) & found) lost |= 1ull << row;
+            } else {
+                lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
+            }
+            top_r = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    R[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? 0.f : R[t][j];
+                    top_r = fmaxf(top_r, __builtin_fabsf(R[t][j]));
+                }
+            top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
+            top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
+        }
+        // a power of two for R, and with it for the next S: not so far up that S leaves fp32
+        const float gamma = lds_get<float>(val + C::kRows + C::kLast);
+        const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
+        const int up_r = min(kTop - max(exponent(top_r), -100), 90 - (top_s - power) - weigh_up - kTop);
+        const float by_r = times2(1.0f, up_r);
+
+        // ---- U = T R (times 2^(up_r + a power for each row)) ----
+        f4 U[4];
+        {
+            const Split r0 = split(R[0], R[1], by_r), r1 = split(R[2], R[3], by_r);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int d = 0; d <= t / 2; ++d) {
+                    const h8 hi = lds_get<h8>(val + C::kHigh + 1024 * tile_of(t, d) + 16 * lane);
+                    const h8 lo = lds_get<h8>(val + C::kLow + 1024 * tile_of(t, d) + 16 * lane);
+                    const Split &r = d ? r1 : r0;
+                    u = mfma16x16x32(hi, r.hi, u);
+                    u = mfma16x16x32(hi, r.lo, u);
+                    u = mfma16x16x32(lo, r.hi, u);
+                }
+                U[t] = u;
+            }
+        }
+
+        // ---- O ----
+        {
+            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
+            h8 u[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int d = 0; d <= t / 2; ++d)
+                    o = mfma16x16x32(lds_get<h8>(val + C::kWithin + 1024 * tile_of(t, d) + 16 * lane), u[d], o);
+                const f4 fs = lds_get<f4>(rows + C::kFromS + 64 * t), fu = lds_get<f4>(rows + C::kFromU + 64 * t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 16 * t + 4 * b + j;
+                    float y = times2(fs[j] * qs[t][j], from_s) + times2(fu[j] * o[j], 20 - up_r);
+                    if (lost >> row & 1) y = __builtin_nanf("");
+                    if (row < n) outs[(int64_t)(kChunk * ci + row) * a.out_stride] = (uint16_t)pack2<BF>(y, 0.f);
+                }
+            }
+        }
+
+        // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
+        if constexpr (!TREE) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const f4 w = lds_get<f4>(rows + C::kWeigh + 64 * t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) U[t][j] *= w[j];
+            }
+            const Split u0 = split(U[0], U[1], 1.0f), u1 = split(U[2], U[3], 1.0f);
+            const int next = up_r + weigh_up;
+            const int by = next - power;
+            power = next;
+#pragma unroll
+            for (int t = 0; t < kRowTiles; ++t) {
+                f4 acc;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = times2(S[t][j] * gamma, by);
+                const h8 k0 = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t)), k1 = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t + 1));
+                acc = mfma16x16x32(k0, u0.hi, acc);
+                acc = mfma16x16x32(k1, u1.hi, acc);
+                acc = mfma16x16x32(k0, u0.lo, acc);
+                S[t] = mfma16x16x32(k1, u1.lo, acc);
+            }
+            if (__builtin_amdgcn_ballot_w64(lost != 0)) {
+#pragma unroll
+                for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[t][j] = lost ? __builtin_nanf("") : S[t][j];
+            }
+        }
+    }
+    wait_loads<0>();
+    if constexpr (!TREE) {
+        if (s.state < 0 && s.n - first <= kChunk * seg.chunks) return;     // (kept for the next segment only)
+        float *const to = pool + (int64_t)(4 * b) * a.value_dim + col;
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[(int64_t)(16 * t + j) * a.value_dim] = times2(S[t][j], -power);
+    }
+}
+
+size_t key_bytes(const DeltaArgs &a) { return a.key_dim == 64 ? Chunk<64>::kKey : Chunk<128>::kKey; }
+size_t chunk_bytes(const DeltaArgs &a) { return a.k_heads * key_bytes(a) + (size_t)a.v_heads * Chunk<128>::kValue; }
+int chunks_of(const DeltaArgs &a) { return a.s.tree ? 1 : (a.s.max_q + kChunk - 1) / kChunk; }
+
+// How a call is cut: sequences and chunks of each that the workspace holds at a time.
+struct Cut {
+    int batch, chunks;
+};
+Cut cut_of(const DeltaArgs &a) {
+    constexpr size_t kMost = (size_t)256 << 20;
+    const size_t slots = std::max<size_t>(1, kMost / chunk_bytes(a));
+    Cut c;
+    c.chunks = (int)std::min<size_t>(chunks_of(a), slots);
+    c.batch = (int)std::min<size_t>(a.s.batch, std::max<size_t>(1, slots / c.chunks));
+    return c;
+}
+
+}  // namespace
+
+size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
+    const Cut c = cut_of(a);
+    size_t bytes = chunk_bytes(a) * c.chunks * c.batch;
+    if (c.chunks < chunks_of(a)) bytes += (size_t)c.batch * a.v_heads * a.key_dim * a.value_dim * 4;
+    return bytes;
+}
+
+hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
+    const Cut c = cut_of(a);
+    auto go = [&](auto bf, auto dk, auto tree) {
+        constexpr int kWaves = 4;
+        Segment seg;
+        seg.keys = static_cast<uint8_t *>(a.workspace);
+        seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<dk()>::kKey;
+        seg.carry = reinterpret_cast<float *>(seg.values + (size_t)c.chunks * c.batch * a.v_heads * Chunk<dk()>::kValue);
+        for (int b0 = 0; b0 < a.s.batch; b0 += c.batch) {
+            for (int c0 = 0; c0 < chunks_of(a); c0 += c.chunks) {
+                seg.first_seq = b0;
+                seg.batch = std::min(c.batch, a.s.batch - b0);
+                seg.first_chunk = c0;
+                seg.chunks = std::min(c.chunks, chunks_of(a) - c0);
+                chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
+                hipError_t e = hipGetLastError();
+                if (e != hipSuccess) return e;
+                chunk_scan_kernel<bf(), dk(), tree(), kWaves>
+                    <<<dim3(a.value_dim / (16 * kWaves), a.v_heads, seg.batch), 64 * kWaves, 0, stream>>>(a, seg);
+                e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
+        }
+        return hipSuccess;
+    };
+    auto sized = [&](auto bf, auto tree) {
+        return a.key_dim == 64 ? go(bf, std::integral_constant<int, 64>{}, tree) : go(bf, std::integral_constant<int, 128>{}, tree);
+    };
+    auto typed = [&](auto tree) { return a.bf16 ? sized(std::true_type{}, tree) : sized(std::false_type{}, tree); };
+    return a.s.tree ? typed(std::true_type{}) : typed(std::false_type{});
+}
+
+}  // namespace w4a16

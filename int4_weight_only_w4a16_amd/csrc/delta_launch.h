@@ -49,7 +49,10 @@ struct DeltaArgs {
     bool bf16 = false, unit = false;
     void *workspace = nullptr;
 };
-// Token by token, the state in registers.
+// Token by token, the state in registers, for a few tokens of each sequence (no tree).
 hipError_t launch_delta_step(const DeltaArgs &a, hipStream_t stream);
+// 64 tokens at a time, or a tree.
+size_t delta_chunk_workspace_bytes(const DeltaArgs &a);
+hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream);
 
 }  // namespace w4a16

@@ -44,29 +44,25 @@ __device__ __forceinline__ void to_unit(float (&x)[N], float eps) {
     for (int i = 0; i < N; ++i) x[i] = (float)(x[i] * f);
 }
 
-template <bool BF, int DK, bool TREE>
+template <bool BF, int DK>
 __global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
     constexpr int kRows = DK / 16;
     const int lane = threadIdx.x, r = lane >> 2, col = blockIdx.x * kColumns + 4 * (lane & 3);
     const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
     Seq s;
     if (!seq_of(a.s, blockIdx.z, &s)) return;
-    if (TREE) s.n = min(s.n, 64);
 
     float *const state = a.state + ((max(s.state, (int64_t)0) * a.v_heads + h) * DK + kRows * r) * a.value_dim + col;
-    f4 S[kRows], begin[TREE ? kRows : 1];
+    f4 S[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
         S[i] = s.fresh ? f4{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const f4 *>(state + (int64_t)i * a.value_dim);
-    if constexpr (TREE)
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) begin[i] = S[i];
     const float rate = a.a_log ? expf(a.a_log[h]) : 0.f, bias = a.a_log ? a.dt_bias[h] : 0.f;
     const uint16_t *const q0 = static_cast<const uint16_t *>(a.q) + hk * DK + kRows * r;
     const uint16_t *const k0 = static_cast<const uint16_t *>(a.k) + hk * DK + kRows * r;
     const uint16_t *const v0 = static_cast<const uint16_t *>(a.v) + h * a.value_dim + col;
 
-    auto token = [&](int t, bool want) {
+    auto token = [&](int t) {
         const int64_t row = s.first + t;
         float q[kRows], k[kRows], v[4];
 #pragma unroll
@@ -112,25 +108,14 @@ __global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
         for (int e = 0; e < 4; ++e) u[e] = gate.beta * (v[e] - keep * sk[e]);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) S[i] = keep * S[i] + k[i] * u;
-        if (want && r == 0) {
+        if (r == 0) {
             const f4 o = a.scale * (keep * sq + qk * u);
             *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + row * a.out_stride + (int64_t)h * a.value_dim + col) =
                 pack4<BF>(o[0], o[1], o[2], o[3]);
         }
     };
 
-    if constexpr (TREE) {
-        for (int t = 0; t < s.n; ++t) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) S[i] = begin[i];
-            const uint64_t word = (uint64_t)a.s.tree[s.first + t];
-            for (int j = 0; j < t; ++j)
-                if (word >> j & 1) token(j, false);
-            token(t, true);
-        }
-        return;
-    }
-    for (int t = 0; t < s.n; ++t) token(t, true);
+    for (int t = 0; t < s.n; ++t) token(t);
     if (s.state < 0) return;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) *reinterpret_cast<f4 *>(state + (int64_t)i * a.value_dim) = S[i];
@@ -141,10 +126,7 @@ __global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
 hipError_t launch_delta_step(const DeltaArgs &a, hipStream_t stream) {
     const dim3 grid(a.value_dim / kColumns, a.v_heads, a.s.batch);
     auto go = [&](auto bf, auto dk) {
-        if (a.s.tree)
-            step_kernel<bf(), dk(), true><<<grid, 64, 0, stream>>>(a);
-        else
-            step_kernel<bf(), dk(), false><<<grid, 64, 0, stream>>>(a);
+        step_kernel<bf(), dk()><<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     };
     auto typed = [&](auto dk) { return a.bf16 ? go(std::true_type{}, dk) : go(std::false_type{}, dk); };
