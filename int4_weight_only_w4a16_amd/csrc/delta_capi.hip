@@ -117,6 +117,8 @@ extern "C" int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, 
     if (st == W4A16_OK) st = check_stride(v_stride, v_heads * value_dim);
     if (st == W4A16_OK) st = check_stride(out_stride, v_heads * value_dim);
     if (st != W4A16_OK) return st;
+    // (a chunk's rows are reached by 32-bit offsets)
+    if (v_stride >= 1 << 23 || out_stride >= 1 << 23) return W4A16_ERR_SHAPE;
     if (!in_range(a_stride, v_heads) || !in_range(b_stride, v_heads) || !std::isfinite(scale) || !(scale > 0.f) ||
         !(eps >= 0.f) || !std::isfinite(eps))
         return W4A16_ERR_SHAPE;

@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kChunk = 64;
 constexpr int kTop = 14;               // operands lie below 2^kTop
+constexpr int kDownT = 15;             // K^T lies so much lower
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Workspace of one chunk: for each key head K, K^T and Q as operands (tiles of 1 KiB: 64 lanes x 16
@@ -100,11 +101,16 @@ __device__ __forceinline__ Split split(const f4 &x, const f4 &y, float by) {
 }
 
 template <bool BF, int DK, bool TREE>
-__global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment seg) {
+__global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kStride = DK + 8, kA = 68, kP = 72;
-    __shared__ __align__(16) _Float16 K[kChunk][kStride], Q[kChunk][kStride];
-    __shared__ __align__(16) float A[kChunk][kA], X[kChunk][kA];
+    // keys and queries, and then in their place A and X
+    constexpr int kPart = kChunk * (2 * kStride > 4 * kA ? 2 * kStride : 4 * kA);
+    __shared__ __align__(16) uint8_t shared[2][kPart];
+    auto &K = *reinterpret_cast<_Float16(*)[kChunk][kStride]>(shared[0]);
+    auto &Q = *reinterpret_cast<_Float16(*)[kChunk][kStride]>(shared[1]);
+    auto &A = *reinterpret_cast<float(*)[kChunk][kA]>(shared[0]);
+    auto &X = *reinterpret_cast<float(*)[kChunk][kA]>(shared[1]);
     __shared__ double G[kChunk];
     __shared__ float beta[kChunk], kf[kChunk], qf[kChunk];
     __shared__ int tau[kChunk];
@@ -207,6 +213,24 @@ __global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment se
     }
     __syncthreads();
 
+    // ---- keys and queries as operands, once for each key head ----
+    if (h % r == 0) {
+#pragma unroll
+        for (int i = 0; i < C::kTiles / 4; ++i) {
+            const int tile = 4 * i + wave;                     // of K and Q: [row tile][DK / 32]
+            const int row = 16 * (tile / (DK / 32)) + m, ch = 32 * (tile % (DK / 32)) + 4 * b;
+            const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
+            const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
+            *reinterpret_cast<h8 *>(to_key + 1024 * tile + 16 * lane) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
+            *reinterpret_cast<h8 *>(to_key + 1024 * (2 * C::kTiles + tile) + 16 * lane) =
+                __builtin_shufflevector(q0, q1, 0, 1, 2, 3, 4, 5, 6, 7);
+            h8 kt;                                             // of K^T: [16 channels][32 tokens]
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kt[e] = K[place(tile & 1, b, e)][16 * (tile >> 1) + m] * (_Float16)(1.0f / (1 << kDownT));
+            *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) = kt;
+        }
+    }
+
     // ---- products of keys with keys and queries; lane (m, b): rows 16 wave + 4 b + j, column 16 nt + m ----
     f4 p[4];
     {
@@ -227,6 +251,7 @@ __global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment se
         }
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
+            if (nt == 0) __syncthreads();      // (keys and queries are done with)
             if (nt > wave) continue;
             const int col = 16 * nt + m;
             const double gc = G[col];
@@ -344,11 +369,11 @@ __global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment se
     if (tid < kChunk) {
         float *const rows = reinterpret_cast<float *>(to + C::kRows);
         const float grow = exp_f32((float)G[tid]), nan = __builtin_nanf("");
-        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], -tau[tid]);
+        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], kDownT - tau[tid]);
         float top = weigh;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const int up = -20 - max(exponent(top), -120);
+        const int up = -24 - max(exponent(top), -120);
         rows[C::kOff / 4 + tid] = bad[tid] & 1 ? nan : grow * kf[tid];
         rows[C::kWeigh / 4 + tid] = times2(weigh, up);
         rows[C::kFromS / 4 + tid] = bad[tid] & 2 ? nan : a.scale * qf[tid] * grow;
@@ -359,36 +384,33 @@ __global__ void __launch_bounds__(256) chunk_prep_kernel(DeltaArgs a, Segment se
             reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
         }
     }
-
-    // ---- keys and queries as operands, once for each key head ----
-    if (h % r != 0) return;
-#pragma unroll
-    for (int i = 0; i < C::kTiles / 4; ++i) {
-        const int tile = 4 * i + wave;                     // of K and Q: [row tile][DK / 32]
-        const int row = 16 * (tile / (DK / 32)) + m, ch = 32 * (tile % (DK / 32)) + 4 * b;
-        const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
-        const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
-        *reinterpret_cast<h8 *>(to_key + 1024 * tile + 16 * lane) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
-        *reinterpret_cast<h8 *>(to_key + 1024 * (2 * C::kTiles + tile) + 16 * lane) =
-            __builtin_shufflevector(q0, q1, 0, 1, 2, 3, 4, 5, 6, 7);
-        h8 kt;                                             // of K^T: [16 channels][32 tokens]
-#pragma unroll
-        for (int e = 0; e < 8; ++e) kt[e] = K[place(tile & 1, b, e)][16 * (tile >> 1) + m];
-        *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) = kt;
-    }
 }
 
 // The largest size in a column's lanes; NaN if there is one.
 __device__ __forceinline__ float top_of_column(float v) {
-    v = __builtin_elementwise_maximum(v, __shfl_xor(v, 16));
-    return __builtin_elementwise_maximum(v, __shfl_xor(v, 32));
+    const uint32_t bits = __float_as_uint(v);
+    const auto halves = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+    const float w = __builtin_elementwise_maximum(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
+    const uint32_t half = __float_as_uint(w);
+    const auto rows = __builtin_amdgcn_permlane16_swap(half, half, false, false);
+    return __builtin_elementwise_maximum(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+}
+
+// Four rows of one column of an LDS tile [rows][16 WAVES columns] of 16-bit values: lane (m, b) hands in the
+// place of row m / 4, columns 4 (m % 4) .. of its group's block and gets column m of all four.
+typedef short s4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u2 read_column(const lds_u8 *p) {
+    typedef __attribute__((address_space(3))) s4 lds_s4;
+    return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)const_cast<lds_u8 *>(p)));
 }
 
 template <bool BF, int DK, bool TREE, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
-    __shared__ __align__(16) uint8_t lds_raw[2 * (C::kKey + C::kValue)];     // two chunks
+    // two chunks, each with V's columns of this workgroup, in whose place their outputs come
+    constexpr int kColumnBytes = 32 * WAVES, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
+    __shared__ __align__(16) uint8_t lds_raw[2 * kStage];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
     const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
@@ -402,93 +424,132 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
     const int col = 16 * (blockIdx.x * WAVES + wave) + m;
     const int64_t slot = (int64_t)blockIdx.z * seg.chunks;
+    // rows of V and of the output by offsets from a chunk's first (the host keeps strides below 2^23 elements)
+    constexpr int kUnits = kColumnBytes / 16;          // 16-byte units of a row
+    const int v_row = 2 * (int)a.v_stride, out_row = 2 * (int)a.out_stride;
+    const int v_at = lane / kUnits * v_row + 16 * (lane % kUnits);
     auto copy = [&](int ci) {
         const uint8_t *const key = seg.keys + ((slot + ci) * a.k_heads + hk) * C::kKey;
         const uint8_t *const value = seg.values + ((slot + ci) * a.v_heads + h) * C::kValue;
-        lds_u8 *const to = lds + (ci & 1) * (C::kKey + C::kValue);
+        lds_u8 *const to = lds + (ci & 1) * kStage;
+        static_assert(C::kKey / 1024 % WAVES == 0 && C::kValue / 1024 % WAVES == 0, "the same in every wave");
 #pragma unroll
-        for (int u = 0; u < C::kUnits; u += WAVES) {
-            const int unit = u + wave;
-            if (unit < C::kKey / 1024)
-                copy_kib(key, C::kKey, 1024 * unit, to + 1024 * unit, lane);
-            else if (unit < C::kUnits)
-                copy_kib(value, C::kValue, 1024 * unit - C::kKey, to + 1024 * unit, lane);
-        }
+        for (int u = 0; u < C::kKey; u += 1024 * WAVES)
+            copy_kib(key, C::kKey, u + 1024 * wave, to + u + 1024 * wave, lane);
+#pragma unroll
+        for (int u = 0; u < C::kValue; u += 1024 * WAVES)
+            copy_kib(value, C::kValue, u + 1024 * wave, to + C::kKey + u + 1024 * wave, lane);
+        // rows past the sequence's come as zeros
+        const int n = min(kChunk, s.n - first - kChunk * ci);
+        const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.v) + (s.first + first + (int64_t)kChunk * ci) * a.v_stride +
+                                        h * a.value_dim + blockIdx.x * (16 * WAVES),
+                                    (uint32_t)((n - 1) * v_row + kColumnBytes));
+#pragma unroll
+        for (int i = 0; i < kTile / 1024 / WAVES; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + C::kKey + C::kValue + 1024 * (WAVES * i + wave)), 16,
+                                                     v_at + (WAVES * i + wave) * (1024 / kColumnBytes) * v_row, 0, 0, 0);
     };
     copy(0);
 
-    // S 2^power, lane (m, b): rows 16 t + 4 b + j of its column
+    // S 2^power, below 2^16; lane (m, b): rows 16 t + 4 b + j of its column
     f4 S[kRowTiles];
-    int power = 0;
+    int power;
     float *const pool = s.state < 0 ? seg.carry + ((int64_t)blockIdx.z * a.v_heads + h) * DK * a.value_dim
                                     : a.state + (s.state * a.v_heads + h) * DK * a.value_dim;
     {
         const bool zero = seg.first_chunk == 0 && s.fresh;
         const float *const from = pool + (int64_t)(4 * b) * a.value_dim + col;
-#pragma unroll
-        for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S[t][j] = zero ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
-    }
-    const uint16_t *const values = static_cast<const uint16_t *>(a.v) + (s.first + first) * a.v_stride +
-                                   (int64_t)h * a.value_dim + col;
-    uint16_t *const outs = static_cast<uint16_t *>(a.out) + (s.first + first) * a.out_stride +
-                           (int64_t)h * a.value_dim + col;
-
-    for (int ci = 0; ci < count; ++ci) {
-        const int n = min(kChunk, s.n - first - kChunk * ci);
-        wait_loads<0>();
-        lds_barrier();                         // this chunk is there, and the other one is done with
-        if (ci + 1 < count) copy(ci + 1);
-        const lds_u8 *const at = lds + (ci & 1) * (C::kKey + C::kValue), *const mine = at + 16 * lane;
-        const lds_u8 *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
-        f4 V[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 16 * t + 4 * b + j;
-                V[t][j] = row < n ? lo_f32<BF>(values[(int64_t)(kChunk * ci + row) * a.v_stride]) : 0.f;
-            }
-
-        // ---- K S and Q S ----
         float top = 0.f;
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = __builtin_elementwise_maximum(top, __builtin_fabsf(S[t][j]));
-        top = top_of_column(top);
-        const int top_s = max(exponent(top), -100);
-        const float by_s = times2(1.0f, kTop - top_s);
-        f4 ks[4], qs[4];
+            for (int j = 0; j < 4; ++j) {
+                S[t][j] = zero ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
+                top = fmaxf(top, __builtin_fabsf(S[t][j]));
+            }
+        power = kTop - max(exponent(top_of_column(top)), -100);
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][j] = times2(S[t][j], power);
+    }
+
+    for (int ci = 0; ci < count; ++ci) {
+        // this chunk is there (the two stores of the last outputs may be under way), and the other one done with
+        if (ci == 0) wait_loads<0>();
+        else wait_loads<2>();
+        lds_barrier();
+        if (ci + 1 < count) copy(ci + 1);
+        lds_u8 *const at = lds + (ci & 1) * kStage, *const mine = at + 16 * lane;
+        const lds_u8 *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
+        lds_u8 *const tile = at + C::kKey + C::kValue + 32 * wave;         // this wave's columns
+
+        // Operands come out of LDS a step ahead of the products that take them, and products that add to one
+        // tile lie apart, so that a single wave keeps the matrix core fed (the barriers hold the order).
+        constexpr int kHold = 0;
+        h8 kq[2][8];                           // K and Q of 32 channels: four row tiles each
+        auto load_kq = [&](int d) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                kq[d & 1][t] = lds_get<h8>(mine + 1024 * (t * kSteps + d));
+                kq[d & 1][4 + t] = lds_get<h8>(mine + 1024 * (2 * C::kTiles + t * kSteps + d));
+            }
+        };
+        load_kq(0);
+        u2 V[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) V[t] = read_column(tile + (16 * t + 4 * b + (m >> 2)) * kColumnBytes + 8 * (m & 3));
+        const float gamma = lds_get<float>(val + C::kRows + C::kLast);
+        const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
+        __builtin_amdgcn_sched_barrier(kHold);
+
+        // ---- K S and Q S ----
+        f4 ks[4], qs[4], off[4];
+        h8 th[6], tl[6];
 #pragma unroll
         for (int t = 0; t < 4; ++t) ks[t] = qs[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < kSteps; ++d) {
-            const Split x = split(S[2 * d], S[2 * d + 1], by_s);
+            if (d + 1 < kSteps) {
+                load_kq(d + 1);
+            } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const h8 k = lds_get<h8>(mine + 1024 * (t * kSteps + d));
-                const h8 q = lds_get<h8>(mine + 1024 * (2 * C::kTiles + t * kSteps + d));
-                ks[t] = mfma16x16x32(k, x.hi, ks[t]);
-                ks[t] = mfma16x16x32(k, x.lo, ks[t]);
-                qs[t] = mfma16x16x32(q, x.hi, qs[t]);
+                for (int t = 0; t < 4; ++t) off[t] = lds_get<f4>(rows + C::kOff + 64 * t);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) {
+                    th[i] = lds_get<h8>(val + C::kHigh + 1024 * i + 16 * lane);
+                    tl[i] = lds_get<h8>(val + C::kLow + 1024 * i + 16 * lane);
+                }
             }
+            __builtin_amdgcn_sched_barrier(kHold);
+            const Split x = split(S[2 * d], S[2 * d + 1], 1.0f);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(kq[d & 1][t], x.hi, ks[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(kq[d & 1][4 + t], x.hi, qs[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(kq[d & 1][t], x.lo, ks[t]);
+            __builtin_amdgcn_sched_barrier(kHold);
         }
-        const int from_s = top_s - kTop - power;           // S's own power of two
+        float top_s = 0.f;                     // for the next S
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top_s = __builtin_elementwise_maximum(top_s, __builtin_fabsf(S[t][j]));
+        top_s = gamma * top_of_column(top_s);
 
         // ---- R = V - e^G K S, its rows as operands ----
+        const float of_s = times2(1.0f, -power);
         f4 R[4];
         float top_r = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f4 off = lds_get<f4>(rows + C::kOff + 64 * t);
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                R[t][j] = V[t][j] - times2(off[j] * ks[t][j], from_s);
+                const float v = j & 1 ? hi_f32<BF>(V[t][j >> 1]) : lo_f32<BF>(V[t][j >> 1]);
+                R[t][j] = __builtin_fmaf(-(off[t][j] * of_s), ks[t][j], v);
                 top_r = __builtin_elementwise_maximum(top_r, __builtin_fabsf(R[t][j]));
             }
-        }
         top_r = top_of_column(top_r);
         uint64_t lost = 0;                     // rows that come after one that is not finite
         if (__builtin_amdgcn_ballot_w64(!(top_r < __builtin_inff()))) {
@@ -517,86 +578,119 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
             top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
             top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
         }
-        // a power of two for R, and with it for the next S: not so far up that S leaves fp32
-        const float gamma = lds_get<float>(val + C::kRows + C::kLast);
-        const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
-        const int up_r = min(kTop - max(exponent(top_r), -100), 90 - (top_s - power) - weigh_up - kTop);
+        // A power of two for R, and with it for the next S, which has at most 2^14 from this one and 2^15 from
+        // U: 64 products of K^T (below 1/2) and rows that lie below 2^10.
+        const int next = min(kTop - max(exponent(top_r), -100) + weigh_up,
+                             power + kTop - (top_s > 0.f ? exponent(top_s) : -200));
+        const int up_r = next - weigh_up;
         const float by_r = times2(1.0f, up_r);
 
         // ---- U = T R (times 2^(up_r + a power for each row)) ----
-        f4 U[4];
+        f4 U[4], fs[4], fu[4], weigh[4];
+        h8 within[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (!TREE) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
+            fs[t] = lds_get<f4>(rows + C::kFromS + 64 * t);
+            fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
+        }
+        __builtin_amdgcn_sched_barrier(kHold);
         {
             const Split r0 = split(R[0], R[1], by_r), r1 = split(R[2], R[3], by_r);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f4 u = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) U[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int d = 0; d <= t / 2; ++d) {
-                    const h8 hi = lds_get<h8>(val + C::kHigh + 1024 * tile_of(t, d) + 16 * lane);
-                    const h8 lo = lds_get<h8>(val + C::kLow + 1024 * tile_of(t, d) + 16 * lane);
-                    const Split &r = d ? r1 : r0;
-                    u = mfma16x16x32(hi, r.hi, u);
-                    u = mfma16x16x32(hi, r.lo, u);
-                    u = mfma16x16x32(lo, r.hi, u);
-                }
-                U[t] = u;
-            }
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int t = 2 * d; t < 4; ++t) {
+                        const Split &r = d ? r1 : r0;
+                        U[t] = mfma16x16x32(part < 2 ? th[tile_of(t, d)] : tl[tile_of(t, d)], part == 1 ? r.lo : r.hi, U[t]);
+                    }
         }
+        __builtin_amdgcn_sched_barrier(kHold);
 
-        // ---- O ----
+        // ---- O, and S <- e^G_last S + (e^(G_last - G) K)^T U ----
+        h8 kt[kRowTiles][2];
+        if constexpr (!TREE)
+#pragma unroll
+            for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                for (int d = 0; d < 2; ++d) kt[t][d] = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t + d));
+        __builtin_amdgcn_sched_barrier(kHold);
+        constexpr float kDown = 1.0f / (1 << 20);          // U lies below 2^34: 64 products of 2^14 each
+        f4 o[4];
         {
-            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
             h8 u[2];
 #pragma unroll
             for (int d = 0; d < 2; ++d)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f4 o = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int d = 0; d <= t / 2; ++d)
-                    o = mfma16x16x32(lds_get<h8>(val + C::kWithin + 1024 * tile_of(t, d) + 16 * lane), u[d], o);
-                const f4 fs = lds_get<f4>(rows + C::kFromS + 64 * t), fu = lds_get<f4>(rows + C::kFromU + 64 * t);
+            for (int d = 0; d < 2; ++d)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = 16 * t + 4 * b + j;
-                    float y = times2(fs[j] * qs[t][j], from_s) + times2(fu[j] * o[j], 20 - up_r);
-                    if (lost >> row & 1) y = __builtin_nanf("");
-                    if (row < n) outs[(int64_t)(kChunk * ci + row) * a.out_stride] = (uint16_t)pack2<BF>(y, 0.f);
-                }
-            }
+                for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
         }
-
-        // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
         if constexpr (!TREE) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f4 w = lds_get<f4>(rows + C::kWeigh + 64 * t);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) U[t][j] *= w[j];
-            }
+                for (int j = 0; j < 4; ++j) U[t][j] *= weigh[t][j];
             const Split u0 = split(U[0], U[1], 1.0f), u1 = split(U[2], U[3], 1.0f);
-            const int next = up_r + weigh_up;
-            const int by = next - power;
+            const float by = times2(gamma, next - power);
             power = next;
 #pragma unroll
-            for (int t = 0; t < kRowTiles; ++t) {
-                f4 acc;
+            for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = times2(S[t][j] * gamma, by);
-                const h8 k0 = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t)), k1 = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t + 1));
-                acc = mfma16x16x32(k0, u0.hi, acc);
-                acc = mfma16x16x32(k1, u1.hi, acc);
-                acc = mfma16x16x32(k0, u0.lo, acc);
-                S[t] = mfma16x16x32(k1, u1.lo, acc);
-            }
+                for (int j = 0; j < 4; ++j) S[t][j] *= by;
+#pragma unroll
+            for (int part = 0; part < 4; ++part)
+#pragma unroll
+                for (int t = 0; t < kRowTiles; ++t)
+                    S[t] = mfma16x16x32(kt[t][part & 1], part == 0 ? u0.hi : part == 1 ? u1.hi : part == 2 ? u0.lo : u1.lo, S[t]);
             if (__builtin_amdgcn_ballot_w64(lost != 0)) {
 #pragma unroll
                 for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) S[t][j] = lost ? __builtin_nanf("") : S[t][j];
             }
+        }
+        const float of_u = times2(1.0f, 20 - up_r);
+        f4 y[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * o[t][j]);
+        if (__builtin_amdgcn_ballot_w64(lost != 0)) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
+        }
+        // through LDS, so that a lane stores eight columns of a row
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
+                lds_u8 *const to = tile + (16 * t + 4 * b + j) * kColumnBytes + 2 * m;
+                lds_put(to, (uint16_t)two);
+                lds_put(to + kColumnBytes, (uint16_t)(two >> 16));
+            }
+        const int n = min(kChunk, s.n - first - kChunk * ci);
+        const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
+                                        h * a.value_dim + blockIdx.x * (16 * WAVES) + 16 * wave,
+                                    (uint32_t)((n - 1) * out_row + 32));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 32 * i + (lane >> 1);
+            const u4 eight = lds_get<u4>(tile + row * kColumnBytes + 16 * (lane & 1));
+            __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
         }
     }
     wait_loads<0>();
