@@ -38,22 +38,21 @@ namespace {
 
 constexpr int kChunk = 64;
 constexpr int kTop = 14;               // operands lie below 2^kTop
-constexpr int kDownT = 15;             // K^T lies so much lower
+constexpr int kTopK = 0;               // and keys below 2^kTopK
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Workspace of one chunk: for each key head K, K^T and Q as operands (tiles of 1 KiB: 64 lanes x 16
+// Workspace of one chunk: for each key head K and Q as operands (tiles of 1 KiB: 64 lanes x 16
 // bytes), for each value head T in two parts, the products with the queries (the six tiles of 16 x 32
 // that are not above the diagonal), and what goes by rows.
 template <int DK>
 struct Chunk {
-    static constexpr int kTiles = DK / 8;                      // of K, K^T and Q each
-    static constexpr int kKey = 3 * kTiles * 1024;
+    static constexpr int kTiles = DK / 8;                      // of K and Q each
+    static constexpr int kKey = 2 * kTiles * 1024;
     static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRows = 18 * 1024;
     static constexpr int kValue = 20 * 1024;
     // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
     // output of S and of U; words of a tree; e^G_last and the power of two in the second of them
     static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kKin = 1024, kLast = 1536;
-    static constexpr int kUnits = (kKey + kValue) / 1024;
 };
 
 // The part of a call that one launch works on: `chunks` chunks from the first_chunk-th of `batch`
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             top = max(top, (uint32_t)__shfl_xor((int)top, 1));
             top = max(top, (uint32_t)__shfl_xor((int)top, 2));
             const bool fine = top < limit;
-            const int up = fine && top ? kTop - exponent(lo_f32<BF>(top)) : 0;
+            const int up = fine && top ? (which ? kTop : kTopK) - exponent(lo_f32<BF>(top)) : 0;
             float sum = 0.f;
             _Float16 *const dst = (which ? Q[row] : K[row]) + part;
 #pragma unroll
@@ -222,12 +221,8 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
             const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
             *reinterpret_cast<h8 *>(to_key + 1024 * tile + 16 * lane) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
-            *reinterpret_cast<h8 *>(to_key + 1024 * (2 * C::kTiles + tile) + 16 * lane) =
+            *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) =
                 __builtin_shufflevector(q0, q1, 0, 1, 2, 3, 4, 5, 6, 7);
-            h8 kt;                                             // of K^T: [16 channels][32 tokens]
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kt[e] = K[place(tile & 1, b, e)][16 * (tile >> 1) + m] * (_Float16)(1.0f / (1 << kDownT));
-            *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) = kt;
         }
     }
 
@@ -369,11 +364,11 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     if (tid < kChunk) {
         float *const rows = reinterpret_cast<float *>(to + C::kRows);
         const float grow = exp_f32((float)G[tid]), nan = __builtin_nanf("");
-        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], kDownT - tau[tid]);
+        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], -tau[tid]);
         float top = weigh;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const int up = -24 - max(exponent(top), -120);
+        const int up = -25 - max(exponent(top), -120);
         rows[C::kOff / 4 + tid] = bad[tid] & 1 ? nan : grow * kf[tid];
         rows[C::kWeigh / 4 + tid] = times2(weigh, up);
         rows[C::kFromS / 4 + tid] = bad[tid] & 2 ? nan : a.scale * qf[tid] * grow;
@@ -404,13 +399,19 @@ __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)const_cast<lds_u8 *>(p)));
 }
 
-template <bool BF, int DK, bool TREE, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Segment seg) {
+// A workgroup walks over the chunks with 16 GROUPS columns of one head.  Wave w < GROUPS takes what the
+// next state needs, for sixteen columns; wave GROUPS + w, on the same SIMD, their outputs, from the state and
+// the rows U that the first hands over in LDS, and the copies.  (All in one wave, the only one on its SIMD,
+// a chunk took 9300 cycles, of which instructions took 3300.)
+template <bool BF, int DK, bool TREE, int GROUPS>
+__global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
-    // two chunks, each with V's columns of this workgroup, in whose place their outputs come
-    constexpr int kColumnBytes = 32 * WAVES, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
-    __shared__ __align__(16) uint8_t lds_raw[2 * kStage];
+    // two chunks, each with V's columns of this workgroup, in whose place their outputs come; and for each
+    // group the state and U as operands, what comes off their sums, and rows that are lost
+    constexpr int kColumnBytes = 32 * GROUPS, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
+    constexpr int kFactors = (kSteps + 2) * 1024, kHand = kFactors + 1024;
+    __shared__ __align__(16) uint8_t lds_raw[2 * kStage + GROUPS * kHand];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
     const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
@@ -421,37 +422,121 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
     if (first >= s.n) return;
     const int count = min(seg.chunks, (s.n - first + kChunk - 1) / kChunk);
 
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
-    const int col = 16 * (blockIdx.x * WAVES + wave) + m;
-    const int64_t slot = (int64_t)blockIdx.z * seg.chunks;
-    // rows of V and of the output by offsets from a chunk's first (the host keeps strides below 2^23 elements)
-    constexpr int kUnits = kColumnBytes / 16;          // 16-byte units of a row
-    const int v_row = 2 * (int)a.v_stride, out_row = 2 * (int)a.out_stride;
-    const int v_at = lane / kUnits * v_row + 16 * (lane % kUnits);
-    auto copy = [&](int ci) {
-        const uint8_t *const key = seg.keys + ((slot + ci) * a.k_heads + hk) * C::kKey;
-        const uint8_t *const value = seg.values + ((slot + ci) * a.v_heads + h) * C::kValue;
-        lds_u8 *const to = lds + (ci & 1) * kStage;
-        static_assert(C::kKey / 1024 % WAVES == 0 && C::kValue / 1024 % WAVES == 0, "the same in every wave");
-#pragma unroll
-        for (int u = 0; u < C::kKey; u += 1024 * WAVES)
-            copy_kib(key, C::kKey, u + 1024 * wave, to + u + 1024 * wave, lane);
-#pragma unroll
-        for (int u = 0; u < C::kValue; u += 1024 * WAVES)
-            copy_kib(value, C::kValue, u + 1024 * wave, to + C::kKey + u + 1024 * wave, lane);
-        // rows past the sequence's come as zeros
-        const int n = min(kChunk, s.n - first - kChunk * ci);
-        const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.v) + (s.first + first + (int64_t)kChunk * ci) * a.v_stride +
-                                        h * a.value_dim + blockIdx.x * (16 * WAVES),
-                                    (uint32_t)((n - 1) * v_row + kColumnBytes));
-#pragma unroll
-        for (int i = 0; i < kTile / 1024 / WAVES; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + C::kKey + C::kValue + 1024 * (WAVES * i + wave)), 16,
-                                                     v_at + (WAVES * i + wave) * (1024 / kColumnBytes) * v_row, 0, 0, 0);
-    };
-    copy(0);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = wave % GROUPS;
+    const int lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
+    const int col = 16 * (blockIdx.x * GROUPS + group) + m;
+    lds_u8 *const hand = lds + 2 * kStage + group * kHand;
+    lds_u8 *const factors = hand + kFactors + 4 * lane, *const lost_at = hand + kFactors + 512 + 8 * lane;
+    constexpr int kHold = 0;                   // of sched_barrier: nothing passes
 
-    // S 2^power, below 2^16; lane (m, b): rows 16 t + 4 b + j of its column
+    if (wave >= GROUPS) {
+        // ======== outputs and copies ========
+        const int64_t slot = (int64_t)blockIdx.z * seg.chunks;
+        // rows of V and of the output by offsets from a chunk's first (the host keeps strides below 2^23 elements)
+        constexpr int kUnits = kColumnBytes / 16;          // 16-byte units of a row
+        const int v_row = 2 * (int)a.v_stride, out_row = 2 * (int)a.out_stride;
+        const int v_at = lane / kUnits * v_row + 16 * (lane % kUnits);
+        auto copy = [&](int ci) {
+            const uint8_t *const key = seg.keys + ((slot + ci) * a.k_heads + hk) * C::kKey;
+            const uint8_t *const value = seg.values + ((slot + ci) * a.v_heads + h) * C::kValue;
+            lds_u8 *const to = lds + (ci & 1) * kStage;
+            static_assert(C::kKey / 1024 % GROUPS == 0 && C::kValue / 1024 % GROUPS == 0, "the same in every wave");
+#pragma unroll
+            for (int u = 0; u < C::kKey; u += 1024 * GROUPS)
+                copy_kib(key, C::kKey, u + 1024 * group, to + u + 1024 * group, lane);
+#pragma unroll
+            for (int u = 0; u < C::kValue; u += 1024 * GROUPS)
+                copy_kib(value, C::kValue, u + 1024 * group, to + C::kKey + u + 1024 * group, lane);
+            // rows past the sequence's come as zeros
+            const int n = min(kChunk, s.n - first - kChunk * ci);
+            const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.v) + (s.first + first + (int64_t)kChunk * ci) * a.v_stride +
+                                            h * a.value_dim + blockIdx.x * (16 * GROUPS),
+                                        (uint32_t)((n - 1) * v_row + kColumnBytes));
+#pragma unroll
+            for (int i = 0; i < kTile / 1024 / GROUPS; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + C::kKey + C::kValue + 1024 * (GROUPS * i + group)), 16,
+                                                         v_at + (GROUPS * i + group) * (1024 / kColumnBytes) * v_row, 0, 0, 0);
+        };
+        copy(0);
+        for (int ci = 0; ci < count; ++ci) {
+            // this chunk is there; the two stores of the last outputs may be under way
+            if (ci == 0) wait_loads<0>();
+            else wait_loads<2>();
+            lds_barrier();                     // (1) and the other chunk's place is free
+            if (ci + 1 < count) copy(ci + 1);
+            lds_u8 *const at = lds + (ci & 1) * kStage;
+            const lds_u8 *const mine = at + 16 * lane, *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
+            lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;        // this group's columns
+            h8 q[kSteps][4];
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q[d][t] = lds_get<h8>(mine + 1024 * (C::kTiles + t * kSteps + d));
+            lds_barrier();                     // (2) the state is handed over
+            f4 qs[4], fs[4], fu[4], o[4];
+            h8 within[6], x[kSteps];
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) x[d] = lds_get<h8>(hand + 1024 * d + 16 * lane);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                fs[t] = lds_get<f4>(rows + C::kFromS + 64 * t);
+                fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
+                qs[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
+            }
+            __builtin_amdgcn_sched_barrier(kHold);
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(q[d][t], x[d], qs[t]);
+            lds_barrier();                     // (3) and U
+            h8 u[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) u[d] = lds_get<h8>(hand + 1024 * (kSteps + d) + 16 * lane);
+            const float of_s = lds_get<float>(factors), of_u = lds_get<float>(factors + 256);
+            const uint64_t lost = lds_get<uint64_t>(lost_at);
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
+            f4 y[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * o[t][j]);
+            if (__builtin_amdgcn_ballot_w64(lost != 0)) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
+            }
+            // through LDS, so that a lane stores eight columns of a row
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
+                    lds_u8 *const to = tile + (16 * t + 4 * b + j) * kColumnBytes + 2 * m;
+                    lds_put(to, (uint16_t)two);
+                    lds_put(to + kColumnBytes, (uint16_t)(two >> 16));
+                }
+            const int n = min(kChunk, s.n - first - kChunk * ci);
+            const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
+                                            h * a.value_dim + blockIdx.x * (16 * GROUPS) + 16 * group,
+                                        (uint32_t)((n - 1) * out_row + 32));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 32 * i + (lane >> 1);
+                const u4 eight = lds_get<u4>(tile + row * kColumnBytes + 16 * (lane & 1));
+                __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
+            }
+        }
+        wait_loads<0>();
+        return;
+    }
+
+    // ======== the state: S 2^power, below 2^16; lane (m, b): rows 16 t + 4 b + j of its column ========
     f4 S[kRowTiles];
     int power;
     float *const pool = s.state < 0 ? seg.carry + ((int64_t)blockIdx.z * a.v_heads + h) * DK * a.value_dim
@@ -463,10 +548,11 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                S[t][j] = zero ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
-                top = fmaxf(top, __builtin_fabsf(S[t][j]));
-            }
+            for (int j = 0; j < 4; ++j) S[t][j] = zero ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = fmaxf(top, __builtin_fabsf(S[t][j]));
         power = kTop - max(exponent(top_of_column(top)), -100);
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
@@ -475,46 +561,39 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
     }
 
     for (int ci = 0; ci < count; ++ci) {
-        // this chunk is there (the two stores of the last outputs may be under way), and the other one done with
-        if (ci == 0) wait_loads<0>();
-        else wait_loads<2>();
-        lds_barrier();
-        if (ci + 1 < count) copy(ci + 1);
-        lds_u8 *const at = lds + (ci & 1) * kStage, *const mine = at + 16 * lane;
+        lds_barrier();                         // (1) this chunk is there
+        const lds_u8 *const at = lds + (ci & 1) * kStage, *const mine = at + 16 * lane;
         const lds_u8 *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
-        lds_u8 *const tile = at + C::kKey + C::kValue + 32 * wave;         // this wave's columns
+        const lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;
 
         // Operands come out of LDS a step ahead of the products that take them, and products that add to one
-        // tile lie apart, so that a single wave keeps the matrix core fed (the barriers hold the order).
-        constexpr int kHold = 0;
-        h8 kq[2][8];                           // K and Q of 32 channels: four row tiles each
-        auto load_kq = [&](int d) {
+        // tile lie apart (the scheduling barriers hold the order).
+        h8 k[2][4];                            // K of 32 channels: four row tiles
+        auto load_k = [&](int d) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                kq[d & 1][t] = lds_get<h8>(mine + 1024 * (t * kSteps + d));
-                kq[d & 1][4 + t] = lds_get<h8>(mine + 1024 * (2 * C::kTiles + t * kSteps + d));
-            }
+            for (int t = 0; t < 4; ++t) k[d & 1][t] = lds_get<h8>(mine + 1024 * (t * kSteps + d));
         };
-        load_kq(0);
+        load_k(0);
         u2 V[4];
+        f4 off[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) V[t] = read_column(tile + (16 * t + 4 * b + (m >> 2)) * kColumnBytes + 8 * (m & 3));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) off[t] = lds_get<f4>(rows + C::kOff + 64 * t);
         const float gamma = lds_get<float>(val + C::kRows + C::kLast);
         const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
         __builtin_amdgcn_sched_barrier(kHold);
 
-        // ---- K S and Q S ----
-        f4 ks[4], qs[4], off[4];
+        // ---- K S ----
+        f4 ks[4];
         h8 th[6], tl[6];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) ks[t] = qs[t] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t) ks[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < kSteps; ++d) {
             if (d + 1 < kSteps) {
-                load_kq(d + 1);
+                load_k(d + 1);
             } else {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) off[t] = lds_get<f4>(rows + C::kOff + 64 * t);
 #pragma unroll
                 for (int i = 0; i < 6; ++i) {
                     th[i] = lds_get<h8>(val + C::kHigh + 1024 * i + 16 * lane);
@@ -523,14 +602,14 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
             }
             __builtin_amdgcn_sched_barrier(kHold);
             const Split x = split(S[2 * d], S[2 * d + 1], 1.0f);
+            lds_put(hand + 1024 * d + 16 * lane, x.hi);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(kq[d & 1][t], x.hi, ks[t]);
+            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.hi, ks[t]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(kq[d & 1][4 + t], x.hi, qs[t]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(kq[d & 1][t], x.lo, ks[t]);
+            for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.lo, ks[t]);
             __builtin_amdgcn_sched_barrier(kHold);
         }
+        lds_barrier();                         // (2) the state is handed over
         float top_s = 0.f;                     // for the next S
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
@@ -563,7 +642,7 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
             found |= __shfl_xor(found, 32);
             if constexpr (TREE) {
                 for (int row = 0; row < kChunk; ++row)
-                    if (lds_get<uint64_t>(val + C::kRows + C::kKin + 8 * row) & found) lost |= 1ull << row;
+                    lost |= lds_get<uint64_t>(val + C::kRows + C::kKin + 8 * row) & found ? 1ull << row : 0ull;
             } else {
                 lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
             }
@@ -579,26 +658,39 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
             top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
         }
         // A power of two for R, and with it for the next S, which has at most 2^14 from this one and 2^15 from
-        // U: 64 products of K^T (below 1/2) and rows that lie below 2^10.
+        // U: 64 products of K^T (below 1) and rows that lie below 2^9.
         const int next = min(kTop - max(exponent(top_r), -100) + weigh_up,
                              power + kTop - (top_s > 0.f ? exponent(top_s) : -200));
         const int up_r = next - weigh_up;
         const float by_r = times2(1.0f, up_r);
 
         // ---- U = T R (times 2^(up_r + a power for each row)) ----
-        f4 U[4], fs[4], fu[4], weigh[4];
-        h8 within[6];
+        f4 U[4], weigh[4];
+        // K^T: four tokens of a channel at a time out of K's operands
+        h8 kt[kRowTiles][2];
+        auto load_kt = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i) within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
+            for (int d = 0; d < 2; ++d) {
+                u2 part[2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if constexpr (!TREE) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
-            fs[t] = lds_get<f4>(rows + C::kFromS + 64 * t);
-            fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
+                for (int e = 0; e < 2; ++e) {
+                    const int from = 1024 * ((2 * d + e) * kSteps + t / 2) + 8 * (t & 1);
+                    part[e] = read_column(at + from + 16 * (16 * (m & 3) + 4 * b + (m >> 2)));
+                }
+                kt[t][d] = __builtin_bit_cast(h8, u4{part[0][0], part[0][1], part[1][0], part[1][1]});
+            }
+        };
+        if constexpr (!TREE) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
         }
         __builtin_amdgcn_sched_barrier(kHold);
         {
             const Split r0 = split(R[0], R[1], by_r), r1 = split(R[2], R[3], by_r);
+            if constexpr (!TREE) {
+#pragma unroll
+                for (int t = 0; t < kRowTiles; ++t) load_kt(t);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -612,30 +704,22 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
                     }
         }
         __builtin_amdgcn_sched_barrier(kHold);
-
-        // ---- O, and S <- e^G_last S + (e^(G_last - G) K)^T U ----
-        h8 kt[kRowTiles][2];
-        if constexpr (!TREE)
-#pragma unroll
-            for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-                for (int d = 0; d < 2; ++d) kt[t][d] = lds_get<h8>(mine + 1024 * (C::kTiles + 2 * t + d));
-        __builtin_amdgcn_sched_barrier(kHold);
-        constexpr float kDown = 1.0f / (1 << 20);          // U lies below 2^34: 64 products of 2^14 each
-        f4 o[4];
         {
-            h8 u[2];
+            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
+            for (int d = 0; d < 2; ++d) {
+                h8 u;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
+                for (int e = 0; e < 8; ++e) u[e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
+                lds_put(hand + 1024 * (kSteps + d) + 16 * lane, u);
+            }
+            lds_put(factors, of_s);
+            lds_put(factors + 256, times2(1.0f, 20 - up_r));
+            lds_put(lost_at, lost);
         }
+        lds_barrier();                         // (3) and U
+
+        // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
         if constexpr (!TREE) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -660,40 +744,7 @@ __global__ void __launch_bounds__(64 * WAVES) chunk_scan_kernel(DeltaArgs a, Seg
                     for (int j = 0; j < 4; ++j) S[t][j] = lost ? __builtin_nanf("") : S[t][j];
             }
         }
-        const float of_u = times2(1.0f, 20 - up_r);
-        f4 y[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * o[t][j]);
-        if (__builtin_amdgcn_ballot_w64(lost != 0)) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
-        }
-        // through LDS, so that a lane stores eight columns of a row
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
-                lds_u8 *const to = tile + (16 * t + 4 * b + j) * kColumnBytes + 2 * m;
-                lds_put(to, (uint16_t)two);
-                lds_put(to + kColumnBytes, (uint16_t)(two >> 16));
-            }
-        const int n = min(kChunk, s.n - first - kChunk * ci);
-        const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
-                                        h * a.value_dim + blockIdx.x * (16 * WAVES) + 16 * wave,
-                                    (uint32_t)((n - 1) * out_row + 32));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 32 * i + (lane >> 1);
-            const u4 eight = lds_get<u4>(tile + row * kColumnBytes + 16 * (lane & 1));
-            __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
-        }
     }
-    wait_loads<0>();
     if constexpr (!TREE) {
         if (s.state < 0 && s.n - first <= kChunk * seg.chunks) return;     // (kept for the next segment only)
         float *const to = pool + (int64_t)(4 * b) * a.value_dim + col;
@@ -733,7 +784,7 @@ size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
 hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
     const Cut c = cut_of(a);
     auto go = [&](auto bf, auto dk, auto tree) {
-        constexpr int kWaves = 4;
+        constexpr int kGroups = 4;
         Segment seg;
         seg.keys = static_cast<uint8_t *>(a.workspace);
         seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<dk()>::kKey;
@@ -747,8 +798,8 @@ hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
                 chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
                 hipError_t e = hipGetLastError();
                 if (e != hipSuccess) return e;
-                chunk_scan_kernel<bf(), dk(), tree(), kWaves>
-                    <<<dim3(a.value_dim / (16 * kWaves), a.v_heads, seg.batch), 64 * kWaves, 0, stream>>>(a, seg);
+                chunk_scan_kernel<bf(), dk(), tree(), kGroups>
+                    <<<dim3(a.value_dim / (16 * kGroups), a.v_heads, seg.batch), 128 * kGroups, 0, stream>>>(a, seg);
                 e = hipGetLastError();
                 if (e != hipSuccess) return e;
             }
