@@ -42,7 +42,8 @@ constexpr int kTopK = 0;               // and keys below 2^kTopK
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Workspace of one chunk: for each key head K and Q as operands (tiles of 1 KiB: 64 lanes x 16
-// bytes), for each value head T in two parts, the products with the queries (the six tiles of 16 x 32
+// bytes; of K the first eight bytes of all lanes and then the others, so that its columns can be
+// read without bank conflicts as well), for each value head T in two parts, the products with the queries (the six tiles of 16 x 32
 // that are not above the diagonal), and what goes by rows.
 template <int DK>
 struct Chunk {
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             const int row = 16 * (tile / (DK / 32)) + m, ch = 32 * (tile % (DK / 32)) + 4 * b;
             const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
             const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
-            *reinterpret_cast<h8 *>(to_key + 1024 * tile + 16 * lane) = __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7);
+            *reinterpret_cast<h4 *>(to_key + 1024 * tile + 8 * lane) = k0;
+            *reinterpret_cast<h4 *>(to_key + 1024 * tile + 512 + 8 * lane) = k1;
             *reinterpret_cast<h8 *>(to_key + 1024 * (C::kTiles + tile) + 16 * lane) =
                 __builtin_shufflevector(q0, q1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
@@ -407,8 +409,7 @@ template <bool BF, int DK, bool TREE, int GROUPS>
 __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
-    // two chunks, each with V's columns of this workgroup, in whose place their outputs come; and for each
-    // group the state and U as operands, what comes off their sums, and rows that are lost
+    // two chunks, each with V's columns of this workgroup; and for each group the state and U as operands, what comes off their sums, and rows that are lost
     constexpr int kColumnBytes = 32 * GROUPS, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
     constexpr int kFactors = (kSteps + 2) * 1024, kHand = kFactors + 1024;
     __shared__ __align__(16) uint8_t lds_raw[2 * kStage + GROUPS * kHand];
@@ -464,9 +465,8 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             else wait_loads<2>();
             lds_barrier();                     // (1) and the other chunk's place is free
             if (ci + 1 < count) copy(ci + 1);
-            lds_u8 *const at = lds + (ci & 1) * kStage;
+            const lds_u8 *const at = lds + (ci & 1) * kStage;
             const lds_u8 *const mine = at + 16 * lane, *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
-            lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;        // this group's columns
             h8 q[kSteps][4];
 #pragma unroll
             for (int d = 0; d < kSteps; ++d)
@@ -511,15 +511,16 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
             }
-            // through LDS, so that a lane stores eight columns of a row
+            // through LDS (the state's place, rows 48 bytes apart), so that a lane stores eight columns of a row
+            static_assert(kHand >= 48 * kChunk && (kSteps + 2) * 1024 >= 48 * kChunk, "room for the outputs");
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; j += 2) {
                     const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
-                    lds_u8 *const to = tile + (16 * t + 4 * b + j) * kColumnBytes + 2 * m;
+                    lds_u8 *const to = hand + 48 * (16 * t + 4 * b + j) + 2 * m;
                     lds_put(to, (uint16_t)two);
-                    lds_put(to + kColumnBytes, (uint16_t)(two >> 16));
+                    lds_put(to + 48, (uint16_t)(two >> 16));
                 }
             const int n = min(kChunk, s.n - first - kChunk * ci);
             const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 32 * i + (lane >> 1);
-                const u4 eight = lds_get<u4>(tile + row * kColumnBytes + 16 * (lane & 1));
+                const u4 eight = lds_get<u4>(hand + 48 * row + 16 * (lane & 1));
                 __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
             }
         }
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 
     for (int ci = 0; ci < count; ++ci) {
         lds_barrier();                         // (1) this chunk is there
-        const lds_u8 *const at = lds + (ci & 1) * kStage, *const mine = at + 16 * lane;
-        const lds_u8 *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
+        const lds_u8 *const at = lds + (ci & 1) * kStage, *const val = at + C::kKey;
+        const lds_u8 *const rows = val + C::kRows + 16 * b;
         const lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;
 
         // Operands come out of LDS a step ahead of the products that take them, and products that add to one
@@ -571,7 +572,11 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         h8 k[2][4];                            // K of 32 channels: four row tiles
         auto load_k = [&](int d) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) k[d & 1][t] = lds_get<h8>(mine + 1024 * (t * kSteps + d));
+            for (int t = 0; t < 4; ++t) {
+                const lds_u8 *const from = at + 1024 * (t * kSteps + d) + 8 * lane;
+                const u2 lo = lds_get<u2>(from), hi = lds_get<u2>(from + 512);
+                k[d & 1][t] = __builtin_bit_cast(h8, u4{lo[0], lo[1], hi[0], hi[1]});
+            }
         };
         load_k(0);
         u2 V[4];
@@ -674,8 +679,8 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 u2 part[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int from = 1024 * ((2 * d + e) * kSteps + t / 2) + 8 * (t & 1);
-                    part[e] = read_column(at + from + 16 * (16 * (m & 3) + 4 * b + (m >> 2)));
+                    const int from = 1024 * ((2 * d + e) * kSteps + t / 2) + 512 * (t & 1);
+                    part[e] = read_column(at + from + 8 * (16 * (m & 3) + 4 * b + (m >> 2)));
                 }
                 kt[t][d] = __builtin_bit_cast(h8, u4{part[0][0], part[0][1], part[1][0], part[1][1]});
             }
@@ -784,7 +789,6 @@ size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
 hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
     const Cut c = cut_of(a);
     auto go = [&](auto bf, auto dk, auto tree) {
-        constexpr int kGroups = 4;
         Segment seg;
         seg.keys = static_cast<uint8_t *>(a.workspace);
         seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<dk()>::kKey;
@@ -798,8 +802,14 @@ hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
                 chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
                 hipError_t e = hipGetLastError();
                 if (e != hipSuccess) return e;
-                chunk_scan_kernel<bf(), dk(), tree(), kGroups>
-                    <<<dim3(a.value_dim / (16 * kGroups), a.v_heads, seg.batch), 128 * kGroups, 0, stream>>>(a, seg);
+                // 32 columns a workgroup while each finds a CU of its own, else 64 (one sequence of 8191 tokens, 48
+                // heads: 290 and 352 us; five of 333 to 2500, 32 heads: 104 and 86)
+                if ((int64_t)a.value_dim / 32 * a.v_heads * seg.batch <= 256)
+                    chunk_scan_kernel<bf(), dk(), tree(), 2>
+                        <<<dim3(a.value_dim / 32, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
+                else
+                    chunk_scan_kernel<bf(), dk(), tree(), 4>
+                        <<<dim3(a.value_dim / 64, a.v_heads, seg.batch), 512, 0, stream>>>(a, seg);
                 e = hipGetLastError();
                 if (e != hipSuccess) return e;
             }
