@@ -100,8 +100,34 @@ __device__ __forceinline__ Split split(const f4 &x, const f4 &y, float by) {
     return {__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
 }
 
+// The largest over the 16 lanes of a row of lanes (DPP: no LDS).
+__device__ __forceinline__ float top_of_row(float v) {
+#define W4A16_TOP_ROR(N) \
+    v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + N, 0xF, 0xF, true)))
+    W4A16_TOP_ROR(8);
+    W4A16_TOP_ROR(4);
+    W4A16_TOP_ROR(2);
+    W4A16_TOP_ROR(1);
+#undef W4A16_TOP_ROR
+    return v;
+}
+
+// The largest size in a column's lanes; NaN if there is one.
+__device__ __forceinline__ float top_of_column(float v) {
+    const uint32_t bits = __float_as_uint(v);
+    const auto halves = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+    const float w = __builtin_elementwise_maximum(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
+    const uint32_t half = __float_as_uint(w);
+    const auto rows = __builtin_amdgcn_permlane16_swap(half, half, false, false);
+    return __builtin_elementwise_maximum(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+}
+
+constexpr int kMostHeads = 4;          // value heads of a workgroup
+
+// One chunk of `heads` value heads that share a key head: what the heads have in common, the products of
+// keys with keys and queries among it, is made once.
 template <bool BF, int DK, bool TREE>
-__global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment seg) {
+__global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
     using C = Chunk<DK>;
     constexpr int kStride = DK + 8, kA = 68, kP = 72;
     // keys and queries, and then in their place A and X
@@ -111,14 +137,14 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     auto &Q = *reinterpret_cast<_Float16(*)[kChunk][kStride]>(shared[1]);
     auto &A = *reinterpret_cast<float(*)[kChunk][kA]>(shared[0]);
     auto &X = *reinterpret_cast<float(*)[kChunk][kA]>(shared[1]);
-    __shared__ double G[kChunk];
-    __shared__ float beta[kChunk], kf[kChunk], qf[kChunk];
+    __shared__ double all_G[kMostHeads][kChunk];
+    __shared__ __align__(16) float all_beta[kMostHeads][kChunk];
+    __shared__ float kf[kChunk], qf[kChunk], within_scale[kChunk];
     __shared__ int tau[kChunk];
     __shared__ uint64_t kin[kChunk];
-    __shared__ uint32_t bad[kChunk];           // 1: the key or a gate, 2: the query is not finite
-    __shared__ float within_scale[kChunk];
+    __shared__ uint32_t bad_row[kChunk], bad_gate[kMostHeads][kChunk];     // 1: the key, 2: the query; a gate
 
-    const int ci = blockIdx.x, h = blockIdx.y, r = a.v_heads / a.k_heads, hk = h / r;
+    const int ci = blockIdx.x, h0 = blockIdx.y * heads, r = a.v_heads / a.k_heads, hk = h0 / r;
     Seq s;
     if (!seq_of(a.s, seg.first_seq + blockIdx.z, &s)) return;
     if (TREE) s.n = min(s.n, kChunk);
@@ -127,97 +153,105 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     const int n = min(kChunk, s.n - t0);
     const int64_t slot = (int64_t)blockIdx.z * seg.chunks + ci;
     uint8_t *const to_key = seg.keys + (slot * a.k_heads + hk) * C::kKey;
-    uint8_t *const to = seg.values + (slot * a.v_heads + h) * C::kValue;
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, b = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), my_lane = tid & 63;
+    int lane = my_lane, m = lane & 15, b = lane >> 4;
 
-    // ---- keys and queries as fp16 rows of about 2^14 at most, and what came off them ----
-    if (tid < kChunk) bad[tid] = 0;
-    __syncthreads();
-    {
-        const int row = tid >> 2, part = (tid & 3) * (DK / 4);
-        const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
+    u4 raw[2][DK / 32];                        // a quarter of a row of K and of Q
+    const int my_row = tid >> 2, my_part = (tid & 3) * (DK / 4);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const uint16_t *const src = (which ? static_cast<const uint16_t *>(a.q) + (s.first + t0 + row) * a.q_stride
-                                               : static_cast<const uint16_t *>(a.k) + (s.first + t0 + row) * a.k_stride) +
-                                        hk * DK + part;
-            u4 raw[DK / 32];
+    for (int which = 0; which < 2; ++which) {
+        const uint16_t *const src = (which ? static_cast<const uint16_t *>(a.q) + (s.first + t0 + my_row) * a.q_stride
+                                           : static_cast<const uint16_t *>(a.k) + (s.first + t0 + my_row) * a.k_stride) +
+                                    hk * DK + my_part;
 #pragma unroll
-            for (int i = 0; i < DK / 32; ++i) raw[i] = row < n ? *reinterpret_cast<const u4 *>(src + 8 * i) : u4{0u, 0u, 0u, 0u};
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < DK / 32; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(raw[i][e] & 0x7FFFu, raw[i][e] >> 16 & 0x7FFFu));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-            const bool fine = top < limit;
-            const int up = fine && top ? (which ? kTop : kTopK) - exponent(lo_f32<BF>(top)) : 0;
-            float sum = 0.f;
-            _Float16 *const dst = (which ? Q[row] : K[row]) + part;
-#pragma unroll
-            for (int i = 0; i < DK / 32; ++i) {
-                h8 v;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x0 = fine ? times2(lo_f32<BF>(raw[i][e]), up) : 0.f;
-                    const float x1 = fine ? times2(hi_f32<BF>(raw[i][e]), up) : 0.f;
-                    sum = __builtin_fmaf(x0, x0, sum);
-                    sum = __builtin_fmaf(x1, x1, sum);
-                    v[2 * e] = (_Float16)x0;
-                    v[2 * e + 1] = (_Float16)x1;
-                }
-                *reinterpret_cast<h8 *>(dst + 8 * i) = v;
-            }
-            sum += __shfl_xor(sum, 1);
-            sum += __shfl_xor(sum, 2);
-            if (part == 0) {
-                // (rows past the sequence's are zeros and count for nothing)
-                float f = a.unit ? 1.0f / sqrtf(sum + times2(a.eps, 2 * up)) : times2(1.0f, -up);
-                if (row >= n) f = 0.f;
-                const bool ok = fine && f < __builtin_inff();
-                (which ? qf : kf)[row] = ok ? f : 0.f;
-                if (!ok) atomicOr(&bad[row], 1u + which);
-            }
-        }
+        for (int i = 0; i < DK / 32; ++i)
+            raw[which][i] = my_row < n ? *reinterpret_cast<const u4 *>(src + 8 * i) : u4{0u, 0u, 0u, 0u};
     }
-    // ---- gates, and their sums in 64 bits: differences of far sums keep their precision ----
-    if (tid < kChunk) {
+
+    // ---- gates, a head in each wave, and their sums in 64 bits: differences of far sums keep their precision ----
+    uint64_t word = (2ull << lane) - 1;
+    if constexpr (TREE) word = lane < n ? ((uint64_t)a.s.tree[s.first + lane] & ((1ull << lane) - 1)) | 1ull << lane : 0;
+    if (wave == 0) kin[lane] = word;
+    if (wave < heads) {
+        const int h = h0 + wave;
         Gates gate{0.f, 0.f};
-        if (tid < n)
-            gate = gates_of<BF>(a, s.first + t0 + tid, h, a.a_log ? expf(a.a_log[h]) : 0.f, a.a_log ? a.dt_bias[h] : 0.f);
+        if (lane < n)
+            gate = gates_of<BF>(a, s.first + t0 + lane, h, a.a_log ? expf(a.a_log[h]) : 0.f, a.a_log ? a.dt_bias[h] : 0.f);
         const bool ok = gate.g < __builtin_inff() && __builtin_fabsf(gate.beta) < __builtin_inff();
-        if (!ok) atomicOr(&bad[tid], 1u);
         // (e^-256 is 0 in fp32, as is all that it multiplies)
         const double g = ok ? (double)fmaxf(gate.g, -256.f) : 0.0;
-        beta[tid] = ok ? gate.beta : 0.f;
         double sum = g;
-        uint64_t word = (2ull << tid) - 1;
         if constexpr (TREE) {
-            word = tid < n ? ((uint64_t)a.s.tree[s.first + tid] & ((1ull << tid) - 1)) | 1ull << tid : 0;
             sum = 0;
-            for (int j = 0; j < kChunk; ++j) {
-                const double gj = __shfl(g, j);
-                if (word >> j & 1) sum += gj;
+            const uint64_t bits = __builtin_bit_cast(uint64_t, g);
+            for (int j = 0; j < n; ++j) {
+                const uint64_t of_j = (uint32_t)__builtin_amdgcn_readlane((uint32_t)bits, j) |
+                                      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(bits >> 32), j) << 32;
+                sum += word >> j & 1 ? __builtin_bit_cast(double, of_j) : 0.0;
             }
         } else {
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
                 const double below = __shfl_up(sum, d);
-                if (tid >= d) sum += below;
+                if (lane >= d) sum += below;
             }
         }
-        G[tid] = sum;
-        kin[tid] = word;
+        all_beta[wave][lane] = ok ? gate.beta : 0.f;
+        all_G[wave][lane] = sum;
+        bad_gate[wave][lane] = ok ? 0u : 1u;
+    }
+
+    // ---- keys and queries as fp16 rows of a common size, and what came off them ----
+    uint32_t bad = 0;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(raw[which][i][e] & 0x7FFFu, raw[which][i][e] >> 16 & 0x7FFFu));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        const bool fine = top < limit;
+        const int up = fine && top ? min((which ? kTop : kTopK) - exponent(lo_f32<BF>(top)), 126) : 0;
+        const float by = fine ? times2(1.0f, up) : 0.f;
+        float sum = 0.f;
+        _Float16 *const dst = (which ? Q[my_row] : K[my_row]) + my_part;
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i) {
+            h8 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = fine ? lo_f32<BF>(raw[which][i][e]) * by : 0.f;
+                const float x1 = fine ? hi_f32<BF>(raw[which][i][e]) * by : 0.f;
+                sum = __builtin_fmaf(x0, x0, sum);
+                sum = __builtin_fmaf(x1, x1, sum);
+                v[2 * e] = (_Float16)x0;
+                v[2 * e + 1] = (_Float16)x1;
+            }
+            *reinterpret_cast<h8 *>(dst + 8 * i) = v;
+        }
+        sum += __shfl_xor(sum, 1);
+        sum += __shfl_xor(sum, 2);
+        if (my_part == 0) {
+            // (rows past the sequence's are zeros and count for nothing)
+            float f = a.unit ? 1.0f / sqrtf(sum + times2(a.eps, 2 * up)) : times2(1.0f, -up);
+            if (my_row >= n) f = 0.f;
+            const bool ok = fine && f < __builtin_inff();
+            (which ? qf : kf)[my_row] = ok ? f : 0.f;
+            if (!ok) bad |= 1u + which;
+            if (which) bad_row[my_row] = bad;
+        }
     }
     __syncthreads();
 
-    // ---- keys and queries as operands, once for each key head ----
-    if (h % r == 0) {
+    // ---- keys and queries as operands ----
+    if (h0 % r == 0) {
 #pragma unroll
         for (int i = 0; i < C::kTiles / 4; ++i) {
-            const int tile = 4 * i + wave;                     // of K and Q: [row tile][DK / 32]
+            const int tile = 4 * i + wave;                 // [row tile][DK / 32]
             const int row = 16 * (tile / (DK / 32)) + m, ch = 32 * (tile % (DK / 32)) + 4 * b;
             const h4 k0 = *reinterpret_cast<const h4 *>(&K[row][ch]), k1 = *reinterpret_cast<const h4 *>(&K[row][ch + 16]);
             const h4 q0 = *reinterpret_cast<const h4 *>(&Q[row][ch]), q1 = *reinterpret_cast<const h4 *>(&Q[row][ch + 16]);
@@ -229,168 +263,178 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     }
 
     // ---- products of keys with keys and queries; lane (m, b): rows 16 wave + 4 b + j, column 16 nt + m ----
-    f4 p[4];
-    {
-        f4 kk[4];
+    f4 kk[4], qk[4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) kk[nt] = p[nt] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int nt = 0; nt < 4; ++nt) kk[nt] = qk[nt] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int d = 0; d < DK / 32; ++d) {
-            const h8 ka = *reinterpret_cast<const h8 *>(&K[16 * wave + m][32 * d + 8 * b]);
-            const h8 qa = *reinterpret_cast<const h8 *>(&Q[16 * wave + m][32 * d + 8 * b]);
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                if (nt > wave) continue;
-                const h8 kb = *reinterpret_cast<const h8 *>(&K[16 * nt + m][32 * d + 8 * b]);
-                kk[nt] = mfma16x16x32(ka, kb, kk[nt]);
-                p[nt] = mfma16x16x32(qa, kb, p[nt]);
-            }
-        }
+    for (int d = 0; d < DK / 32; ++d) {
+        const h8 ka = *reinterpret_cast<const h8 *>(&K[16 * wave + m][32 * d + 8 * b]);
+        const h8 qa = *reinterpret_cast<const h8 *>(&Q[16 * wave + m][32 * d + 8 * b]);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-            if (nt == 0) __syncthreads();      // (keys and queries are done with)
+            if (nt > wave) continue;
+            const h8 kb = *reinterpret_cast<const h8 *>(&K[16 * nt + m][32 * d + 8 * b]);
+            kk[nt] = mfma16x16x32(ka, kb, kk[nt]);
+            qk[nt] = mfma16x16x32(qa, kb, qk[nt]);
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        if (nt > wave) continue;
+        const int col = 16 * nt + m;
+        const float kc = kf[col];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * wave + 4 * b + j;
+            kk[nt][j] = col < row ? kf[row] * kk[nt][j] * kc : 0.f;
+            qk[nt][j] = a.scale * (qf[row] * qk[nt][j] * kc);
+        }
+    }
+
+    for (int hi = 0; hi < heads; ++hi) {
+        // (opaque: else every address that they go into is kept in registers through the loop, 120 more than there are)
+        asm volatile("" : "+v"(lane), "+v"(m), "+v"(b));
+        const int h = h0 + hi;
+        const double *const G = all_G[hi];
+        const float *const beta = all_beta[hi];
+        uint8_t *const to = seg.values + (slot * a.v_heads + h) * C::kValue;
+        __syncthreads();                       // keys and queries, or the head before, are done with
+        f4 p[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
             if (nt > wave) continue;
             const int col = 16 * nt + m;
             const double gc = G[col];
-            const float kc = kf[col];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = 16 * wave + 4 * b + j;
                 const bool sees = TREE ? kin[row] >> col & 1 : col <= row;
-                const float w = sees ? exp_f32((float)(G[row] - gc)) * kc : 0.f;
-                A[row][col] = col < row ? beta[row] * (kf[row] * kk[nt][j] * w) : 0.f;
-                p[nt][j] = a.scale * (qf[row] * p[nt][j] * w);
+                const float w = sees ? exp_f32((float)(G[row] - gc)) : 0.f;
+                A[row][col] = beta[row] * (kk[nt][j] * w);
+                p[nt][j] = qk[nt][j] * w;
             }
         }
-    }
-    __syncthreads();
-
-    // ---- X = (I + A)^-1: blocks of 16 on the diagonal by substitution, the others from them ----
-    {
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = i == m ? 1.f : 0.f;
-#pragma unroll
-            for (int j = 0; j < i; ++j) v = __builtin_fmaf(-A[16 * wave + i][16 * wave + j], x[j], v);
-            x[i] = v;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (b == i / 4) X[16 * wave + i][16 * wave + m] = x[i];
-    }
-#pragma unroll
-    for (int d = 1; d < 4; ++d) {
         __syncthreads();
-        const int i = wave + d, j = wave;
-        if (i < 4) {
-            f4 acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
-            for (int mid = j; mid < i; ++mid) {
-                const f4 left = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * mid + 4 * b]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], X[16 * mid + 4 * b + e][16 * j + m], acc, 0, 0, 0);
-            }
-            const f4 left = *reinterpret_cast<const f4 *>(&X[16 * i + m][16 * i + 4 * b]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) out = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], acc[e], out, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) X[16 * i + 4 * b + e][16 * j + m] = -out[e];
-        }
-    }
-    __syncthreads();
 
-    // ---- T = X diag(beta) as operands; lane (m, b): row 16 wave + m ----
-    {
-        const int row = 16 * wave + m;
-        float t[2][8], top = 0.f;
+        // ---- X = (I + A)^-1: blocks of 16 on the diagonal by substitution, the others from them ----
+        {
+            float x[16];
 #pragma unroll
-        for (int d = 0; d < 2; ++d)
+            for (int i = 0; i < 16; ++i) {
+                float v = i == m ? 1.f : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const int col = place(d, b, e);
-                const bool in = 2 * d + (e >> 2) <= wave;
-                f4 v = {0.f, 0.f, 0.f, 0.f};
-                if (in) v = *reinterpret_cast<const f4 *>(&X[row][col]);
+                for (int j = 0; j < i; ++j) v = __builtin_fmaf(-A[16 * wave + i][16 * wave + j], x[j], v);
+                x[i] = v;
+                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);       // (else all of A's rows come into registers first)
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    t[d][e + i] = in ? v[i] * beta[col + i] : 0.f;
-                    top = fmaxf(top, __builtin_fabsf(t[d][e + i]));
+            for (int i = 0; i < 16; ++i)
+                if (b == i / 4) X[16 * wave + i][16 * wave + m] = x[i];
+        }
+#pragma unroll
+        for (int d = 1; d < 4; ++d) {
+            __syncthreads();
+            const int i = wave + d, j = wave;
+            if (i < 4) {
+                f4 acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
+                for (int mid = j; mid < i; ++mid) {
+                    const f4 left = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * mid + 4 * b]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], X[16 * mid + 4 * b + e][16 * j + m], acc, 0, 0, 0);
                 }
+                const f4 left = *reinterpret_cast<const f4 *>(&X[16 * i + m][16 * i + 4 * b]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], acc[e], out, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[16 * i + 4 * b + e][16 * j + m] = -out[e];
             }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const int up = kTop - max(exponent(top), -60);
-        if (b == 0) tau[row] = up;
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-            if (2 * d > wave) continue;
-            const Split x = split(f4{t[d][0], t[d][1], t[d][2], t[d][3]}, f4{t[d][4], t[d][5], t[d][6], t[d][7]}, times2(1.0f, up));
-            const int tile = tile_of(wave, d);
-            *reinterpret_cast<h8 *>(to + C::kHigh + 1024 * tile + 16 * lane) = x.hi;
-            *reinterpret_cast<h8 *>(to + C::kLow + 1024 * tile + 16 * lane) = x.lo;
         }
-    }
-    __syncthreads();
+        __syncthreads();
 
-    // ---- products with the queries: by what the rows of U carry, through LDS into operands ----
-    _Float16 *const P = reinterpret_cast<_Float16 *>(&A[0][0]);      // [64][kP]
+        // ---- T = X diag(beta) as operands; lane (m, b): row 16 wave + m ----
+        {
+            const int row = 16 * wave + m;
+            float t[2][8], top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = 16 * wave + 4 * b + j;
-        float top = 0.f;
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const int col = place(d, b, e);
+                    const bool in = 2 * d + (e >> 2) <= wave;
+                    f4 v = {0.f, 0.f, 0.f, 0.f}, w = v;
+                    if (in) {
+                        v = *reinterpret_cast<const f4 *>(&X[row][col]);
+                        w = *reinterpret_cast<const f4 *>(&beta[col]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        t[d][e + i] = v[i] * w[i];
+                        top = fmaxf(top, __builtin_fabsf(t[d][e + i]));
+                    }
+                }
+            const int up = kTop - max(exponent(top_of_column(top)), -60);
+            if (b == 0) tau[row] = up;
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                if (2 * d > wave) continue;
+                const Split x = split(f4{t[d][0], t[d][1], t[d][2], t[d][3]}, f4{t[d][4], t[d][5], t[d][6], t[d][7]}, times2(1.0f, up));
+                const int tile = tile_of(wave, d);
+                *reinterpret_cast<h8 *>(to + C::kHigh + 1024 * tile + 16 * lane) = x.hi;
+                *reinterpret_cast<h8 *>(to + C::kLow + 1024 * tile + 16 * lane) = x.lo;
+            }
+        }
+        __syncthreads();
+
+        // ---- products with the queries: by what the rows of U carry, through LDS into operands ----
+        _Float16 *const P = reinterpret_cast<_Float16 *>(&A[0][0]);      // [64][kP]
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt > wave) continue;
-            p[nt][j] = times2(p[nt][j], -tau[16 * nt + m]);
-            top = fmaxf(top, __builtin_fabsf(p[nt][j]));
+            const float down = times2(1.0f, -tau[16 * nt + m]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[nt][j] *= down;
         }
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const int up = kTop - max(exponent(top), -100);
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * wave + 4 * b + j;
+            float top = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)times2(p[nt][j], up);
-        if (m == 0) within_scale[row] = times2(1.0f, -up);
-    }
-    __syncthreads();
+            for (int nt = 0; nt < 4; ++nt)
+                if (nt <= wave) top = fmaxf(top, __builtin_fabsf(p[nt][j]));
+            const int up = kTop - max(exponent(top_of_row(top)), -100);
+            const float by = times2(1.0f, up);
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-        if (2 * d > wave) continue;
-        const _Float16 *const from = P + (16 * wave + m) * kP + 32 * d + 4 * b;
-        const h4 lo = *reinterpret_cast<const h4 *>(from), hi = *reinterpret_cast<const h4 *>(from + 16);
-        *reinterpret_cast<h8 *>(to + C::kWithin + 1024 * tile_of(wave, d) + 16 * lane) =
-            __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
+            for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)(p[nt][j] * by);
+            if (m == 0) within_scale[row] = times2(1.0f, -up);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            if (2 * d > wave) continue;
+            const _Float16 *const from = P + (16 * wave + m) * kP + 32 * d + 4 * b;
+            const h4 lo = *reinterpret_cast<const h4 *>(from), hi4 = *reinterpret_cast<const h4 *>(from + 16);
+            *reinterpret_cast<h8 *>(to + C::kWithin + 1024 * tile_of(wave, d) + 16 * lane) =
+                __builtin_shufflevector(lo, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
 
-    // ---- what goes by rows ----
-    if (tid < kChunk) {
-        float *const rows = reinterpret_cast<float *>(to + C::kRows);
-        const float grow = exp_f32((float)G[tid]), nan = __builtin_nanf("");
-        const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[tid])) * kf[tid], -tau[tid]);
-        float top = weigh;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const int up = -25 - max(exponent(top), -120);
-        rows[C::kOff / 4 + tid] = bad[tid] & 1 ? nan : grow * kf[tid];
-        rows[C::kWeigh / 4 + tid] = times2(weigh, up);
-        rows[C::kFromS / 4 + tid] = bad[tid] & 2 ? nan : a.scale * qf[tid] * grow;
-        rows[C::kFromU / 4 + tid] = within_scale[tid];
-        reinterpret_cast<uint64_t *>(to + C::kRows + C::kKin)[tid] = kin[tid];
-        if (tid == 0) {
-            rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
-            reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
+        // ---- what goes by rows ----
+        if (wave == 0) {
+            float *const rows = reinterpret_cast<float *>(to + C::kRows);
+            const float grow = exp_f32((float)G[lane]), nan = __builtin_nanf("");
+            const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[lane])) * kf[lane], -tau[lane]);
+            const int up = -25 - max(exponent(top_of_column(top_of_row(weigh))), -120);
+            rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
+            rows[C::kWeigh / 4 + lane] = times2(weigh, up);
+            rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
+            rows[C::kFromU / 4 + lane] = within_scale[lane];
+            reinterpret_cast<uint64_t *>(to + C::kRows + C::kKin)[lane] = kin[lane];
+            if (lane == 0) {
+                rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
+                reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
+            }
         }
     }
-}
-
-// The largest size in a column's lanes; NaN if there is one.
-__device__ __forceinline__ float top_of_column(float v) {
-    const uint32_t bits = __float_as_uint(v);
-    const auto halves = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
-    const float w = __builtin_elementwise_maximum(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
-    const uint32_t half = __float_as_uint(w);
-    const auto rows = __builtin_amdgcn_permlane16_swap(half, half, false, false);
-    return __builtin_elementwise_maximum(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
 }
 
 // Four rows of one column of an LDS tile [rows][16 WAVES columns] of 16-bit values: lane (m, b) hands in the
@@ -799,7 +843,11 @@ hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
                 seg.batch = std::min(c.batch, a.s.batch - b0);
                 seg.first_chunk = c0;
                 seg.chunks = std::min(c.chunks, chunks_of(a) - c0);
-                chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
+                // value heads that share a key head in one workgroup, as long as that leaves some for every CU
+                int heads = 1;
+                for (int i = 2; i <= kMostHeads; ++i)
+                    if (a.v_heads / a.k_heads % i == 0 && (int64_t)seg.chunks * a.v_heads / i * seg.batch >= 512) heads = i;
+                chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads / heads, seg.batch), 256, 0, stream>>>(a, seg, heads);
                 hipError_t e = hipGetLastError();
                 if (e != hipSuccess) return e;
                 // 32 columns a workgroup while each finds a CU of its own, else 64 (one sequence of 8191 tokens, 48
