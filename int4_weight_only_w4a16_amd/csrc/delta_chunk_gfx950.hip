@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     auto &X = *reinterpret_cast<float(*)[kChunk][kA]>(shared[1]);
     __shared__ double all_G[kMostHeads][kChunk];
     __shared__ __align__(16) float all_beta[kMostHeads][kChunk];
-    __shared__ float kf[kChunk], qf[kChunk], within_scale[kChunk];
+    __shared__ __align__(16) float kf[kChunk], qf[kChunk];
     __shared__ int tau[kChunk];
     __shared__ uint64_t kin[kChunk];
     __shared__ uint32_t bad_row[kChunk], bad_gate[kMostHeads][kChunk];     // 1: the key, 2: the query; a gate
@@ -278,16 +278,18 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             qk[nt] = mfma16x16x32(qa, kb, qk[nt]);
         }
     }
+    {
+        const f4 of_k = *reinterpret_cast<const f4 *>(&kf[16 * wave + 4 * b]), of_q = *reinterpret_cast<const f4 *>(&qf[16 * wave + 4 * b]);
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        if (nt > wave) continue;
-        const int col = 16 * nt + m;
-        const float kc = kf[col];
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt > wave) continue;
+            const int col = 16 * nt + m;
+            const float kc = kf[col];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = 16 * wave + 4 * b + j;
-            kk[nt][j] = col < row ? kf[row] * kk[nt][j] * kc : 0.f;
-            qk[nt][j] = a.scale * (qf[row] * qk[nt][j] * kc);
+            for (int j = 0; j < 4; ++j) {
+                kk[nt][j] = col < 16 * wave + 4 * b + j ? of_k[j] * kk[nt][j] * kc : 0.f;
+                qk[nt][j] = a.scale * (of_q[j] * qk[nt][j] * kc);
+            }
         }
     }
 
@@ -300,18 +302,30 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
         uint8_t *const to = seg.values + (slot * a.v_heads + h) * C::kValue;
         __syncthreads();                       // keys and queries, or the head before, are done with
         f4 p[4];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            if (nt > wave) continue;
-            const int col = 16 * nt + m;
-            const double gc = G[col];
+        {
+            // (all that is read comes before A is written, which the compiler takes to overlap it)
+            const int row0 = 16 * wave + 4 * b;
+            double of_row[4], of_col[4];
+            uint64_t words[TREE ? 4 : 1];
+            f4 strength;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = 16 * wave + 4 * b + j;
-                const bool sees = TREE ? kin[row] >> col & 1 : col <= row;
-                const float w = sees ? exp_f32((float)(G[row] - gc)) : 0.f;
-                A[row][col] = beta[row] * (kk[nt][j] * w);
-                p[nt][j] = qk[nt][j] * w;
+                of_row[j] = G[row0 + j];
+                of_col[j] = G[16 * j + m];
+                strength[j] = beta[row0 + j];
+                if constexpr (TREE) words[j] = kin[row0 + j];
+            }
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                if (nt > wave) continue;
+                const int col = 16 * nt + m;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool sees = TREE ? words[TREE ? j : 0] >> col & 1 : col <= row0 + j;
+                    const float w = sees ? exp_f32((float)(of_row[j] - of_col[nt])) : 0.f;
+                    A[row0 + j][col] = strength[j] * (kk[nt][j] * w);
+                    p[nt][j] = qk[nt][j] * w;
+                }
             }
         }
         __syncthreads();
@@ -327,27 +341,33 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
                 x[i] = v;
                 if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);       // (else all of A's rows come into registers first)
             }
+            f4 mine = {0.f, 0.f, 0.f, 0.f};    // rows 4 b + e of the block
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (b == i / 4) X[16 * wave + i][16 * wave + m] = x[i];
-        }
+            for (int i = 0; i < 16; ++i) mine[i & 3] = b == i / 4 ? x[i] : mine[i & 3];
 #pragma unroll
-        for (int d = 1; d < 4; ++d) {
+            for (int e = 0; e < 4; ++e) X[16 * wave + 4 * b + e][16 * wave + m] = mine[e];
             __syncthreads();
-            const int i = wave + d, j = wave;
-            if (i < 4) {
-                f4 acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
-                for (int mid = j; mid < i; ++mid) {
-                    const f4 left = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * mid + 4 * b]);
+            // a wave's column of blocks below: X_ij = -X_ii sum_(j <= k < i) A_ik X_kj, its own X_kj in registers as
+            // the products leave them, which is how they go into the next
+            f4 column[4];
+            column[0] = mine;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], X[16 * mid + 4 * b + e][16 * j + m], acc, 0, 0, 0);
-                }
-                const f4 left = *reinterpret_cast<const f4 *>(&X[16 * i + m][16 * i + 4 * b]);
+            for (int d = 1; d < 4; ++d) {
+                const int i = wave + d;
+                if (i >= 4) break;
+                f4 left[4], acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], acc[e], out, 0, 0, 0);
+                for (int k = 0; k < d; ++k) left[k] = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * (wave + k) + 4 * b]);
+                left[3] = *reinterpret_cast<const f4 *>(&X[16 * i + m][16 * i + 4 * b]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) X[16 * i + 4 * b + e][16 * j + m] = -out[e];
+                for (int k = 0; k < d; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[k][e], column[k][e], acc, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out = __builtin_amdgcn_mfma_f32_16x16x4f32(left[3][e], acc[e], out, 0, 0, 0);
+                column[d] = -out;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[16 * i + 4 * b + e][16 * wave + m] = column[d][e];
             }
         }
         __syncthreads();
@@ -406,9 +426,9 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             const float by = times2(1.0f, up);
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)(p[nt][j] * by);
-            if (m == 0) within_scale[row] = times2(1.0f, -up);
+            if (m == 0) reinterpret_cast<float *>(to + C::kRows + C::kFromU)[row] = times2(1.0f, -up);
         }
-        __syncthreads();
+        // (a wave reads the rows that it wrote)
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
             if (2 * d > wave) continue;
@@ -427,7 +447,6 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
             rows[C::kWeigh / 4 + lane] = times2(weigh, up);
             rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
-            rows[C::kFromU / 4 + lane] = within_scale[lane];
             reinterpret_cast<uint64_t *>(to + C::kRows + C::kKin)[lane] = kin[lane];
             if (lane == 0) {
                 rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
