@@ -157,10 +157,11 @@ extern "C" int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, 
     d.bf16 = (flags & W4A16_X_BF16) != 0;
     d.unit = (flags & W4A16_UNIT_QK) != 0;
     d.workspace = workspace;
-    if (in_chunks(d)) {
+    const size_t need = in_chunks(d) ? w4a16::delta_chunk_workspace_bytes(d) : 0;
+    if (need > 0) {
         if (!workspace) return W4A16_ERR_NULL;
         if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
-        if (workspace_bytes < w4a16::delta_chunk_workspace_bytes(d)) return W4A16_ERR_WORKSPACE;
+        if (workspace_bytes < need) return W4A16_ERR_WORKSPACE;
     }
     if (device_ok() != W4A16_OK) return W4A16_ERR_DEVICE;
     const hipStream_t on = reinterpret_cast<hipStream_t>(stream);

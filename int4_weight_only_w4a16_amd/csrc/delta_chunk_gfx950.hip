@@ -52,8 +52,8 @@ struct Chunk {
     static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRows = 18 * 1024;
     static constexpr int kValue = 20 * 1024;
     // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
-    // output of S and of U; words of a tree; e^G_last and the power of two in the second of them
-    static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kKin = 1024, kLast = 1536;
+    // output of S and of U; e^G_last and the power of two in the second of them
+    static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kLast = 1024;
 };
 
 // The part of a call that one launch works on: `chunks` chunks from the first_chunk-th of `batch`
@@ -125,18 +125,20 @@ __device__ __forceinline__ float top_of_column(float v) {
 constexpr int kMostHeads = 4;          // value heads of a workgroup
 
 // One chunk of `heads` value heads that share a key head: what the heads have in common, the products of
-// keys with keys and queries among it, is made once.
+// keys with keys and queries among it, is made once.  TREE: of one head, and its outputs as well, since there
+// is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 36 us with the outputs in a launch of their own).
 template <bool BF, int DK, bool TREE>
-__global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
+__global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
     using C = Chunk<DK>;
     constexpr int kStride = DK + 8, kA = 68, kP = 72;
-    // keys and queries, and then in their place A and X
+    // keys and queries, and A and X (of a chunk among others in their place)
     constexpr int kPart = kChunk * (2 * kStride > 4 * kA ? 2 * kStride : 4 * kA);
-    __shared__ __align__(16) uint8_t shared[2][kPart];
+    __shared__ __align__(16) uint8_t shared[TREE ? 4 : 2][kPart];
+    __shared__ __align__(16) float tree_rows[TREE ? 4 * kChunk : 4];
     auto &K = *reinterpret_cast<_Float16(*)[kChunk][kStride]>(shared[0]);
     auto &Q = *reinterpret_cast<_Float16(*)[kChunk][kStride]>(shared[1]);
-    auto &A = *reinterpret_cast<float(*)[kChunk][kA]>(shared[0]);
-    auto &X = *reinterpret_cast<float(*)[kChunk][kA]>(shared[1]);
+    auto &A = *reinterpret_cast<float(*)[kChunk][kA]>(shared[TREE ? 2 : 0]);
+    auto &X = *reinterpret_cast<float(*)[kChunk][kA]>(shared[TREE ? 3 : 1]);
     __shared__ double all_G[kMostHeads][kChunk];
     __shared__ __align__(16) float all_beta[kMostHeads][kChunk];
     __shared__ __align__(16) float kf[kChunk], qf[kChunk];
@@ -157,6 +159,20 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), my_lane = tid & 63;
     int lane = my_lane, m = lane & 15, b = lane >> 4;
 
+    // of a tree, the state: two groups of sixteen columns at a time in each wave
+    constexpr int kRowTiles = DK / 16, kSteps = DK / 32;
+    f4 S[TREE ? 2 : 1][kRowTiles];
+    auto load_state = [&](int g0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int g = min(g0 + 4 * u, a.value_dim / 16 - 1);
+            const float *const from = a.state + ((max(s.state, (int64_t)0) * a.v_heads + h0) * DK + 4 * b) * a.value_dim + 16 * g + m;
+#pragma unroll
+            for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[u][t][j] = s.fresh ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
+        }
+    };
     u4 raw[2][DK / 32];                        // a quarter of a row of K and of Q
     const int my_row = tid >> 2, my_part = (tid & 3) * (DK / 4);
 #pragma unroll
@@ -168,6 +184,7 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
         for (int i = 0; i < DK / 32; ++i)
             raw[which][i] = my_row < n ? *reinterpret_cast<const u4 *>(src + 8 * i) : u4{0u, 0u, 0u, 0u};
     }
+    if constexpr (TREE) load_state(wave);
 
     // ---- gates, a head in each wave, and their sums in 64 bits: differences of far sums keep their precision ----
     uint64_t word = (2ull << lane) - 1;
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
     __syncthreads();
 
     // ---- keys and queries as operands ----
-    if (h0 % r == 0) {
+    if (!TREE && h0 % r == 0) {
 #pragma unroll
         for (int i = 0; i < C::kTiles / 4; ++i) {
             const int tile = 4 * i + wave;                 // [row tile][DK / 32]
@@ -395,19 +412,22 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
                 }
             const int up = kTop - max(exponent(top_of_column(top)), -60);
             if (b == 0) tau[row] = up;
+            if constexpr (TREE) __syncthreads();               // X is done with: T comes in its place
+            uint8_t *const tiles = TREE ? reinterpret_cast<uint8_t *>(&X[0][0]) : to;
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
                 if (2 * d > wave) continue;
                 const Split x = split(f4{t[d][0], t[d][1], t[d][2], t[d][3]}, f4{t[d][4], t[d][5], t[d][6], t[d][7]}, times2(1.0f, up));
                 const int tile = tile_of(wave, d);
-                *reinterpret_cast<h8 *>(to + C::kHigh + 1024 * tile + 16 * lane) = x.hi;
-                *reinterpret_cast<h8 *>(to + C::kLow + 1024 * tile + 16 * lane) = x.lo;
+                *reinterpret_cast<h8 *>(tiles + C::kHigh + 1024 * tile + 16 * lane) = x.hi;
+                *reinterpret_cast<h8 *>(tiles + C::kLow + 1024 * tile + 16 * lane) = x.lo;
             }
         }
         __syncthreads();
 
         // ---- products with the queries: by what the rows of U carry, through LDS into operands ----
         _Float16 *const P = reinterpret_cast<_Float16 *>(&A[0][0]);      // [64][kP]
+        float *const rows = TREE ? tree_rows : reinterpret_cast<float *>(to + C::kRows);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt > wave) continue;
@@ -426,12 +446,12 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
             const float by = times2(1.0f, up);
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)(p[nt][j] * by);
-            if (m == 0) reinterpret_cast<float *>(to + C::kRows + C::kFromU)[row] = times2(1.0f, -up);
+            if (m == 0) rows[C::kFromU / 4 + row] = times2(1.0f, -up);
         }
         // (a wave reads the rows that it wrote)
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
-            if (2 * d > wave) continue;
+            if (TREE || 2 * d > wave) continue;
             const _Float16 *const from = P + (16 * wave + m) * kP + 32 * d + 4 * b;
             const h4 lo = *reinterpret_cast<const h4 *>(from), hi4 = *reinterpret_cast<const h4 *>(from + 16);
             *reinterpret_cast<h8 *>(to + C::kWithin + 1024 * tile_of(wave, d) + 16 * lane) =
@@ -440,17 +460,149 @@ __global__ void __launch_bounds__(256, 3) chunk_prep_kernel(DeltaArgs a, Segment
 
         // ---- what goes by rows ----
         if (wave == 0) {
-            float *const rows = reinterpret_cast<float *>(to + C::kRows);
             const float grow = exp_f32((float)G[lane]), nan = __builtin_nanf("");
             const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[lane])) * kf[lane], -tau[lane]);
             const int up = -25 - max(exponent(top_of_column(top_of_row(weigh))), -120);
             rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
             rows[C::kWeigh / 4 + lane] = times2(weigh, up);
             rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
-            reinterpret_cast<uint64_t *>(to + C::kRows + C::kKin)[lane] = kin[lane];
-            if (lane == 0) {
+            if (!TREE && lane == 0) {
                 rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
                 reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
+            }
+        }
+    }
+
+    // ======== a tree's outputs: as chunk_scan_kernel has them, two groups of columns at a time ========
+    if constexpr (TREE) {
+        __syncthreads();
+        const uint8_t *const tiles = reinterpret_cast<const uint8_t *>(&X[0][0]);
+        const _Float16 *const P = reinterpret_cast<const _Float16 *>(&A[0][0]);
+        const int v_row = 2 * (int)a.v_stride, out_row = 2 * (int)a.out_stride;
+        const auto from = make_rsrc(static_cast<const uint16_t *>(a.v) + s.first * a.v_stride, (uint32_t)(n * v_row));
+        const auto into = make_rsrc(static_cast<const uint16_t *>(a.out) + s.first * a.out_stride, (uint32_t)(n * out_row));
+        for (int g0 = wave; g0 < a.value_dim / 16; g0 += 8) {
+            // (opaque: what does not change from one pair of groups to the next is not all kept in registers)
+            asm volatile("" : "+v"(lane), "+v"(m), "+v"(b) : : "memory");
+            if (g0 != wave) load_state(g0);
+            int at[2];                         // bytes to this lane's column
+#pragma unroll
+            for (int u = 0; u < 2; ++u) at[u] = 2 * (h0 * a.value_dim + 16 * min(g0 + 4 * u, a.value_dim / 16 - 1) + m);
+            uint16_t V[2][4][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        V[u][t][j] = __builtin_amdgcn_raw_buffer_load_b16(from, (16 * t + 4 * b + j) * v_row + at[u], 0, 0);
+            Split x[2][kSteps];
+            float of_s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float top = 0.f;
+#pragma unroll
+                for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top = fmaxf(top, __builtin_fabsf(S[u][t][j]));
+                const int power = kTop - max(exponent(top_of_column(top)), -100);
+                of_s[u] = times2(1.0f, -power);
+#pragma unroll
+                for (int d = 0; d < kSteps; ++d) x[u][d] = split(S[u][2 * d], S[u][2 * d + 1], times2(1.0f, power));
+            }
+            f4 ks[2][4], qs[2][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                ks[0][t] = ks[1][t] = qs[0][t] = qs[1][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int d = 0; d < kSteps; ++d) {
+                    const _Float16 *const kr = &K[16 * t + m][32 * d + 4 * b], *const qr = &Q[16 * t + m][32 * d + 4 * b];
+                    const h8 k = __builtin_shufflevector(*reinterpret_cast<const h4 *>(kr), *reinterpret_cast<const h4 *>(kr + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+                    const h8 q = __builtin_shufflevector(*reinterpret_cast<const h4 *>(qr), *reinterpret_cast<const h4 *>(qr + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        ks[u][t] = mfma16x16x32(k, x[u][d].hi, ks[u][t]);
+                        qs[u][t] = mfma16x16x32(q, x[u][d].hi, qs[u][t]);
+                        ks[u][t] = mfma16x16x32(k, x[u][d].lo, ks[u][t]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (g0 + 4 * u >= a.value_dim / 16) break;
+                f4 R[4];
+                float top = 0.f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const f4 off = *reinterpret_cast<const f4 *>(&tree_rows[C::kOff / 4 + 16 * t + 4 * b]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        R[t][j] = __builtin_fmaf(-(off[j] * of_s[u]), ks[u][t][j], lo_f32<BF>(V[u][t][j]));
+                        top = __builtin_elementwise_maximum(top, __builtin_fabsf(R[t][j]));
+                    }
+                }
+                top = top_of_column(top);
+                uint64_t lost = 0;             // rows that come after one that is not finite
+                if (__builtin_amdgcn_ballot_w64(!(top < __builtin_inff()))) {
+                    uint64_t found = 0;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            found |= __builtin_fabsf(R[t][j]) < __builtin_inff() ? 0ull : 1ull << (16 * t + 4 * b + j);
+                    found |= __shfl_xor(found, 16);
+                    found |= __shfl_xor(found, 32);
+                    for (int row = 0; row < kChunk; ++row) lost |= kin[row] & found ? 1ull << row : 0ull;
+                    top = 0.f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            R[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? 0.f : R[t][j];
+                            top = fmaxf(top, __builtin_fabsf(R[t][j]));
+                        }
+                    top = top_of_column(top);
+                }
+                const int up = kTop - max(exponent(top), -100);
+                const Split r0 = split(R[0], R[1], times2(1.0f, up)), r1 = split(R[2], R[3], times2(1.0f, up));
+                f4 U[4], o[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    U[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int d = 0; d <= t / 2; ++d) {
+                        const h8 hi = *reinterpret_cast<const h8 *>(tiles + C::kHigh + 1024 * tile_of(t, d) + 16 * lane);
+                        const h8 lo = *reinterpret_cast<const h8 *>(tiles + C::kLow + 1024 * tile_of(t, d) + 16 * lane);
+                        const Split &rows = d ? r1 : r0;
+                        U[t] = mfma16x16x32(hi, rows.hi, U[t]);
+                        U[t] = mfma16x16x32(hi, rows.lo, U[t]);
+                        U[t] = mfma16x16x32(lo, rows.hi, U[t]);
+                    }
+                }
+                h8 v[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * (1.0f / (1 << 20)));
+                const float of_u = times2(1.0f, 20 - up);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                    for (int d = 0; d <= t / 2; ++d) {
+                        const _Float16 *const pr = P + (16 * t + m) * kP + 32 * d + 4 * b;
+                        const h8 p = __builtin_shufflevector(*reinterpret_cast<const h4 *>(pr), *reinterpret_cast<const h4 *>(pr + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+                        o[t] = mfma16x16x32(p, v[d], o[t]);
+                    }
+                    const f4 fs = *reinterpret_cast<const f4 *>(&tree_rows[C::kFromS / 4 + 16 * t + 4 * b]);
+                    const f4 fu = *reinterpret_cast<const f4 *>(&tree_rows[C::kFromU / 4 + 16 * t + 4 * b]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = 16 * t + 4 * b + j;
+                        float y = __builtin_fmaf(fs[j] * of_s[u], qs[u][t][j], (fu[j] * of_u) * o[t][j]);
+                        y = lost >> row & 1 ? __builtin_nanf("") : y;
+                        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack2<BF>(y, 0.f), into, row * out_row + at[u], 0, 0);
+                    }
+                }
             }
         }
     }
@@ -468,7 +620,7 @@ __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
 // next state needs, for sixteen columns; wave GROUPS + w, on the same SIMD, their outputs, from the state and
 // the rows U that the first hands over in LDS, and the copies.  (All in one wave, the only one on its SIMD,
 // a chunk took 9300 cycles, of which instructions took 3300.)
-template <bool BF, int DK, bool TREE, int GROUPS>
+template <bool BF, int DK, int GROUPS>
 __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
@@ -481,7 +633,6 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
     const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
     Seq s;
     if (!seq_of(a.s, seg.first_seq + blockIdx.z, &s)) return;
-    if (TREE) s.n = min(s.n, kChunk);
     const int first = kChunk * seg.first_chunk;
     if (first >= s.n) return;
     const int count = min(seg.chunks, (s.n - first + kChunk - 1) / kChunk);
@@ -708,12 +859,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                     found |= __builtin_fabsf(R[t][j]) < __builtin_inff() ? 0ull : 1ull << (16 * t + 4 * b + j);
             found |= __shfl_xor(found, 16);
             found |= __shfl_xor(found, 32);
-            if constexpr (TREE) {
-                for (int row = 0; row < kChunk; ++row)
-                    lost |= lds_get<uint64_t>(val + C::kRows + C::kKin + 8 * row) & found ? 1ull << row : 0ull;
-            } else {
-                lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
-            }
+            lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
             top_r = 0.f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -748,17 +894,13 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 kt[t][d] = __builtin_bit_cast(h8, u4{part[0][0], part[0][1], part[1][0], part[1][1]});
             }
         };
-        if constexpr (!TREE) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
-        }
+        for (int t = 0; t < 4; ++t) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
         __builtin_amdgcn_sched_barrier(kHold);
         {
             const Split r0 = split(R[0], R[1], by_r), r1 = split(R[2], R[3], by_r);
-            if constexpr (!TREE) {
 #pragma unroll
-                for (int t = 0; t < kRowTiles; ++t) load_kt(t);
-            }
+            for (int t = 0; t < kRowTiles; ++t) load_kt(t);
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -788,7 +930,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         lds_barrier();                         // (3) and U
 
         // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
-        if constexpr (!TREE) {
+        {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -813,7 +955,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             }
         }
     }
-    if constexpr (!TREE) {
+    {
         if (s.state < 0 && s.n - first <= kChunk * seg.chunks) return;     // (kept for the next segment only)
         float *const to = pool + (int64_t)(4 * b) * a.value_dim + col;
 #pragma unroll
@@ -825,7 +967,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 
 size_t key_bytes(const DeltaArgs &a) { return a.key_dim == 64 ? Chunk<64>::kKey : Chunk<128>::kKey; }
 size_t chunk_bytes(const DeltaArgs &a) { return a.k_heads * key_bytes(a) + (size_t)a.v_heads * Chunk<128>::kValue; }
-int chunks_of(const DeltaArgs &a) { return a.s.tree ? 1 : (a.s.max_q + kChunk - 1) / kChunk; }
+int chunks_of(const DeltaArgs &a) { return (a.s.max_q + kChunk - 1) / kChunk; }
 
 // How a call is cut: sequences and chunks of each that the workspace holds at a time.
 struct Cut {
@@ -840,9 +982,52 @@ Cut cut_of(const DeltaArgs &a) {
     return c;
 }
 
+template <bool BF, int DK>
+hipError_t launch_row(const DeltaArgs &a, hipStream_t stream) {
+    const Cut c = cut_of(a);
+    Segment seg;
+    seg.keys = static_cast<uint8_t *>(a.workspace);
+    seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<DK>::kKey;
+    seg.carry = reinterpret_cast<float *>(seg.values + (size_t)c.chunks * c.batch * a.v_heads * Chunk<DK>::kValue);
+    for (int b0 = 0; b0 < a.s.batch; b0 += c.batch) {
+        for (int c0 = 0; c0 < chunks_of(a); c0 += c.chunks) {
+            seg.first_seq = b0;
+            seg.batch = std::min(c.batch, a.s.batch - b0);
+            seg.first_chunk = c0;
+            seg.chunks = std::min(c.chunks, chunks_of(a) - c0);
+            // value heads that share a key head in one workgroup, as long as that leaves some for every CU
+            int heads = 1;
+            for (int i = 2; i <= kMostHeads; ++i)
+                if (a.v_heads / a.k_heads % i == 0 && (int64_t)seg.chunks * a.v_heads / i * seg.batch >= 512) heads = i;
+            chunk_prep_kernel<BF, DK, false><<<dim3(seg.chunks, a.v_heads / heads, seg.batch), 256, 0, stream>>>(a, seg, heads);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            // 32 columns a workgroup while each finds a CU of its own, else 64 (one sequence of 8191 tokens, 48
+            // heads: 290 and 352 us; five of 333 to 2500, 32 heads: 104 and 86)
+            if ((int64_t)a.value_dim / 32 * a.v_heads * seg.batch <= 256)
+                chunk_scan_kernel<BF, DK, 2><<<dim3(a.value_dim / 32, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
+            else
+                chunk_scan_kernel<BF, DK, 4><<<dim3(a.value_dim / 64, a.v_heads, seg.batch), 512, 0, stream>>>(a, seg);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+template <bool BF, int DK>
+hipError_t launch_tree(const DeltaArgs &a, hipStream_t stream) {
+    Segment seg{};
+    seg.batch = a.s.batch;
+    seg.chunks = 1;
+    chunk_prep_kernel<BF, DK, true><<<dim3(1, a.v_heads, a.s.batch), 256, 0, stream>>>(a, seg, 1);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
+    if (a.s.tree) return 0;
     const Cut c = cut_of(a);
     size_t bytes = chunk_bytes(a) * c.chunks * c.batch;
     if (c.chunks < chunks_of(a)) bytes += (size_t)c.batch * a.v_heads * a.key_dim * a.value_dim * 4;
@@ -850,44 +1035,13 @@ size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
 }
 
 hipError_t launch_delta_chunk(const DeltaArgs &a, hipStream_t stream) {
-    const Cut c = cut_of(a);
-    auto go = [&](auto bf, auto dk, auto tree) {
-        Segment seg;
-        seg.keys = static_cast<uint8_t *>(a.workspace);
-        seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<dk()>::kKey;
-        seg.carry = reinterpret_cast<float *>(seg.values + (size_t)c.chunks * c.batch * a.v_heads * Chunk<dk()>::kValue);
-        for (int b0 = 0; b0 < a.s.batch; b0 += c.batch) {
-            for (int c0 = 0; c0 < chunks_of(a); c0 += c.chunks) {
-                seg.first_seq = b0;
-                seg.batch = std::min(c.batch, a.s.batch - b0);
-                seg.first_chunk = c0;
-                seg.chunks = std::min(c.chunks, chunks_of(a) - c0);
-                // value heads that share a key head in one workgroup, as long as that leaves some for every CU
-                int heads = 1;
-                for (int i = 2; i <= kMostHeads; ++i)
-                    if (a.v_heads / a.k_heads % i == 0 && (int64_t)seg.chunks * a.v_heads / i * seg.batch >= 512) heads = i;
-                chunk_prep_kernel<bf(), dk(), tree()><<<dim3(seg.chunks, a.v_heads / heads, seg.batch), 256, 0, stream>>>(a, seg, heads);
-                hipError_t e = hipGetLastError();
-                if (e != hipSuccess) return e;
-                // 32 columns a workgroup while each finds a CU of its own, else 64 (one sequence of 8191 tokens, 48
-                // heads: 290 and 352 us; five of 333 to 2500, 32 heads: 104 and 86)
-                if ((int64_t)a.value_dim / 32 * a.v_heads * seg.batch <= 256)
-                    chunk_scan_kernel<bf(), dk(), tree(), 2>
-                        <<<dim3(a.value_dim / 32, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
-                else
-                    chunk_scan_kernel<bf(), dk(), tree(), 4>
-                        <<<dim3(a.value_dim / 64, a.v_heads, seg.batch), 512, 0, stream>>>(a, seg);
-                e = hipGetLastError();
-                if (e != hipSuccess) return e;
-            }
-        }
-        return hipSuccess;
+    auto go = [&](auto bf, auto dk) {
+        return a.s.tree ? launch_tree<bf(), dk()>(a, stream) : launch_row<bf(), dk()>(a, stream);
     };
-    auto sized = [&](auto bf, auto tree) {
-        return a.key_dim == 64 ? go(bf, std::integral_constant<int, 64>{}, tree) : go(bf, std::integral_constant<int, 128>{}, tree);
+    auto sized = [&](auto bf) {
+        return a.key_dim == 64 ? go(bf, std::integral_constant<int, 64>{}) : go(bf, std::integral_constant<int, 128>{});
     };
-    auto typed = [&](auto tree) { return a.bf16 ? sized(std::true_type{}, tree) : sized(std::false_type{}, tree); };
-    return a.s.tree ? typed(std::true_type{}) : typed(std::false_type{});
+    return a.bf16 ? sized(std::true_type{}) : sized(std::false_type{});
 }
 
 }  // namespace w4a16
