@@ -624,9 +624,10 @@ template <bool BF, int DK, int GROUPS>
 __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, Segment seg) {
     using C = Chunk<DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
-    // two chunks, each with V's columns of this workgroup; and for each group the state and U as operands, what comes off their sums, and rows that are lost
+    // two chunks, each with V's columns of this workgroup; and for each group the state as operands, U, what
+    // comes off their sums, and rows that are lost
     constexpr int kColumnBytes = 32 * GROUPS, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
-    constexpr int kFactors = (kSteps + 2) * 1024, kHand = kFactors + 1024;
+    constexpr int kU = kSteps * 1024, kFactors = kU + 4096, kHand = kFactors + 1024;
     __shared__ __align__(16) uint8_t lds_raw[2 * kStage + GROUPS * kHand];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
@@ -642,7 +643,6 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
     const int col = 16 * (blockIdx.x * GROUPS + group) + m;
     lds_u8 *const hand = lds + 2 * kStage + group * kHand;
     lds_u8 *const factors = hand + kFactors + 4 * lane, *const lost_at = hand + kFactors + 512 + 8 * lane;
-    constexpr int kHold = 0;                   // of sched_barrier: nothing passes
 
     if (wave >= GROUPS) {
         // ======== outputs and copies ========
@@ -673,24 +673,21 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                                                          v_at + (GROUPS * i + group) * (1024 / kColumnBytes) * v_row, 0, 0, 0);
         };
         copy(0);
+        if (count > 1) copy(1);
+        wait_loads<0>();
+        lds_barrier();                         // (0) the first chunk is there
         for (int ci = 0; ci < count; ++ci) {
-            // this chunk is there; the two stores of the last outputs may be under way
-            if (ci == 0) wait_loads<0>();
-            else wait_loads<2>();
-            lds_barrier();                     // (1) and the other chunk's place is free
-            if (ci + 1 < count) copy(ci + 1);
             const lds_u8 *const at = lds + (ci & 1) * kStage;
             const lds_u8 *const mine = at + 16 * lane, *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
-            h8 q[kSteps][4];
+            lds_barrier();                     // (1) the state is handed over
+            f4 qs[4], fs[4], fu[4], o[4];
+            h8 within[6], x[kSteps], q[kSteps][4];
 #pragma unroll
-            for (int d = 0; d < kSteps; ++d)
+            for (int d = 0; d < kSteps; ++d) {
+                x[d] = lds_get<h8>(hand + 1024 * d + 16 * lane);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) q[d][t] = lds_get<h8>(mine + 1024 * (C::kTiles + t * kSteps + d));
-            lds_barrier();                     // (2) the state is handed over
-            f4 qs[4], fs[4], fu[4], o[4];
-            h8 within[6], x[kSteps];
-#pragma unroll
-            for (int d = 0; d < kSteps; ++d) x[d] = lds_get<h8>(hand + 1024 * d + 16 * lane);
+            }
 #pragma unroll
             for (int i = 0; i < 6; ++i) within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
 #pragma unroll
@@ -699,15 +696,26 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
                 qs[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
             }
-            __builtin_amdgcn_sched_barrier(kHold);
 #pragma unroll
             for (int d = 0; d < kSteps; ++d)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(q[d][t], x[d], qs[t]);
-            lds_barrier();                     // (3) and U
+            // the next chunk is there; the two stores of the last outputs may be under way
+            if (ci == 0) wait_loads<0>();
+            else wait_loads<2>();
+            lds_barrier();                     // (2) U is handed over, and all of this chunk's is in registers
+            if (ci + 2 < count) copy(ci + 2);
             h8 u[2];
+            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
 #pragma unroll
-            for (int d = 0; d < 2; ++d) u[d] = lds_get<h8>(hand + 1024 * (kSteps + d) + 16 * lane);
+            for (int d = 0; d < 2; ++d) {
+                const f4 u0 = lds_get<f4>(hand + kU + 2048 * d + 16 * lane), u1 = lds_get<f4>(hand + kU + 2048 * d + 1024 + 16 * lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    u[d][e] = (_Float16)(u0[e] * kDown);
+                    u[d][4 + e] = (_Float16)(u1[e] * kDown);
+                }
+            }
             const float of_s = lds_get<float>(factors), of_u = lds_get<float>(factors + 256);
             const uint64_t lost = lds_get<uint64_t>(lost_at);
 #pragma unroll
@@ -725,16 +733,16 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
             }
-            // through LDS (the state's place, rows 48 bytes apart), so that a lane stores eight columns of a row
-            static_assert(kHand >= 48 * kChunk && (kSteps + 2) * 1024 >= 48 * kChunk, "room for the outputs");
+            // through LDS (U's place), so that a lane stores eight columns of a row
+            lds_u8 *const staged = hand + kU;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; j += 2) {
                     const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
-                    lds_u8 *const to = hand + 48 * (16 * t + 4 * b + j) + 2 * m;
+                    lds_u8 *const to = staged + 32 * (16 * t + 4 * b + j) + 2 * m;
                     lds_put(to, (uint16_t)two);
-                    lds_put(to + 48, (uint16_t)(two >> 16));
+                    lds_put(to + 32, (uint16_t)(two >> 16));
                 }
             const int n = min(kChunk, s.n - first - kChunk * ci);
             const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 32 * i + (lane >> 1);
-                const u4 eight = lds_get<u4>(hand + 48 * row + 16 * (lane & 1));
+                const u4 eight = lds_get<u4>(staged + 32 * row + 16 * (lane & 1));
                 __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
             }
         }
@@ -775,14 +783,14 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             for (int j = 0; j < 4; ++j) S[t][j] = times2(S[t][j], power);
     }
 
+    lds_barrier();                             // (0) the first chunk is there
     for (int ci = 0; ci < count; ++ci) {
-        lds_barrier();                         // (1) this chunk is there
         const lds_u8 *const at = lds + (ci & 1) * kStage, *const val = at + C::kKey;
         const lds_u8 *const rows = val + C::kRows + 16 * b;
         const lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;
 
         // Operands come out of LDS a step ahead of the products that take them, and products that add to one
-        // tile lie apart (the scheduling barriers hold the order).
+        // tile lie apart.
         h8 k[2][4];                            // K of 32 channels: four row tiles
         auto load_k = [&](int d) {
 #pragma unroll
@@ -801,7 +809,6 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         for (int t = 0; t < 4; ++t) off[t] = lds_get<f4>(rows + C::kOff + 64 * t);
         const float gamma = lds_get<float>(val + C::kRows + C::kLast);
         const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
-        __builtin_amdgcn_sched_barrier(kHold);
 
         // ---- K S ----
         f4 ks[4];
@@ -819,16 +826,14 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                     tl[i] = lds_get<h8>(val + C::kLow + 1024 * i + 16 * lane);
                 }
             }
-            __builtin_amdgcn_sched_barrier(kHold);
             const Split x = split(S[2 * d], S[2 * d + 1], 1.0f);
             lds_put(hand + 1024 * d + 16 * lane, x.hi);
 #pragma unroll
             for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.hi, ks[t]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.lo, ks[t]);
-            __builtin_amdgcn_sched_barrier(kHold);
         }
-        lds_barrier();                         // (2) the state is handed over
+        lds_barrier();                         // (1) the state is handed over
         float top_s = 0.f;                     // for the next S
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
@@ -896,7 +901,6 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         };
 #pragma unroll
         for (int t = 0; t < 4; ++t) weigh[t] = lds_get<f4>(rows + C::kWeigh + 64 * t);
-        __builtin_amdgcn_sched_barrier(kHold);
         {
             const Split r0 = split(R[0], R[1], by_r), r1 = split(R[2], R[3], by_r);
 #pragma unroll
@@ -913,21 +917,12 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                         U[t] = mfma16x16x32(part < 2 ? th[tile_of(t, d)] : tl[tile_of(t, d)], part == 1 ? r.lo : r.hi, U[t]);
                     }
         }
-        __builtin_amdgcn_sched_barrier(kHold);
-        {
-            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                h8 u;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
-                lds_put(hand + 1024 * (kSteps + d) + 16 * lane, u);
-            }
-            lds_put(factors, of_s);
-            lds_put(factors + 256, times2(1.0f, 20 - up_r));
-            lds_put(lost_at, lost);
-        }
-        lds_barrier();                         // (3) and U
+        for (int t = 0; t < 4; ++t) lds_put(hand + kU + 1024 * t + 16 * lane, U[t]);
+        lds_put(factors, of_s);
+        lds_put(factors + 256, times2(1.0f, 20 - up_r));
+        lds_put(lost_at, lost);
+        lds_barrier();                         // (2) and U, and the next chunk is there
 
         // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
         {
