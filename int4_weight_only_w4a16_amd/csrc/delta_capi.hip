@@ -90,8 +90,13 @@ extern "C" int w4a16_short_conv(const void *x, int64_t x_stride, const float *we
     return launched(w4a16::launch_short_conv(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
-// Most tokens of a sequence that go token by token.
-static constexpr int64_t kStepTokens = 8;
+// Most tokens of a sequence that go token by token.  In steps and in chunks, us, 48 heads of 128 x 128
+// (32 of 64 x 128):
+//   tokens              8                 16                24
+//   1 sequence      11 (9) and 17 (14)  18 (14) and 17 (15)   24 (20) and 17 (14)
+//   8               22 (13) and 40 (24) 37 (21) and 40 (25)   51 (28) and 40 (25)
+//   32              63 (34) and 104 (58) 111 (61) and 105 (58) 159 (86) and 107 (59)
+static constexpr int64_t kStepTokens = 16;
 
 static bool in_chunks(const w4a16::DeltaArgs &d) { return d.s.tree || d.s.max_q > kStepTokens; }
 

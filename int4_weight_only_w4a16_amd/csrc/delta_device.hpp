@@ -30,15 +30,20 @@ struct Gates {
     float g, beta;
 };
 
+// From the projections x = a + dt_bias and b: g = -rate softplus(x), beta = sigmoid(b).
+__device__ __forceinline__ Gates gates_from(float a, float b, float rate, float bias) {
+    const float x = a + bias;
+    // log1p keeps softplus precise where e^x is small, as it is for heads that forget slowly
+    const float soft = fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+    return {x != x ? x : -rate * soft, 1.0f / (1.0f + expf(-b))};
+}
+
 template <bool BF>
 __device__ __forceinline__ Gates gates_of(const DeltaArgs &a, int64_t row, int h, float rate, float bias) {
     if (!a.a_log)
         return {static_cast<const float *>(a.a)[row * a.a_stride + h], static_cast<const float *>(a.b)[row * a.b_stride + h]};
-    const float x = lo_f32<BF>(static_cast<const uint16_t *>(a.a)[row * a.a_stride + h]) + bias;
-    const float y = lo_f32<BF>(static_cast<const uint16_t *>(a.b)[row * a.b_stride + h]);
-    // softplus; log1p keeps its precision where e^x is small, as it is for heads that forget slowly
-    const float soft = fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-    return {x != x ? x : -rate * soft, 1.0f / (1.0f + expf(-y))};
+    return gates_from(lo_f32<BF>(static_cast<const uint16_t *>(a.a)[row * a.a_stride + h]),
+                      lo_f32<BF>(static_cast<const uint16_t *>(a.b)[row * a.b_stride + h]), rate, bias);
 }
 
 }  // namespace w4a16

@@ -15,12 +15,20 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kColumns = 16;
+constexpr int kColumns = 16;           // of a wave
+constexpr int kWaves = 4;              // of a workgroup: whole lines of memory (64 sequences: 67 us, with one wave 95)
 
-__device__ __forceinline__ float over_rows(float v) {      // sum over the lanes of one column
-#pragma unroll
-    for (int d = 4; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+// Sum over the lanes of one column, those that are equal mod 4, without LDS.
+__device__ __forceinline__ float over_rows(float v) {
+#define W4A16_ADD_ROR(N) \
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + N, 0xF, 0xF, true))
+    W4A16_ADD_ROR(8);
+    W4A16_ADD_ROR(4);
+#undef W4A16_ADD_ROR
+    const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
 }
 
 // x / sqrt(sum x^2 + eps) over the lanes of a column; in 64 bits where squares leave fp32.
@@ -31,7 +39,7 @@ __device__ __forceinline__ void to_unit(float (&x)[N], float eps) {
     for (int i = 0; i < N; ++i) sum = __builtin_fmaf(x[i], x[i], sum);
     sum = over_rows(sum) + eps;
     if (sum > 1e-30f && sum < 1e38f) {
-        const float f = 1.0f / sqrtf(sum);
+        const float f = __builtin_amdgcn_rsqf(sum);        // (within 2^-23)
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] *= f;
         return;
@@ -44,47 +52,67 @@ __device__ __forceinline__ void to_unit(float (&x)[N], float eps) {
     for (int i = 0; i < N; ++i) x[i] = (float)(x[i] * f);
 }
 
+// What a lane needs of one token.
+template <int ROWS>
+struct Token {
+    u2 q[ROWS / 4], k[ROWS / 4], v;
+};
+
 template <bool BF, int DK>
-__global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(64 * kWaves) step_kernel(DeltaArgs a) {
     constexpr int kRows = DK / 16;
-    const int lane = threadIdx.x, r = lane >> 2, col = blockIdx.x * kColumns + 4 * (lane & 3);
+    const int lane = threadIdx.x & 63, r = lane >> 2;
+    const int col = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * kColumns + 4 * (lane & 3);
     const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
     Seq s;
     if (!seq_of(a.s, blockIdx.z, &s)) return;
 
     float *const state = a.state + ((max(s.state, (int64_t)0) * a.v_heads + h) * DK + kRows * r) * a.value_dim + col;
     f4 S[kRows];
+    if (s.fresh) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-        S[i] = s.fresh ? f4{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const f4 *>(state + (int64_t)i * a.value_dim);
-    const float rate = a.a_log ? expf(a.a_log[h]) : 0.f, bias = a.a_log ? a.dt_bias[h] : 0.f;
+        for (int i = 0; i < kRows; ++i) S[i] = f4{0.f, 0.f, 0.f, 0.f};
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) S[i] = *reinterpret_cast<const f4 *>(state + (int64_t)i * a.value_dim);
+    }
     const uint16_t *const q0 = static_cast<const uint16_t *>(a.q) + hk * DK + kRows * r;
     const uint16_t *const k0 = static_cast<const uint16_t *>(a.k) + hk * DK + kRows * r;
     const uint16_t *const v0 = static_cast<const uint16_t *>(a.v) + h * a.value_dim + col;
-
-    auto token = [&](int t) {
+    auto load = [&](int t) {
         const int64_t row = s.first + t;
-        float q[kRows], k[kRows], v[4];
+        Token<kRows> x;
 #pragma unroll
-        for (int i = 0; i < kRows; i += 4) {
-            const u2 qq = *reinterpret_cast<const u2 *>(q0 + row * a.q_stride + i);
-            const u2 kk = *reinterpret_cast<const u2 *>(k0 + row * a.k_stride + i);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                q[i + 2 * e] = lo_f32<BF>(qq[e]);
-                q[i + 2 * e + 1] = hi_f32<BF>(qq[e]);
-                k[i + 2 * e] = lo_f32<BF>(kk[e]);
-                k[i + 2 * e + 1] = hi_f32<BF>(kk[e]);
-            }
+        for (int i = 0; i < kRows / 4; ++i) {
+            x.q[i] = *reinterpret_cast<const u2 *>(q0 + row * a.q_stride + 4 * i);
+            x.k[i] = *reinterpret_cast<const u2 *>(k0 + row * a.k_stride + 4 * i);
         }
-        const u2 vv = *reinterpret_cast<const u2 *>(v0 + row * a.v_stride);
-        v[0] = lo_f32<BF>(vv[0]);
-        v[1] = hi_f32<BF>(vv[0]);
-        v[2] = lo_f32<BF>(vv[1]);
-        v[3] = hi_f32<BF>(vv[1]);
-        const Gates gate = gates_of<BF>(a, row, h, rate, bias);
-        const float keep = expf(gate.g);
+        x.v = *reinterpret_cast<const u2 *>(v0 + row * a.v_stride);
+        return x;
+    };
 
+    Token<kRows> next = load(0);
+    const float rate = a.a_log ? expf(a.a_log[h]) : 0.f, bias = a.a_log ? a.dt_bias[h] : 0.f;
+    float all_keep = 0.f, all_beta = 0.f;      // of 64 tokens, one in each lane
+    for (int t = 0; t < s.n; ++t) {
+        const Token<kRows> x = next;
+        if (t + 1 < s.n) next = load(t + 1);
+        if (t % 64 == 0) {
+            const Gates gate = t + lane < s.n ? gates_of<BF>(a, s.first + t + lane, h, rate, bias) : Gates{0.f, 0.f};
+            all_keep = expf(gate.g);
+            all_beta = gate.beta;
+        }
+        const float keep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all_keep), t % 64));
+        const float beta = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all_beta), t % 64));
+        float q[kRows], k[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; i += 2) {
+            q[i] = lo_f32<BF>(x.q[i / 4][i / 2 % 2]);
+            q[i + 1] = hi_f32<BF>(x.q[i / 4][i / 2 % 2]);
+            k[i] = lo_f32<BF>(x.k[i / 4][i / 2 % 2]);
+            k[i + 1] = hi_f32<BF>(x.k[i / 4][i / 2 % 2]);
+        }
+        const f4 v = {lo_f32<BF>(x.v[0]), hi_f32<BF>(x.v[0]), lo_f32<BF>(x.v[1]), hi_f32<BF>(x.v[1])};
         if (a.unit) {
             to_unit(k, a.eps);
             to_unit(q, a.eps);
@@ -103,19 +131,15 @@ __global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
             sk[e] = over_rows(sk[e]);
             sq[e] = over_rows(sq[e]);
         }
-        f4 u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = gate.beta * (v[e] - keep * sk[e]);
+        const f4 u = beta * (v - keep * sk);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) S[i] = keep * S[i] + k[i] * u;
         if (r == 0) {
             const f4 o = a.scale * (keep * sq + qk * u);
-            *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + row * a.out_stride + (int64_t)h * a.value_dim + col) =
+            *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + (s.first + t) * a.out_stride + (int64_t)h * a.value_dim + col) =
                 pack4<BF>(o[0], o[1], o[2], o[3]);
         }
-    };
-
-    for (int t = 0; t < s.n; ++t) token(t);
+    }
     if (s.state < 0) return;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) *reinterpret_cast<f4 *>(state + (int64_t)i * a.value_dim) = S[i];
@@ -124,9 +148,9 @@ __global__ void __launch_bounds__(64) step_kernel(DeltaArgs a) {
 }  // namespace
 
 hipError_t launch_delta_step(const DeltaArgs &a, hipStream_t stream) {
-    const dim3 grid(a.value_dim / kColumns, a.v_heads, a.s.batch);
+    const dim3 grid(a.value_dim / (kColumns * kWaves), a.v_heads, a.s.batch);
     auto go = [&](auto bf, auto dk) {
-        step_kernel<bf(), dk()><<<grid, 64, 0, stream>>>(a);
+        step_kernel<bf(), dk()><<<grid, 64 * kWaves, 0, stream>>>(a);
         return hipGetLastError();
     };
     auto typed = [&](auto dk) { return a.bf16 ? go(std::true_type{}, dk) : go(std::false_type{}, dk); };
