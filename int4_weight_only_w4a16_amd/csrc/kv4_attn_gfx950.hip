@@ -672,6 +672,44 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Kv4AttnArgs a, Plan plan) {
         a.lse[at * a.q_heads + head] = total == 0.f ? -__builtin_inff() : (m + __log2f(total)) * (1.0f / kLog2e);
 }
 
+// The same for trees, which have many rows: D/4 lanes take a whole row each, so that a workgroup joins
+// 1024 / D of them (12 trees of 5 to 37 drafts over 900 to 12000 slots, four chunks: 21 us a row at a
+// time, 6.5 here; 7 over 1000, six chunks: 4.3 and 6.1).
+template <bool BF, int D>
+__global__ void __launch_bounds__(kJoin) join_rows_kernel(Kv4AttnArgs a, Plan plan) {
+    constexpr int kLanes = D / 4, kSets = kJoin / kLanes;
+    const int rows = plan.rows, kvh = a.c.kv_heads, G = a.q_heads / kvh;
+    Work w;
+    const int col = blockIdx.x * kSets + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    if (!work_of(a, blockIdx.z, blockIdx.y % kvh, (blockIdx.y / kvh) * rows, rows, &w)) return;
+    const int row = w.row0 + col;
+    if (col >= rows || row >= w.rows || w.t1 - w.t0 <= plan.chunk) return;
+    const int chunks = (w.t1 - w.t0 + plan.chunk - 1) / plan.chunk;
+    const int64_t step = (int64_t)rows * (D + 2);
+    const float *part = static_cast<const float *>(a.workspace) +
+                        ((int64_t)w.b * gridDim.y + blockIdx.y) * plan.chunks * step;
+    const float *refs = part + rows * D + col, *sums = refs + rows;
+    float m = kNone, total = 0.f;
+    f4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < chunks; ++c) m = fmaxf(m, refs[c * step]);
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) {
+        const float f = __builtin_amdgcn_exp2f(refs[c * step] - m);
+        total += f * sums[c * step];
+        y += f * *reinterpret_cast<const f4 *>(part + c * step + col * D + 4 * lane);
+    }
+    const int i = row / G, head = w.h * G + row - i * G;
+    const int64_t at = w.first + i;
+    const float inv = total == 0.f ? 0.f : 1.0f / total;
+    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at * a.out_stride + (int64_t)head * D + 4 * lane) =
+        pack4<BF>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && lane == 0)
+        a.lse[at * a.q_heads + head] = total == 0.f ? -__builtin_inff() : (m + __log2f(total)) * (1.0f / kLog2e);
+}
+
+// Most chunks of a row that one set of lanes goes through, and the least workgroups of a row each from which it does.
+constexpr int kJoinChunks = 16, kJoinMany = 4096;
+
 template <typename F>
 hipError_t by_shape(const Kv4Cache &c, F f) {
     auto typed = [&](auto d, auto ng) {
@@ -711,7 +749,13 @@ hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
                 attend_kernel<bf(), d(), ng(), 2, false><<<grid, kThreads, 0, stream>>>(a, p);
         }
         hipError_t e = hipGetLastError();
-        if (e == hipSuccess && p.chunks > 1) {
+        const int64_t of_row = (int64_t)std::min(p.rows, rows_of(a)) * grid.y * grid.z;
+        if (e == hipSuccess && p.chunks > 1 && a.tree && p.chunks <= kJoinChunks && of_row >= kJoinMany) {
+            constexpr int kSets = 4 * kJoin / d();
+            join_rows_kernel<bf(), d()>
+                <<<dim3((std::min(p.rows, rows_of(a)) + kSets - 1) / kSets, grid.y, grid.z), kJoin, 0, stream>>>(a, p);
+            e = hipGetLastError();
+        } else if (e == hipSuccess && p.chunks > 1) {
             join_kernel<bf(), d()><<<dim3(std::min(p.rows, rows_of(a)), grid.y, grid.z), kJoin, 0, stream>>>(a, p);
             e = hipGetLastError();
         }

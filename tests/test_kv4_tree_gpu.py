@@ -260,3 +260,15 @@ def test_binding_refusals(dev):
         with pytest.raises(w4.W4A16Error) as e:
             w4.kv4_tree_attention(**args(words, **kw))
         assert e.value.status == w4.W4A16_ERR_SHAPE
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,group,hq", [(64, 64, 8), (128, 32, 8), (128, 64, 40), (256, 128, 16)])
+def test_many_trees_split_over_workgroups(dev, D, group, hq, dtype):
+    """Enough rows, and slots, that several rows are joined by a workgroup."""
+    sizes = 4 * [20, 9, 24, 1, 0, 17]
+    lens = [700, 2600, 1300, 30, 5, 1025] + 18 * [900]
+    trees, cache, q = make(21, sizes, lens, 8, D, group, 32, dtype, hq)
+    out, lse = attend(dev, cache, q, trees)
+    check(out, lse, q, cache, trees)
+    assert torch.equal(out, attend(dev, cache, q, trees)[0])
