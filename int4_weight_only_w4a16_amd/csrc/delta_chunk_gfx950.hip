@@ -672,6 +672,32 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + C::kKey + C::kValue + 1024 * (GROUPS * i + group)), 16,
                                                          v_at + (GROUPS * i + group) * (1024 / kColumnBytes) * v_row, 0, 0, 0);
         };
+        // Outputs of a chunk are stored while the next one's U is made: between (1) and (2) this wave has time
+        // left, between (2) and (1) the other one.  Through LDS (the state's place, once it is in
+        // registers), so that a lane stores eight columns of a row.
+        u2 made[4];
+        auto store = [&](int ci) {
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    lds_u8 *const to = hand + 32 * (16 * t + 4 * b + 2 * j) + 2 * m;
+                    lds_put(to, (uint16_t)made[t][j]);
+                    lds_put(to + 32, (uint16_t)(made[t][j] >> 16));
+                }
+            asm volatile("" ::: "memory");
+            const int n = min(kChunk, s.n - first - kChunk * ci);
+            const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
+                                            h * a.value_dim + blockIdx.x * (16 * GROUPS) + 16 * group,
+                                        (uint32_t)((n - 1) * out_row + 32));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 32 * i + (lane >> 1);
+                const u4 eight = lds_get<u4>(hand + 32 * row + 16 * (lane & 1));
+                __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
+            }
+        };
         copy(0);
         if (count > 1) copy(1);
         wait_loads<0>();
@@ -700,7 +726,8 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             for (int d = 0; d < kSteps; ++d)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(q[d][t], x[d], qs[t]);
-            // the next chunk is there; the two stores of the last outputs may be under way
+            if (ci > 0) store(ci - 1);
+            // the next chunk is there; the two stores may be under way
             if (ci == 0) wait_loads<0>();
             else wait_loads<2>();
             lds_barrier();                     // (2) U is handed over, and all of this chunk's is in registers
@@ -733,28 +760,10 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? __builtin_nanf("") : y[t][j];
             }
-            // through LDS (U's place), so that a lane stores eight columns of a row
-            lds_u8 *const staged = hand + kU;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    const uint32_t two = pack2<BF>(y[t][j], y[t][j + 1]);
-                    lds_u8 *const to = staged + 32 * (16 * t + 4 * b + j) + 2 * m;
-                    lds_put(to, (uint16_t)two);
-                    lds_put(to + 32, (uint16_t)(two >> 16));
-                }
-            const int n = min(kChunk, s.n - first - kChunk * ci);
-            const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
-                                            h * a.value_dim + blockIdx.x * (16 * GROUPS) + 16 * group,
-                                        (uint32_t)((n - 1) * out_row + 32));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = 32 * i + (lane >> 1);
-                const u4 eight = lds_get<u4>(staged + 32 * row + 16 * (lane & 1));
-                __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
-            }
+            for (int t = 0; t < 4; ++t) made[t] = pack4<BF>(y[t][0], y[t][1], y[t][2], y[t][3]);
         }
+        store(count - 1);
         wait_loads<0>();
         return;
     }
