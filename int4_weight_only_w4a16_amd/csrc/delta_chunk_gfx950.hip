@@ -21,7 +21,10 @@
 // products for a pair of such factors, lo x lo left out (2^-22).  Inputs are exact as they are, bfloat16
 // ones too, once a power of two for each row brings them into fp16's range; so do powers of
 // two for each row of T and each column of S and of the rows.  What goes into the output
-// alone has one part (2^-12).  Powers of two come off in fp32.
+// alone has one part (2^-12), an eighth of a bfloat16 output's own rounding.  An fp16 output would be
+// 1.7 times as far off as its rounding alone: there U has two parts and the triangle a second one
+// of e4m3 (1.1 times; five prompts 112 -> 119 us); a tree's have two of S and U (1.2 times).
+// Powers of two come off in fp32.
 //
 // What is not finite (in a key, a gate, a value) would reach earlier rows, or a tree's other
 // branches, through products with zero.  Its row is taken out as zeros and marked, and the rows
@@ -39,18 +42,21 @@ namespace {
 constexpr int kChunk = 64;
 constexpr int kTop = 14;               // operands lie below 2^kTop
 constexpr int kTopK = 0;               // and keys below 2^kTopK
+constexpr float kDown = 1.0f / (1 << 20);      // U comes out below 2^34: 64 products of 2^14 each
+constexpr float kRestUp = 64.f;        // what fp16 leaves of a number below 2^14 is at most 4; with this, 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Workspace of one chunk: for each key head K and Q as operands (tiles of 1 KiB: 64 lanes x 16
 // bytes; of K the first eight bytes of all lanes and then the others, so that its columns can be
 // read without bank conflicts as well), for each value head T in two parts, the products with the queries (the six tiles of 16 x 32
 // that are not above the diagonal), and what goes by rows.
-template <int DK>
+// For fp16 also what those products leave of their rounding, in e4m3.
+template <bool BF, int DK>
 struct Chunk {
     static constexpr int kTiles = DK / 8;                      // of K and Q each
     static constexpr int kKey = 2 * kTiles * 1024;
-    static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRows = 18 * 1024;
-    static constexpr int kValue = 20 * 1024;
+    static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRest = 18 * 1024, kRows = BF ? kRest : 21 * 1024;
+    static constexpr int kValue = kRows + 2 * 1024;
     // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
     // output of S and of U; e^G_last and the power of two in the second of them
     static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kLast = 1024;
@@ -100,6 +106,14 @@ __device__ __forceinline__ Split split(const f4 &x, const f4 &y, float by) {
     return {__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
 }
 
+// An operand of e4m3 from eight fp32 values times `by`.
+__device__ __forceinline__ int64_t in_fp8(const f4 &x, const f4 &y, float by) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * by, x[1] * by, 0, false);
+    const int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * by, y[1] * by, 0, false);
+    return __builtin_bit_cast(int64_t, u2{(uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * by, x[3] * by, lo, true),
+                                          (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2] * by, y[3] * by, hi, true)});
+}
+
 // The largest over the 16 lanes of a row of lanes (DPP: no LDS).
 __device__ __forceinline__ float top_of_row(float v) {
 #define W4A16_TOP_ROR(N) \
@@ -129,7 +143,7 @@ constexpr int kMostHeads = 4;          // value heads of a workgroup
 // is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 36 us with the outputs in a launch of their own).
 template <bool BF, int DK, bool TREE>
 __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
-    using C = Chunk<DK>;
+    using C = Chunk<BF, DK>;
     constexpr int kStride = DK + 8, kA = 68, kP = 72;
     // keys and queries, and A and X (of a chunk among others in their place)
     constexpr int kPart = kChunk * (2 * kStride > 4 * kA ? 2 * kStride : 4 * kA);
@@ -427,6 +441,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
 
         // ---- products with the queries: by what the rows of U carry, through LDS into operands ----
         _Float16 *const P = reinterpret_cast<_Float16 *>(&A[0][0]);      // [64][kP]
+        uint8_t *const left = reinterpret_cast<uint8_t *>(P + kChunk * kP);
+        static_assert(sizeof(A) >= kChunk * kP * 3, "both in A's place");
         float *const rows = TREE ? tree_rows : reinterpret_cast<float *>(to + C::kRows);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -445,7 +461,15 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             const int up = kTop - max(exponent(top_of_row(top)), -100);
             const float by = times2(1.0f, up);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) P[row * kP + 16 * nt + m] = nt > wave ? (_Float16)0.f : (_Float16)(p[nt][j] * by);
+            for (int nt = 0; nt < 4; ++nt) {
+                uint32_t one = nt > wave ? 0 : pack2<false>(p[nt][j] * by, 0.f);
+                asm("" : "+v"(one));           // (as in split2)
+                P[row * kP + 16 * nt + m] = __builtin_bit_cast(h2, one)[0];
+                if constexpr (!TREE && !BF) {
+                    const float rest = nt > wave ? 0.f : __builtin_fmaf(p[nt][j], by, -lo_f32<false>(one)) * kRestUp;
+                    left[row * kP + 16 * nt + m] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(rest, rest, 0, false);
+                }
+            }
             if (m == 0) rows[C::kFromU / 4 + row] = times2(1.0f, -up);
         }
         // (a wave reads the rows that it wrote)
@@ -456,6 +480,11 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             const h4 lo = *reinterpret_cast<const h4 *>(from), hi4 = *reinterpret_cast<const h4 *>(from + 16);
             *reinterpret_cast<h8 *>(to + C::kWithin + 1024 * tile_of(wave, d) + 16 * lane) =
                 __builtin_shufflevector(lo, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+            if constexpr (!BF) {
+                const uint8_t *const rest = left + (16 * wave + m) * kP + 32 * d + 4 * b;
+                *reinterpret_cast<u2 *>(to + C::kRest + 512 * tile_of(wave, d) + 8 * lane) =
+                    u2{*reinterpret_cast<const uint32_t *>(rest), *reinterpret_cast<const uint32_t *>(rest + 16)};
+            }
         }
 
         // ---- what goes by rows ----
@@ -524,6 +553,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                         ks[u][t] = mfma16x16x32(k, x[u][d].hi, ks[u][t]);
                         qs[u][t] = mfma16x16x32(q, x[u][d].hi, qs[u][t]);
                         ks[u][t] = mfma16x16x32(k, x[u][d].lo, ks[u][t]);
+                        qs[u][t] = mfma16x16x32(q, x[u][d].lo, qs[u][t]);
                     }
                 }
             }
@@ -579,11 +609,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                         U[t] = mfma16x16x32(lo, rows.hi, U[t]);
                     }
                 }
-                h8 v[2];
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * (1.0f / (1 << 20)));
+                const Split v[2] = {split(U[0], U[1], kDown), split(U[2], U[3], kDown)};
                 const float of_u = times2(1.0f, 20 - up);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -591,7 +617,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                     for (int d = 0; d <= t / 2; ++d) {
                         const _Float16 *const pr = P + (16 * t + m) * kP + 32 * d + 4 * b;
                         const h8 p = __builtin_shufflevector(*reinterpret_cast<const h4 *>(pr), *reinterpret_cast<const h4 *>(pr + 16), 0, 1, 2, 3, 4, 5, 6, 7);
-                        o[t] = mfma16x16x32(p, v[d], o[t]);
+                        o[t] = mfma16x16x32(p, v[d].hi, o[t]);
+                        o[t] = mfma16x16x32(p, v[d].lo, o[t]);
                     }
                     const f4 fs = *reinterpret_cast<const f4 *>(&tree_rows[C::kFromS / 4 + 16 * t + 4 * b]);
                     const f4 fu = *reinterpret_cast<const f4 *>(&tree_rows[C::kFromU / 4 + 16 * t + 4 * b]);
@@ -622,12 +649,12 @@ __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
 // a chunk took 9300 cycles, of which instructions took 3300.)
 template <bool BF, int DK, int GROUPS>
 __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, Segment seg) {
-    using C = Chunk<DK>;
+    using C = Chunk<BF, DK>;
     constexpr int kSteps = DK / 32, kRowTiles = DK / 16;
     // two chunks, each with V's columns of this workgroup; and for each group the state as operands, U, what
     // comes off their sums, and rows that are lost
     constexpr int kColumnBytes = 32 * GROUPS, kTile = kChunk * kColumnBytes, kStage = C::kKey + C::kValue + kTile;
-    constexpr int kU = kSteps * 1024, kFactors = kU + 4096, kHand = kFactors + 1024;
+    constexpr int kU = kSteps * 1024, kFactors = kU + 4096, kHand = kFactors + 256;
     __shared__ __align__(16) uint8_t lds_raw[2 * kStage + GROUPS * kHand];
     lds_u8 *const lds = (lds_u8 *)lds_raw;
 
@@ -642,7 +669,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
     const int lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
     const int col = 16 * (blockIdx.x * GROUPS + group) + m;
     lds_u8 *const hand = lds + 2 * kStage + group * kHand;
-    lds_u8 *const factors = hand + kFactors + 4 * lane, *const lost_at = hand + kFactors + 512 + 8 * lane;
+    lds_u8 *const factors = hand + kFactors + 4 * m, *const lost_at = hand + kFactors + 128 + 8 * m;
 
     if (wave >= GROUPS) {
         // ======== outputs and copies ========
@@ -655,13 +682,14 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             const uint8_t *const key = seg.keys + ((slot + ci) * a.k_heads + hk) * C::kKey;
             const uint8_t *const value = seg.values + ((slot + ci) * a.v_heads + h) * C::kValue;
             lds_u8 *const to = lds + (ci & 1) * kStage;
-            static_assert(C::kKey / 1024 % GROUPS == 0 && C::kValue / 1024 % GROUPS == 0, "the same in every wave");
+            static_assert(C::kKey / 1024 % GROUPS == 0, "the same in every wave");
 #pragma unroll
             for (int u = 0; u < C::kKey; u += 1024 * GROUPS)
                 copy_kib(key, C::kKey, u + 1024 * group, to + u + 1024 * group, lane);
 #pragma unroll
             for (int u = 0; u < C::kValue; u += 1024 * GROUPS)
-                copy_kib(value, C::kValue, u + 1024 * group, to + C::kKey + u + 1024 * group, lane);
+                if (u + 1024 * GROUPS <= C::kValue || u + 1024 * group < C::kValue)
+                    copy_kib(value, C::kValue, u + 1024 * group, to + C::kKey + u + 1024 * group, lane);
             // rows past the sequence's come as zeros
             const int n = min(kChunk, s.n - first - kChunk * ci);
             const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.v) + (s.first + first + (int64_t)kChunk * ci) * a.v_stride +
@@ -698,62 +726,51 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 __builtin_amdgcn_raw_buffer_store_b128(eight, rsrc, row * out_row + 16 * (lane & 1), 0, 0);
             }
         };
-        copy(0);
-        if (count > 1) copy(1);
-        wait_loads<0>();
-        lds_barrier();                         // (0) the first chunk is there
-        for (int ci = 0; ci < count; ++ci) {
-            const lds_u8 *const at = lds + (ci & 1) * kStage;
-            const lds_u8 *const mine = at + 16 * lane, *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
-            lds_barrier();                     // (1) the state is handed over
-            f4 qs[4], fs[4], fu[4], o[4];
-            h8 within[6], x[kSteps], q[kSteps][4];
+        // What the outputs of a chunk are made of waits in registers while the next one's copies are issued.
+        f4 qs[4], fs[4], fu[4], U[4];
+        h8 within[6];
+        int64_t rest[BF ? 1 : 6];
+        float of_s, of_u;
+        uint64_t lost;
+        auto make = [&] {
+            f4 o[4], r[4];
 #pragma unroll
-            for (int d = 0; d < kSteps; ++d) {
-                x[d] = lds_get<h8>(hand + 1024 * d + 16 * lane);
+            for (int t = 0; t < 4; ++t) o[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (BF) {
+                h8 u[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) q[d][t] = lds_get<h8>(mine + 1024 * (C::kTiles + t * kSteps + d));
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
+            } else {
+                const Split u[2] = {split(U[0], U[1], kDown), split(U[2], U[3], kDown)};
+                const int64_t few[2] = {in_fp8(U[0], U[1], kDown / kRestUp), in_fp8(U[2], U[3], kDown / kRestUp)};
+                // (these with accumulators of their own, and first: a product of one type does not wait for one of
+                // another as long as it must, if it adds to it)
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int t = 2 * d; t < 4; ++t)
+                        r[t] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(rest[tile_of(t, d)], few[d], r[t], 0, 0, 0);
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d].hi, o[t]);
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+#pragma unroll
+                    for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d].lo, o[t]);
             }
-#pragma unroll
-            for (int i = 0; i < 6; ++i) within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                fs[t] = lds_get<f4>(rows + C::kFromS + 64 * t);
-                fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
-                qs[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
-            }
-#pragma unroll
-            for (int d = 0; d < kSteps; ++d)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(q[d][t], x[d], qs[t]);
-            if (ci > 0) store(ci - 1);
-            // the next chunk is there; the two stores may be under way
-            if (ci == 0) wait_loads<0>();
-            else wait_loads<2>();
-            lds_barrier();                     // (2) U is handed over, and all of this chunk's is in registers
-            if (ci + 2 < count) copy(ci + 2);
-            h8 u[2];
-            constexpr float kDown = 1.0f / (1 << 20);      // U lies below 2^34: 64 products of 2^14 each
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const f4 u0 = lds_get<f4>(hand + kU + 2048 * d + 16 * lane), u1 = lds_get<f4>(hand + kU + 2048 * d + 1024 + 16 * lane);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    u[d][e] = (_Float16)(u0[e] * kDown);
-                    u[d][4 + e] = (_Float16)(u1[e] * kDown);
-                }
-            }
-            const float of_s = lds_get<float>(factors), of_u = lds_get<float>(factors + 256);
-            const uint64_t lost = lds_get<uint64_t>(lost_at);
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
             f4 y[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * o[t][j]);
+                for (int j = 0; j < 4; ++j)
+                    y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * (BF ? o[t][j] : o[t][j] + r[t][j]));
             if (__builtin_amdgcn_ballot_w64(lost != 0)) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -762,7 +779,52 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) made[t] = pack4<BF>(y[t][0], y[t][1], y[t][2], y[t][3]);
+        };
+        copy(0);
+        if (count > 1) copy(1);
+        wait_loads<0>();
+        lds_barrier();                         // (0) the first chunk is there
+        for (int ci = 0; ci < count; ++ci) {
+            const lds_u8 *const at = lds + (ci & 1) * kStage;
+            const lds_u8 *const mine = at + 16 * lane, *const val = at + C::kKey, *const rows = val + C::kRows + 16 * b;
+            lds_barrier();                     // (1) the state is handed over
+            h8 x[kSteps], q[kSteps][4];
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) {
+                x[d] = lds_get<h8>(hand + 1024 * d + 16 * lane);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) q[d][t] = lds_get<h8>(mine + 1024 * (C::kTiles + t * kSteps + d));
+            }
+            if (ci > 0) make();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) qs[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) qs[t] = mfma16x16x32(q[d][t], x[d], qs[t]);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                within[i] = lds_get<h8>(val + C::kWithin + 1024 * i + 16 * lane);
+                if constexpr (!BF) rest[i] = lds_get<int64_t>(val + C::kRest + 512 * i + 8 * lane);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                fs[t] = lds_get<f4>(rows + C::kFromS + 64 * t);
+                fu[t] = lds_get<f4>(rows + C::kFromU + 64 * t);
+            }
+            if (ci > 0) store(ci - 1);
+            // the next chunk is there; the two stores may be under way
+            if (ci == 0) wait_loads<0>();
+            else wait_loads<2>();
+            lds_barrier();                     // (2) U is handed over, and all of this chunk's is in registers
+            if (ci + 2 < count) copy(ci + 2);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) U[t] = lds_get<f4>(hand + kU + 1024 * t + 16 * lane);
+            of_s = lds_get<float>(factors);
+            of_u = lds_get<float>(factors + 64);
+            lost = lds_get<uint64_t>(lost_at);
         }
+        make();
         store(count - 1);
         wait_loads<0>();
         return;
@@ -929,7 +991,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
         for (int t = 0; t < 4; ++t) lds_put(hand + kU + 1024 * t + 16 * lane, U[t]);
         lds_put(factors, of_s);
-        lds_put(factors + 256, times2(1.0f, 20 - up_r));
+        lds_put(factors + 64, times2(1.0f, 20 - up_r));
         lds_put(lost_at, lost);
         lds_barrier();                         // (2) and U, and the next chunk is there
 
@@ -969,8 +1031,9 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
     }
 }
 
-size_t key_bytes(const DeltaArgs &a) { return a.key_dim == 64 ? Chunk<64>::kKey : Chunk<128>::kKey; }
-size_t chunk_bytes(const DeltaArgs &a) { return a.k_heads * key_bytes(a) + (size_t)a.v_heads * Chunk<128>::kValue; }
+size_t key_bytes(const DeltaArgs &a) { return a.key_dim == 64 ? Chunk<true, 64>::kKey : Chunk<true, 128>::kKey; }
+size_t value_bytes(const DeltaArgs &a) { return a.bf16 ? Chunk<true, 128>::kValue : Chunk<false, 128>::kValue; }
+size_t chunk_bytes(const DeltaArgs &a) { return a.k_heads * key_bytes(a) + a.v_heads * value_bytes(a); }
 int chunks_of(const DeltaArgs &a) { return (a.s.max_q + kChunk - 1) / kChunk; }
 
 // How a call is cut: sequences and chunks of each that the workspace holds at a time.
@@ -991,8 +1054,8 @@ hipError_t launch_row(const DeltaArgs &a, hipStream_t stream) {
     const Cut c = cut_of(a);
     Segment seg;
     seg.keys = static_cast<uint8_t *>(a.workspace);
-    seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<DK>::kKey;
-    seg.carry = reinterpret_cast<float *>(seg.values + (size_t)c.chunks * c.batch * a.v_heads * Chunk<DK>::kValue);
+    seg.values = seg.keys + (size_t)c.chunks * c.batch * a.k_heads * Chunk<BF, DK>::kKey;
+    seg.carry = reinterpret_cast<float *>(seg.values + (size_t)c.chunks * c.batch * a.v_heads * Chunk<BF, DK>::kValue);
     for (int b0 = 0; b0 < a.s.batch; b0 += c.batch) {
         for (int c0 = 0; c0 < chunks_of(a); c0 += c.chunks) {
             seg.first_seq = b0;
