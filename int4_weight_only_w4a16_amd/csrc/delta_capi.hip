@@ -1,6 +1,7 @@
 // C ABI of the short convolution and the gated delta rule: argument validation and launches.
 // See include/w4a16.h for the contract.  Every check runs before any HIP call.
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/w4a16.h"
@@ -185,5 +186,10 @@ extern "C" size_t w4a16_delta_rule_workspace_bytes(int64_t batch, int64_t T, int
     d.v_heads = (int)v_heads;
     d.key_dim = (int)key_dim;
     d.value_dim = (int)value_dim;
-    return in_chunks(d) ? w4a16::delta_chunk_workspace_bytes(d) : 0;
+    size_t most = 0;                   // over both types: what a call is cut into depends on its own
+    for (const bool bf16 : {false, true}) {
+        d.bf16 = bf16;
+        if (in_chunks(d)) most = std::max(most, w4a16::delta_chunk_workspace_bytes(d));
+    }
+    return most;
 }

@@ -73,6 +73,32 @@ def test_valid_calls_reach_the_device_check(lib):  # noqa: F811
         assert delta(lib, **kw) == w4.W4A16_ERR_DEVICE
 
 
+@pytest.mark.parametrize("hk,hv,dk,batch,max_q", [(2, 4, 128, 3, 17), (16, 48, 128, 1, 8191), (16, 64, 128, 2, 4480),
+                                                  (16, 64, 128, 2, 20000), (1, 1, 64, 1, 100), (4, 32, 64, 40, 640)])
+def test_workspace_of_both_types(lib, hk, hv, dk, batch, max_q):  # noqa: F811
+    """What the size function says is enough for a call of either type, and for one of them no more than that."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    T = batch * max_q
+    need = w4.delta_rule_workspace_bytes(batch, T, hk, hv, dk, 128, max_q)
+    assert need > 0 and w4.delta_rule_workspace_bytes(batch, T, hk, hv, dk, 128, max_q) == need
+    sizes = dict(T=T, hk=hk, hv=hv, dk=dk, dv=128, qs=hk * dk, ks=hk * dk, vs=hv * 128, os=hv * 128, as_=hv, bs=hv,
+                 batch=batch, max_q=max_q)
+    short = []
+    for flags in (0, w4.W4A16_X_BF16):
+        sizes["flags"] = flags
+        assert delta(lib, **sizes, wsb=need) == w4.W4A16_ERR_DEVICE
+        assert delta(lib, **sizes, ws=None, wsb=0) == w4.W4A16_ERR_NULL
+        assert delta(lib, **sizes, ws=0xd0008, wsb=need) == w4.W4A16_ERR_ALIGN
+        assert delta(lib, **sizes, wsb=1024) == w4.W4A16_ERR_WORKSPACE
+        short.append(delta(lib, **sizes, wsb=need - 1))
+    assert w4.W4A16_ERR_WORKSPACE in short
+    for n in (1, 16):                      # token by token: none
+        assert w4.delta_rule_workspace_bytes(batch, batch * n, hk, hv, dk, 128, n) == 0
+    assert w4.delta_rule_workspace_bytes(batch, 64 * batch, hk, hv, dk, 128, 64, tree=True) == 0
+
+
 def test_a_chunk_s_triangular_form_is_the_recurrence():
     """The form that long calls are computed in, against the definition: U = T (V - e^G K S)."""
     import torch

@@ -424,6 +424,86 @@ def test_delta_on_another_stream_and_replayed_from_a_graph(dev, ns):
         w4.gated_delta_rule(**{**every[0][0], "state": every[0][0]["state"].clone()})
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n", [9, 15, 16, 17, 18])
+def test_delta_around_the_longest_call_token_by_token(dev, n, dtype):
+    d = Delta([n, 1, n - 1, 0, n], 2, 4, 128, 128, dtype, seed=n, fresh=(2,), index=[3, 0, 1, 2, -1])
+    d.check(*d.call(dev), tight=False)
+    chain = Delta([n], 1, 2, 64, 64, dtype, seed=n, trees=[tr.chain(n)])
+    chain.check(*chain.call(dev), tight=False)
+
+
+@pytest.mark.parametrize("ns,index", [([9500, 130, 9500], [1, 0, -1]), ([640] * 20 + [3] + [640] * 19, None)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_delta_cut_into_several_launches(dev, dtype, ns, index):
+    """More chunks than the workspace holds, against a few heads at a time, which it holds.  Cut between sequences:
+    the same bits.  Within one: up to the cut.  There the state goes through memory, exactly but for the power of
+    two that its 16-bit parts are made with, so what follows differs by those parts' 2^-22: states by less than the
+    2^-18 that each may be off, and an output, if that takes it over a border, by one step of its type, twice its u."""
+    T, hk, hv, d = sum(ns), 16, 64, 128
+    g = torch.Generator(device=dev).manual_seed(1)
+    r = lambda *shape: torch.randn(*shape, generator=g, device=dev)
+    q, k, v = r(T, hk, d).to(dtype), r(T, hk, d).to(dtype), r(T, hv, d).to(dtype)
+    a, b = r(T, hv).to(dtype), r(T, hv).to(dtype)
+    a_log, dt_bias = torch.rand(hv, generator=g, device=dev), -4 * torch.rand(hv, generator=g, device=dev)
+    start = r(len(ns) + 1, hv, d, d)
+    call = lambda hks, hvs, state: w4.gated_delta_rule(
+        q[:, hks], k[:, hks], v[:, hvs], a[:, hvs], b[:, hvs], state, ints(index or list(range(len(ns))), dev),
+        starts(ns, dev), max(ns), a_log=a_log[hvs].contiguous(), dt_bias=dt_bias[hvs].contiguous(), unit_qk=True)
+    state = start.clone()
+    out = call(slice(0, hk), slice(0, hv), state)
+    assert torch.isfinite(out).all()
+    for i in (0, 7, 15):
+        hvs = slice(4 * i, 4 * i + 4)
+        few = start[:, hvs].contiguous()
+        want = call(slice(i, i + 1), hvs, few)
+        at = 0
+        for b_, n in enumerate(ns):
+            part = slice(at, at + min(n, 64 * 128))        # (at least 132 chunks fit)
+            at += n
+            assert torch.equal(out[part, hvs], want[part])
+        if index is None:
+            assert torch.equal(out[:, hvs], want) and torch.equal(state[:, hvs], few)
+        u = ref.U[dtype]
+        off, size = (out[:, hvs].double() - want.double()).norm(dim=2), want.double().norm(dim=2)
+        assert (off <= (2 * u + 2.0 ** -18) * size + 2.0 ** -24).all()
+        off, size = (state[:, hvs].double() - few.double()).norm(dim=(2, 3)), few.double().norm(dim=(2, 3))
+        assert (off <= 2.0 ** -18 * size).all()
+
+
+def test_delta_nan_stays_on_its_branch(dev):
+    rng = random.Random(5)
+    trees = [tr.random_tree(n, rng, 2) for n in (20, 64, 9)]
+    d = Delta([len(t) for t in trees], 2, 4, 64, 64, BF16, trees=trees)
+    want, _ = d.call(dev)
+    d.v[3, 1, 5] = float("nan")              # a column of a head, in the first tree
+    d.k[20 + 4, 1, 0] = float("inf")         # a key head, in the second
+    d.q[84 + 2, 0, 0] = float("nan")         # a query head, in the third: its own row alone
+    out, state = d.call(dev)
+    hit = torch.zeros_like(want, dtype=torch.bool)
+    for j in range(20):
+        hit[j, 1, 5] = 3 in tr.path(trees[0], j)
+    for j in range(64):
+        hit[20 + j, 2:] = 4 in tr.path(trees[1], j)
+    hit[84 + 2, :2] = True
+    assert torch.equal(out[~hit], want[~hit]) and torch.isnan(out[hit]).all()
+    assert torch.equal(state.cpu(), d.state)
+
+
+def test_two_sequences_of_one_call_on_two_streams(dev):
+    """Calls under way at the same time, each with a workspace of its own."""
+    made = [Delta([300, 41], 2, 4, 128, 64, BF16, seed=s) for s in range(2)]
+    want = [d.call(dev) for d in made]
+    args = [d.args(dev) for d in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = [w4.gated_delta_rule(**a, stream=s.cuda_stream, workspace=torch.empty(1 << 24, dtype=torch.uint8, device=dev))
+           for a, s in zip(args, streams)]
+    torch.cuda.synchronize()
+    for (out, state), o, a in zip(want, got, args):
+        assert torch.equal(o, out) and torch.equal(a["state"], state)
+
+
 def test_binding_refusals(dev):
     d = Delta([3], 1, 2, 64, 64, F16)
     good = d.args(dev)
