@@ -36,6 +36,24 @@ struct Work {
     int t0, t1;                   // tiles of slots that any row of the tile sees
 };
 
+// Which part of the work a workgroup takes: a chunk of slots, a head's tile of rows (the tile-th, head
+// group % kv_heads) of `groups`, a sequence.  The launches for trees have the chunks outermost: sequences
+// differ in length, and chunks that only some have would, innermost, keep some XCDs (block index modulo 8)
+// busier than others (12 trees over 900 to 12000 slots, four chunks:
+// 157 us for the call; 113 with them outermost).
+struct Place {
+    int chunk, group, groups, batch;
+};
+template <bool TREE>
+__device__ __forceinline__ Place place_of(const Plan &plan, int kv_heads) {
+    const int groups = kv_heads * plan.row_tiles;
+    if (TREE) return {(int)(blockIdx.x / groups), (int)(blockIdx.x % groups), groups, (int)blockIdx.y};
+    return {(int)blockIdx.x, (int)blockIdx.y, groups, (int)blockIdx.z};
+}
+inline dim3 tree_grid(const Kv4AttnArgs &a, const Plan &p) {
+    return dim3((unsigned)(a.c.kv_heads * p.row_tiles * p.chunks), (unsigned)a.c.batch);
+}
+
 __device__ __forceinline__ bool work_of(const Kv4AttnArgs &a, int b, int h, int row0, int rows_per, Work *w) {
     const int64_t first = a.cu[b], end = a.cu[b + 1], kv_len = max(a.kv_len[b], 0);
     const int64_t n64 = min(end, a.T) - first;

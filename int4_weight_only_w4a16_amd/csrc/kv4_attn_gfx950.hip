@@ -183,16 +183,17 @@ __global__ void __launch_bounds__(kThreads)
     // that no copy waits for a page id.  Without a window a chunk's place does not depend on the
     // sequence's lengths, and the ids are loaded beside them.
     const int tpp = a.c.tiles_per_page, kvh = a.c.kv_heads;
+    const Place me = place_of<TREE>(plan, kvh);
     auto load_ids = [&](int tile) {
         const int at = tile / tpp + lane;
-        return at < a.c.table_stride ? a.c.table[(int64_t)blockIdx.z * a.c.table_stride + at] : -1;
+        return at < a.c.table_stride ? a.c.table[(int64_t)me.batch * a.c.table_stride + at] : -1;
     };
-    int ids = load_ids((int)blockIdx.x * plan.chunk);
+    int ids = load_ids(me.chunk * plan.chunk);
     Work w;
-    if (!work_of(a, blockIdx.z, blockIdx.y % kvh, (blockIdx.y / kvh) * kRows, kRows, &w)) return;
-    const int chunk0 = w.t0 + (int)blockIdx.x * plan.chunk;
+    if (!work_of(a, me.batch, me.group % kvh, (me.group / kvh) * kRows, kRows, &w)) return;
+    const int chunk0 = w.t0 + me.chunk * plan.chunk;
     const int chunk1 = min(chunk0 + plan.chunk, w.t1);
-    if (blockIdx.x > 0 && chunk0 >= w.t1) return;
+    if (me.chunk > 0 && chunk0 >= w.t1) return;
     const int G = a.q_heads / kvh;
 
     const int page0 = chunk0 / tpp;
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     const bool whole = w.t1 - w.t0 <= plan.chunk;       // this workgroup saw everything
     float *part = static_cast<float *>(a.workspace) +
-                  (((int64_t)w.b * gridDim.y + blockIdx.y) * plan.chunks + blockIdx.x) * kRows * (D + 2);
+                  (((int64_t)w.b * me.groups + me.group) * plan.chunks + me.chunk) * kRows * (D + 2);
     for (int idx = threadIdx.x; idx < kRows * (D / 4); idx += kThreads) {
         const int col = idx / (D / 4), d = 4 * (idx % (D / 4));
         const int row = w.row0 + col;
@@ -724,6 +725,11 @@ int64_t kv4_attention_row_tiles(const Kv4AttnArgs &a) {
     return ((int64_t)rows_of(a) + tile_rows(a) - 1) / tile_rows(a);
 }
 
+int64_t kv4_tree_blocks(const Kv4AttnArgs &a) {
+    const Plan p = plan_of(a);
+    return (int64_t)a.c.kv_heads * p.row_tiles * p.chunks;
+}
+
 size_t kv4_attention_workspace_bytes(const Kv4AttnArgs &a) {
     const Plan p = plan_of(a);
     if (p.chunks <= 1) return 0;
@@ -739,12 +745,12 @@ hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream) {
             if (e != hipSuccess) return e;
         } else if (p.rows == 16) {
             if (a.tree)
-                attend_kernel<bf(), d(), ng(), 1, true><<<grid, kThreads, 0, stream>>>(a, p);
+                attend_kernel<bf(), d(), ng(), 1, true><<<tree_grid(a, p), kThreads, 0, stream>>>(a, p);
             else
                 attend_kernel<bf(), d(), ng(), 1, false><<<grid, kThreads, 0, stream>>>(a, p);
         } else if constexpr (d() <= 128) {
             if (a.tree)
-                attend_kernel<bf(), d(), ng(), 2, true><<<grid, kThreads, 0, stream>>>(a, p);
+                attend_kernel<bf(), d(), ng(), 2, true><<<tree_grid(a, p), kThreads, 0, stream>>>(a, p);
             else
                 attend_kernel<bf(), d(), ng(), 2, false><<<grid, kThreads, 0, stream>>>(a, p);
         }

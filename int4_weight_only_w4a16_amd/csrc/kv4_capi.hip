@@ -301,6 +301,7 @@ static int attend(const CacheShape &s, const void *q, int64_t q_stride, const vo
     if (!attention_fits(a)) return W4A16_ERR_SHAPE;
     if (!aligned(lse, 4) || !aligned(tree, 8)) return W4A16_ERR_ALIGN;
     if (T == 0 || batch == 0 || max_q == 0) return W4A16_OK;
+    if (is_tree && !grid_ok(w4a16::kv4_tree_blocks(a), 512)) return W4A16_ERR_SHAPE;
     if (is_tree && !tree) return W4A16_ERR_NULL;
     st = check_cache_pointers(pages, table, cu_seqlens, kv_len);
     if (st != W4A16_OK) return st;

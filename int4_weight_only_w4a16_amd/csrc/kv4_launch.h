@@ -102,6 +102,7 @@ struct Kv4AttnArgs {
 // Tiles of rows that a head of one sequence is divided into (the attention's launch has them and
 // the heads in one dimension).
 int64_t kv4_attention_row_tiles(const Kv4AttnArgs &a);
+int64_t kv4_tree_blocks(const Kv4AttnArgs &a);       // in the first dimension of a tree's launch
 size_t kv4_attention_workspace_bytes(const Kv4AttnArgs &a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, hipStream_t stream);
 hipError_t launch_kv4_mass(const Kv4AttnArgs &a, hipStream_t stream);

@@ -100,13 +100,14 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int kvh = a.c.kv_heads, G = a.q_heads / kvh;
+    const Place me = place_of<TREE>(plan, kvh);
     Work w;
     // later rows see more slots: the longest tiles of rows first
-    const int row_tile = plan.row_tiles - 1 - (int)(blockIdx.y / kvh);
-    if (!work_of(a, blockIdx.z, blockIdx.y % kvh, row_tile * Shape::kRows, Shape::kRows, &w)) return;
-    const int chunk0 = w.t0 + (int)blockIdx.x * plan.chunk;
+    const int row_tile = plan.row_tiles - 1 - me.group / kvh;
+    if (!work_of(a, me.batch, me.group % kvh, row_tile * Shape::kRows, Shape::kRows, &w)) return;
+    const int chunk0 = w.t0 + me.chunk * plan.chunk;
     const int chunk1 = min(chunk0 + plan.chunk, w.t1);
-    if (blockIdx.x > 0 && chunk0 >= w.t1) return;
+    if (me.chunk > 0 && chunk0 >= w.t1) return;
 
     // ---- this lane's column: a row of q, its channels as matrix operands, what it sees ----
     const int row = w.row0 + 32 * wave + col;
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     // ---- the rows' results: register 4 i + e of block o holds channel 32 o + 8 i + 4 half + e ----
     const bool whole = w.t1 - w.t0 <= plan.chunk;
     float *part = static_cast<float *>(a.workspace) +
-                  (((int64_t)w.b * gridDim.y + row_tile * kvh + w.h) * plan.chunks + blockIdx.x) * Shape::kRows * (D + 2);
+                  (((int64_t)w.b * me.groups + row_tile * kvh + w.h) * plan.chunks + me.chunk) * Shape::kRows * (D + 2);
     sum += __shfl_xor(sum, 32);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -577,7 +578,7 @@ hipError_t launch_kv4_prefill(const Kv4AttnArgs &a, const Plan &p, hipStream_t s
     const dim3 grid((unsigned)p.chunks, (unsigned)(a.c.kv_heads * p.row_tiles), (unsigned)a.c.batch);
     return by_shape(a.c, [&](auto bf, auto d, auto ng) {
         if (a.tree)
-            prefill_kernel<bf(), d(), ng(), true><<<grid, kManyThreads<d()>, 0, stream>>>(a, p);
+            prefill_kernel<bf(), d(), ng(), true><<<tree_grid(a, p), kManyThreads<d()>, 0, stream>>>(a, p);
         else
             prefill_kernel<bf(), d(), ng(), false><<<grid, kManyThreads<d()>, 0, stream>>>(a, p);
         return hipGetLastError();

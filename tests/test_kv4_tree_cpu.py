@@ -30,6 +30,9 @@ def tree(lib, **kw):  # noqa: F811
     (dict(D=96), w4.W4A16_ERR_SHAPE),
     (dict(group=16), w4.W4A16_ERR_GROUP),
     (dict(scale=0.0), w4.W4A16_ERR_SHAPE),
+    # more workgroups than a launch has
+    (dict(hq=60000, hk=60000, D=64, group=64, page=32, qs=60000 * 64, os=60000 * 64, max_q=1, max_kv=1 << 20),
+     w4.W4A16_ERR_SHAPE),
     (dict(max_kv=100000, wsb=0), w4.W4A16_ERR_WORKSPACE),
     (dict(max_kv=100000, ws=None), w4.W4A16_ERR_NULL),
     (dict(T=0, tree=None), w4.W4A16_OK),
