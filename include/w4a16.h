@@ -630,7 +630,7 @@ int w4a16_short_conv(const void *x, int64_t x_stride, const float *weight, const
  *     S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
  *   q, k : [T, k_heads, key_dim], key_dim 64 or 128
  *   v, out : [T, v_heads, value_dim], value_dim 64, 128, 192 or 256, strides
- *     below 2^23
+ *     below 2^23; out must not overlap an input
  *   a_log, dt_bias : fp32 [v_heads]: g = -exp(a_log) softplus(a + dt_bias) and
  *     beta = sigmoid(b), a and b [T, v_heads] of the activation type; or both
  *     null: a is g and b is beta, fp32.  g is not positive.  (a_stride, b_stride

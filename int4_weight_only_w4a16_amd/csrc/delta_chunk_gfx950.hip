@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
     const int t0 = kChunk * (seg.first_chunk + ci);
     if (t0 >= s.n) return;
     const int n = min(kChunk, s.n - t0);
+    const int row_tiles = TREE ? (n + 15) / 16 : 4;        // of a tree those with tokens alone
     const int64_t slot = (int64_t)blockIdx.z * seg.chunks + ci;
     uint8_t *const to_key = seg.keys + (slot * a.k_heads + hk) * C::kKey;
 
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
 #pragma unroll
             for (int d = 1; d < 4; ++d) {
                 const int i = wave + d;
-                if (i >= 4) break;
+                if (i >= row_tiles) break;
                 f4 left[4], acc = {0.f, 0.f, 0.f, 0.f}, out = acc;
 #pragma unroll
                 for (int k = 0; k < d; ++k) left[k] = *reinterpret_cast<const f4 *>(&A[16 * i + m][16 * (wave + k) + 4 * b]);
@@ -544,8 +545,10 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             }
             f4 ks[2][4], qs[2][4];
 #pragma unroll
+            for (int t = 0; t < 4; ++t) ks[0][t] = ks[1][t] = qs[0][t] = qs[1][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
             for (int t = 0; t < 4; ++t) {
-                ks[0][t] = ks[1][t] = qs[0][t] = qs[1][t] = f4{0.f, 0.f, 0.f, 0.f};
+                if (t >= row_tiles) break;
 #pragma unroll
                 for (int d = 0; d < kSteps; ++d) {
                     const _Float16 *const kr = &K[16 * t + m][32 * d + 4 * b], *const qr = &Q[16 * t + m][32 * d + 4 * b];
@@ -600,8 +603,10 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 const Split r0 = split(R[0], R[1], times2(1.0f, up)), r1 = split(R[2], R[3], times2(1.0f, up));
                 f4 U[4], o[4];
 #pragma unroll
+                for (int t = 0; t < 4; ++t) U[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    U[t] = o[t] = f4{0.f, 0.f, 0.f, 0.f};
+                    if (t >= row_tiles) break;
 #pragma unroll
                     for (int d = 0; d <= t / 2; ++d) {
                         const h8 hi = *reinterpret_cast<const h8 *>(tiles + C::kHigh + 1024 * tile_of(t, d) + 16 * lane);
@@ -616,6 +621,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 const float of_u = times2(1.0f, 20 - up);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
+                    if (t >= row_tiles) break;
 #pragma unroll
                     for (int d = 0; d <= t / 2; ++d) {
                         const _Float16 *const pr = P + (16 * t + m) * kP + 32 * d + 4 * b;
