@@ -433,6 +433,21 @@ def test_delta_around_the_longest_call_token_by_token(dev, n, dtype):
     chain.check(*chain.call(dev), tight=False)
 
 
+@pytest.mark.parametrize("heads", [(2, 4, 128, 128), (1, 3, 64, 64)])
+@pytest.mark.parametrize("n", [333, 64])
+def test_delta_fp16_outputs_are_little_further_off_than_their_rounding(dev, n, heads):
+    """As a whole, against the exact outputs rounded: one more rounding to eleven bits, of the state, enters the
+    outputs, and its share is at most as large as theirs: together less than 1.5 times (the root of two)."""
+    for trees in (None, [tr.random_tree(n, random.Random(n), 2)] if n <= 64 else None):
+        d = Delta([n], *heads, F16, seed=n, trees=trees)
+        out, _ = d.call(dev)
+        g, beta = ref.gates(d.a, d.b, d.a_log, d.dt_bias)
+        o, _, _ = ref.delta(d.q, d.k, d.v, g, beta, d.state[d.index[0]], heads[2] ** -0.5, True, d.eps,
+                            trees[0] if trees else None)
+        rounding = (o.to(F16).double() - o).norm()
+        assert (out.cpu().double() - o).norm() <= 1.5 * rounding
+
+
 @pytest.mark.parametrize("ns,index", [([9500, 130, 9500], [1, 0, -1]), ([640] * 20 + [3] + [640] * 19, None)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_delta_cut_into_several_launches(dev, dtype, ns, index):
