@@ -113,11 +113,11 @@ __global__ void __launch_bounds__(kManyThreads<D>)
     const int row = w.row0 + 32 * wave + col;
     const bool in_seq = row < w.rows;
     const int token = in_seq ? row / G : 0, head = w.h * G + (in_seq ? row - token * G : 0);
-    uint64_t kin = 0;
+    uint64_t of_tree = 0;
     int depth = token;
     if constexpr (TREE) {
-        kin = in_seq ? kin_of(a.tree[w.first + token], token) : 0;
-        depth = __popcll(kin) - 1;
+        of_tree = in_seq ? kin_of(a.tree[w.first + token], token) : 0;
+        depth = __popcll(of_tree) - 1;
     }
     const int lo = in_seq ? row_lo(depth, w.start, a.window) : 0;
     const int hi = in_seq ? row_hi(token, w.start, w.len, a.causal) : 0;
@@ -437,12 +437,27 @@ __global__ void __launch_bounds__(kManyThreads<D>)
         if (found != (1u << kTiles) - 1 || 32 * tile < all_lo || 32 * (tile + kTiles) > all_hi) {
             // (opaque bounds: the differences with them are not kept in registers from stage to stage)
             int from = lo - 32 * tile - 4 * half, to_slot = hi - 32 * tile - 4 * half;
-            asm volatile("" : "+v"(from), "+v"(to_slot));
+            if constexpr (!TREE) asm volatile("" : "+v"(from), "+v"(to_slot));
+            uint64_t kin = of_tree;
+            int first_seen = lo, past_seen = hi;
+            if constexpr (TREE && D == 256) {
+                // what a row sees is made again for these few stages (opaque: it is not kept in registers, which are
+                // short here: 176 bytes of a lane's in scratch, 152 so; with 128 channels, where they are not, it
+                // costs 143 -> 163 us for 64 drafts over 65000 slots)
+                int again = lane;
+                asm volatile("" : "+v"(again));
+                again = w.row0 + 32 * wave + (again & 31);
+                const int mine = again < w.rows ? again / G : 0;
+                kin = again < w.rows ? kin_of(a.tree[w.first + mine], mine) : 0;
+                first_seen = again < w.rows ? row_lo(__popcll(kin) - 1, w.start, a.window) : 0;
+                past_seen = again < w.rows ? row_hi(mine, w.start, w.len, a.causal) : 0;
+            }
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
                 if constexpr (TREE) {            // (selects: there are no branches for a lane's slots here)
                     const uint32_t there = found >> t & 1 ? ~0u : 0u;
-                    const uint32_t bits = (seen_bits(kin, lo, hi, w.start, 32 * (tile + t)) & there) >> (4 * half);
+                    const uint32_t bits =
+                        (seen_bits(kin, first_seen, past_seen, w.start, 32 * (tile + t)) & there) >> (4 * half);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         x[t][i] = bits >> (16 * ((i >> 2) & 1) + 8 * (i >> 3) + (i & 3)) & 1 ? x[t][i] : -__builtin_inff();
