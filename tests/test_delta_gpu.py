@@ -173,6 +173,39 @@ def test_conv_extremes(dev):
     assert (got[:, 7].abs() < 1e-30).all()
 
 
+@pytest.mark.parametrize("tree", [False, True])
+def test_conv_on_another_stream_and_replayed_from_a_graph(dev, tree):
+    """Rows, lengths, indices, states and words are read on the device: a captured call follows them."""
+    rng = random.Random(9)
+    made = [Conv([9, 30, 2], 72, 4, BF16, seed=s, fresh=f, trees=[tr.random_tree(n, rng, 2) for n in (9, 30, 2)])
+            for s, f in ((1, ()), (2, (1,)), (3, (0, 2)))]
+    def args(c):
+        return dict(x=c.x.to(dev), weight=c.weight.to(dev), state=c.state.to(dev), state_index=ints(c.index, dev),
+                    cu_seqlens=starts(c.ns, dev), max_q=30, bias=c.bias.to(dev), seen=ints(c.seen, dev),
+                    tree=words(c.trees, dev) if tree else None)
+    every = []
+    for c in made:
+        eager = args(c)
+        every.append((args(c), w4.short_conv(**eager), eager["state"]))
+    live = {k: v.clone() if torch.is_tensor(v) else v for k, v in every[0][0].items()}
+    out = torch.zeros_like(every[0][1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        w4.short_conv(**live, out=out)
+    for i in (0, 1, 2, 0, 2, 1):
+        for k, v in every[i][0].items():
+            if torch.is_tensor(v):
+                live[k].copy_(v)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, every[i][1]), i
+        assert torch.equal(live["state"].view(torch.int16), every[i][2].view(torch.int16)), i
+        w4.short_conv(**{**every[0][0], "state": every[0][0]["state"].clone()})
+
+
 # ---- delta rule ----
 
 class Delta:
