@@ -45,6 +45,7 @@ namespace {
 constexpr int kChunk = 64;
 constexpr int kTop = 14;               // operands lie below 2^kTop
 constexpr int kTopK = 0;               // and keys below 2^kTopK
+constexpr int kTopU = 9;               // and rows of U for the next state below 2^kTopU
 constexpr float kDown = 1.0f / (1 << 20);      // U comes out below 2^34: 64 products of 2^14 each
 constexpr float kRestUp = 64.f;        // what fp16 leaves of a number below 2^14 is at most 4; with this, 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -956,11 +957,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
             top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
         }
-        // A power of two for R, and with it for the next S, which has at most 2^14 from this one and 2^15 from
-        // U: 64 products of K^T (below 1) and rows that lie below 2^9.
-        const int next = min(kTop - max(exponent(top_r), -100) + weigh_up,
-                             power + kTop - (top_s > 0.f ? exponent(top_s) : -200));
-        const int up_r = next - weigh_up;
+        const int up_r = kTop - max(exponent(top_r), -100);
         const float by_r = times2(1.0f, up_r);
 
         // ---- U = T R (times 2^(up_r + a power for each row)) ----
@@ -1006,11 +1003,23 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 
         // ---- S <- e^G_last S + (e^(G_last - G) K)^T U ----
         {
+            float top_u = 0.f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) U[t][j] *= weigh[t][j];
-            const Split u0 = split(U[0], U[1], 1.0f), u1 = split(U[2], U[3], 1.0f);
+                for (int j = 0; j < 4; ++j) {
+                    U[t][j] *= weigh[t][j];
+                    top_u = fmaxf(top_u, __builtin_fabsf(U[t][j]));
+                }
+            top_u = top_of_column(top_u);
+            // A power of two for the next S, which has at most 2^14 from this one and 2^15 from the weighed U: 64
+            // products of K^T (below 1) and rows below 2^9.  It goes by the largest of them as they are: R's largest
+            // may be a row that counts for nothing at the chunk's end.
+            const int base = up_r + weigh_up;
+            const int next = min(min(kTop + power - (top_s > 0.f ? exponent(top_s) : -200),
+                                     kTopU + base - (top_u > 0.f ? max(exponent(top_u), -100) : -200)), power + 100);
+            const float by_u = times2(1.0f, next - base);
+            const Split u0 = split(U[0], U[1], by_u), u1 = split(U[2], U[3], by_u);
             const float by = times2(gamma, next - power);
             power = next;
 #pragma unroll
