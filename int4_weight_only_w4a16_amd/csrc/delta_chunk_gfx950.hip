@@ -26,6 +26,12 @@
 // of e4m3 (1.1 times; five prompts 112 -> 119 us); a tree's have two of S and U (1.2 times).
 // Powers of two come off in fp32.
 //
+// Two parts hold 22 bits of what is within 2^-16 of the largest they are made with, and fewer of what is smaller:
+// of a row of R beside a column's largest, which may be a later token's, or one that has faded by the chunk's end.
+// So each chunk is looked at (least and weighed rows of R), and one where a row or the next state would lose by it
+// is gone through token by token, in fp32 from the inputs (0.7 us a token; the look, and U's powers of two by its own
+// largest, cost 2 %: 8191 tokens 300 -> 304 us, five prompts 122.6 -> 126).
+//
 // Bound by the chain of chunks: one sequence of 8191 tokens, 16 + 48 heads of 128 x 128, bfloat16,
 // takes 76 us for the preparation and 232 to 244 for the scan, 1.9 a chunk (memory alone: 58).
 
@@ -47,6 +53,12 @@ constexpr int kTop = 14;               // operands lie below 2^kTop
 constexpr int kTopK = 0;               // and keys below 2^kTopK
 constexpr int kTopU = 9;               // and rows of U for the next state below 2^kTopU
 constexpr float kDown = 1.0f / (1 << 20);      // U comes out below 2^34: 64 products of 2^14 each
+// What 16-bit parts take from a column's small rows for its largest's sake: from U as it comes out (rows of T below 2^14
+// by rows of R below 2^14) about 2^-10, so that what an output adds up is to be kLeastU of those at least, kLost
+// of R; from its weighed rows (2^-25 of U at most), the next state's, 2^-35, and kSmall of R in their heaviest.
+constexpr float kLeastU = 2.0f, kLost = 1.0f / (1 << 26), kSmall = 1.0f / (1 << 17);
+constexpr int kLeastWeighed = -15;
+constexpr int kWalked = -(1 << 30);    // in the place of U's power of two: the outputs are made already
 constexpr float kRestUp = 64.f;        // what fp16 leaves of a number below 2^14 is at most 4; with this, 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -62,8 +74,9 @@ struct Chunk {
     static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRest = 18 * 1024, kRows = BF ? kRest : 21 * 1024;
     static constexpr int kValue = kRows + 2 * 1024;
     // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
-    // output of S and of U; e^G_last and the power of two in the second of them
-    static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kLast = 1024;
+    // output of S and of U; e^G_last, the power of two in the second of them; what the last
+    // sixteen rows count for S, of the heaviest; e^g, T's power of two, and its diagonal
+    static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kLast = 1024, kHeavy = 1040, kKeep = 1280, kTau = 1536, kDiagonal = 1792;
 };
 
 // The part of a call that one launch works on: `chunks` chunks from the first_chunk-th of `batch`
@@ -500,6 +513,14 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
             rows[C::kWeigh / 4 + lane] = times2(weigh, up);
             rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
+            if constexpr (!TREE) {
+                rows[C::kKeep / 4 + lane] = exp_f32((float)(G[lane] - (lane ? G[lane - 1] : 0.0)));
+                reinterpret_cast<int *>(rows)[C::kTau / 4 + lane] = tau[lane];
+                rows[C::kDiagonal / 4 + lane] = times2(beta[lane], tau[lane]);
+                const float counts = times2(__builtin_fabsf(weigh * beta[lane]), tau[lane]);
+                const float most = top_of_column(top_of_row(counts));
+                if (lane >= 48) rows[C::kHeavy / 4 + lane - 48] = most > 0.f ? counts / most : 1.f;
+            }
             if (!TREE && lane == 0) {
                 rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
                 reinterpret_cast<int *>(rows)[C::kLast / 4 + 1] = up;
@@ -653,6 +674,52 @@ __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)const_cast<lds_u8 *>(p)));
 }
 
+// One token of a head for the columns of a wave, in fp32 throughout as the kernel for tokens has it: moves S on
+// (rows 16 t + 4 b + j of column `col`, the (lane % 16)-th of the wave's) and returns the output.
+template <bool BF, int DK>
+__device__ __forceinline__ float one_token(const DeltaArgs &a, int64_t row, int h, int col, int b, float keep, float beta,
+                                           f4 (&S)[DK / 16]) {
+    constexpr int kTiles = DK / 16;
+    const int hk = h / (a.v_heads / a.k_heads);
+    const uint16_t *const qr = static_cast<const uint16_t *>(a.q) + row * a.q_stride + hk * DK + 4 * b;
+    const uint16_t *const kr = static_cast<const uint16_t *>(a.k) + row * a.k_stride + hk * DK + 4 * b;
+    const float v = lo_f32<BF>(static_cast<const uint16_t *>(a.v)[row * a.v_stride + (int64_t)h * a.value_dim + col]);
+    float q[4 * kTiles], k[4 * kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const u2 q4 = *reinterpret_cast<const u2 *>(qr + 16 * t), k4 = *reinterpret_cast<const u2 *>(kr + 16 * t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            q[4 * t + 2 * i] = lo_f32<BF>(q4[i]);
+            q[4 * t + 2 * i + 1] = hi_f32<BF>(q4[i]);
+            k[4 * t + 2 * i] = lo_f32<BF>(k4[i]);
+            k[4 * t + 2 * i + 1] = hi_f32<BF>(k4[i]);
+        }
+    }
+    if (a.unit) {
+        to_unit<16>(k, a.eps);
+        to_unit<16>(q, a.eps);
+    }
+    float qk = 0.f, sk = 0.f, sq = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            qk = __builtin_fmaf(q[4 * t + j], k[4 * t + j], qk);
+            sk = __builtin_fmaf(S[t][j], k[4 * t + j], sk);
+            sq = __builtin_fmaf(S[t][j], q[4 * t + j], sq);
+        }
+    qk = over_lanes<16>(qk);
+    sk = over_lanes<16>(sk);
+    sq = over_lanes<16>(sq);
+    const float u = beta * (v - keep * sk);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[t][j] = __builtin_fmaf(k[4 * t + j], u, keep * S[t][j]);
+    return a.scale * (keep * sq + qk * u);
+}
+
 // A workgroup walks over the chunks with 16 GROUPS columns of one head.  Wave w < GROUPS takes what the
 // next state needs, for sixteen columns; wave GROUPS + w, on the same SIMD, their outputs, from the state and
 // the rows U that the first hands over in LDS, and the copies.  (All in one wave, the only one on its SIMD,
@@ -679,10 +746,10 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
     const int lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
     const int col = 16 * (blockIdx.x * GROUPS + group) + m;
     lds_u8 *const hand = lds + 2 * kStage + group * kHand;
-    lds_u8 *const factors = hand + kFactors + 4 * m, *const lost_at = hand + kFactors + 128 + 8 * m;
 
     if (wave >= GROUPS) {
         // ======== outputs and copies ========
+        const lds_u8 *const factors = hand + kFactors + 4 * m, *const lost_at = hand + kFactors + 128 + 8 * m;
         const int64_t slot = (int64_t)blockIdx.z * seg.chunks;
         // rows of V and of the output by offsets from a chunk's first (the host keeps strides below 2^23 elements)
         constexpr int kUnits = kColumnBytes / 16;          // 16-byte units of a row
@@ -714,6 +781,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         // left, between (2) and (1) the other one.  Through LDS (the state's place, once it is in
         // registers), so that a lane stores eight columns of a row.
         u2 made[4];
+        bool walked = false;                   // they are there already: nothing is stored
         auto store = [&](int ci) {
             asm volatile("" ::: "memory");
 #pragma unroll
@@ -728,7 +796,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             const int n = min(kChunk, s.n - first - kChunk * ci);
             const auto rsrc = make_rsrc(static_cast<const uint16_t *>(a.out) + (s.first + first + (int64_t)kChunk * ci) * a.out_stride +
                                             h * a.value_dim + blockIdx.x * (16 * GROUPS) + 16 * group,
-                                        (uint32_t)((n - 1) * out_row + 32));
+                                        walked ? 0u : (uint32_t)((n - 1) * out_row + 32));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 32 * i + (lane >> 1);
@@ -740,10 +808,19 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         f4 qs[4], fs[4], fu[4], U[4];
         h8 within[6];
         int64_t rest[BF ? 1 : 6];
-        float of_s, of_u;
+        float of_s;
+        int up_r;
         uint64_t lost;
         auto make = [&] {
             f4 o[4], r[4];
+            // (by its own largest, not by the most that it may be, which would leave small rows fewer bits)
+            float top = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = fmaxf(top, __builtin_fabsf(U[t][j]));
+            const int up_u = kTop - max(exponent(top_of_column(top)), -60);
+            const float by = times2(1.0f, up_u), of_u = times2(1.0f, -up_u - up_r);
 #pragma unroll
             for (int t = 0; t < 4; ++t) o[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
             if constexpr (BF) {
@@ -751,14 +828,15 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                 for (int d = 0; d < 2; ++d)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * kDown);
+                    for (int e = 0; e < 8; ++e) u[d][e] = (_Float16)(U[2 * d + (e >> 2)][e & 3] * by);
 #pragma unroll
                 for (int d = 0; d < 2; ++d)
 #pragma unroll
                     for (int t = 2 * d; t < 4; ++t) o[t] = mfma16x16x32(within[tile_of(t, d)], u[d], o[t]);
             } else {
-                const Split u[2] = {split(U[0], U[1], kDown), split(U[2], U[3], kDown)};
-                const int64_t few[2] = {in_fp8(U[0], U[1], kDown / kRestUp), in_fp8(U[2], U[3], kDown / kRestUp)};
+                const Split u[2] = {split(U[0], U[1], by), split(U[2], U[3], by)};
+                const float by8 = by / kRestUp;
+                const int64_t few[2] = {in_fp8(U[0], U[1], by8), in_fp8(U[2], U[3], by8)};
                 // (these with accumulators of their own, and first: a product of one type does not wait for one of
                 // another as long as it must, if it adds to it)
 #pragma unroll
@@ -781,7 +859,9 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     y[t][j] = __builtin_fmaf(fs[t][j] * of_s, qs[t][j], (fu[t][j] * of_u) * (BF ? o[t][j] : o[t][j] + r[t][j]));
+            walked = false;
             if (__builtin_amdgcn_ballot_w64(lost != 0)) {
+                walked = __builtin_amdgcn_readfirstlane(up_r) == kWalked;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -831,7 +911,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = lds_get<f4>(hand + kU + 1024 * t + 16 * lane);
             of_s = lds_get<float>(factors);
-            of_u = lds_get<float>(factors + 64);
+            up_r = lds_get<int>(factors + 64);
             lost = lds_get<uint64_t>(lost_at);
         }
         make();
@@ -864,8 +944,78 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             for (int j = 0; j < 4; ++j) S[t][j] = times2(S[t][j], power);
     }
 
-    lds_barrier();                             // (0) the first chunk is there
-    for (int ci = 0; ci < count; ++ci) {
+    // Whether rows of R are lost beside larger ones of their column: of some output, all that it adds up is
+    // small, its own row and the one before as far as it is kept (of a row alone, that is chance and no
+    // loss); or all that the next state consists of, `of_old` of it the last one.  A row that is zero is
+    // right, unless earlier ones fade: what it takes back of them is not.
+    auto lose = [&](const f4 (&R)[4], float by, const lds_u8 *rows, float gamma, float of_old, int n, int lane, int b) {
+        const float none = gamma < kSmall ? -1.f : 0.f;
+        float top = 0.f, before = 0.f;
+        bool is = false;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f4 keep = lds_get<f4>(rows + C::kKeep + 64 * t), weigh = lds_get<f4>(rows + C::kWeigh + 64 * t);
+            const f4 diagonal = lds_get<f4>(rows + C::kDiagonal + 64 * t);
+            const u4 tau = lds_get<u4>(rows + C::kTau + 64 * t);
+            float u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = __builtin_fabsf(diagonal[j] * (R[t][j] * by));
+            // the row before the first of these four, without its power of two
+            const float end = times2(u[3], -(int)tau[3]), below = __shfl(end, lane - 16);
+            float back = b > 0 ? below : before;
+            before = __shfl(end, lane + 48);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                is |= 16 * t + 4 * b + j < n && diagonal[j] != 0.f && __builtin_fabsf(R[t][j]) > none &&
+                      __builtin_fmaf(keep[j], times2(back, (int)tau[j]), u[j]) < kLeastU;
+                top = fmaxf(top, u[j] * weigh[j]);
+                back = times2(u[j], -(int)tau[j]);
+            }
+        }
+        top = fmaxf(top_of_column(top), of_old);
+        return is || (top > 0.f && exponent(top) < kLeastWeighed);
+    };
+
+    // A chunk whose numbers the products' parts cannot hold beside each other, token by token from the inputs.
+    auto walk = [&](int ci) {
+        int n = min(kChunk, s.n - first - kChunk * ci), head = h, my_col = col, my_b = b;
+        asm volatile("" : "+s"(n), "+s"(head), "+v"(my_col), "+v"(my_b));      // (nothing of this is made before the loop)
+        const int64_t row0 = s.first + first + (int64_t)kChunk * ci;
+        Gates gate{0.f, 0.f};                  // of 64 tokens, one in each lane
+        if (lane < n) gate = gates_of<BF>(a, row0 + lane, head, a.a_log ? expf(a.a_log[head]) : 0.f,
+                                          a.a_log ? a.dt_bias[head] : 0.f);
+        const float all_keep = expf(gate.g);
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][j] = times2(S[t][j], -power);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const float keep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all_keep), i));
+            const float beta = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate.beta), i));
+            const float o = one_token<BF, DK>(a, row0 + i, head, my_col, my_b, keep, beta, S);
+            if (my_b == 0)
+                static_cast<uint16_t *>(a.out)[(row0 + i) * a.out_stride + (int64_t)head * a.value_dim + my_col] =
+                    (uint16_t)pack2<BF>(o, 0.f);
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = fmaxf(top, __builtin_fabsf(S[t][j]));
+        power = kTop - max(exponent(top_of_column(top)), -100);
+#pragma unroll
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t][j] = times2(S[t][j], power);
+    };
+
+    // One chunk.  Without WARY, false if anything in it asks for a look: nothing is changed then, and the wary form
+    // begins again (`again`: between the barriers (1) and (2)).
+    auto one_chunk = [&](auto wary, int ci, bool again) __attribute__((always_inline)) {
+        constexpr bool WARY = wary();
+        const int lane = threadIdx.x & 63, m = lane & 15, b = lane >> 4;
+        lds_u8 *const factors = hand + kFactors + 4 * m, *const lost_at = hand + kFactors + 128 + 8 * m;
         const lds_u8 *const at = lds + (ci & 1) * kStage, *const val = at + C::kKey;
         const lds_u8 *const rows = val + C::kRows + 16 * b;
         const lds_u8 *const tile = at + C::kKey + C::kValue + 32 * group;
@@ -890,31 +1040,35 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         for (int t = 0; t < 4; ++t) off[t] = lds_get<f4>(rows + C::kOff + 64 * t);
         const float gamma = lds_get<float>(val + C::kRows + C::kLast);
         const int weigh_up = lds_get<int>(val + C::kRows + C::kLast + 4);
+        const f4 heavy = lds_get<f4>(rows + C::kHeavy);
 
         // ---- K S ----
         f4 ks[4];
         h8 th[6], tl[6];
+        auto load_t = [&] {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                th[i] = lds_get<h8>(val + C::kHigh + 1024 * i + 16 * lane);
+                tl[i] = lds_get<h8>(val + C::kLow + 1024 * i + 16 * lane);
+            }
+        };
 #pragma unroll
         for (int t = 0; t < 4; ++t) ks[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < kSteps; ++d) {
             if (d + 1 < kSteps) {
                 load_k(d + 1);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 6; ++i) {
-                    th[i] = lds_get<h8>(val + C::kHigh + 1024 * i + 16 * lane);
-                    tl[i] = lds_get<h8>(val + C::kLow + 1024 * i + 16 * lane);
-                }
+            } else if constexpr (!WARY) {
+                load_t();
             }
             const Split x = split(S[2 * d], S[2 * d + 1], 1.0f);
-            lds_put(hand + 1024 * d + 16 * lane, x.hi);
+            if (!WARY || !again) lds_put(hand + 1024 * d + 16 * lane, x.hi);
 #pragma unroll
             for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.hi, ks[t]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) ks[t] = mfma16x16x32(k[d & 1][t], x.lo, ks[t]);
         }
-        lds_barrier();                         // (1) the state is handed over
+        if (!WARY || !again) lds_barrier();    // (1) the state is handed over
         float top_s = 0.f;                     // for the next S
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
@@ -925,7 +1079,7 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         // ---- R = V - e^G K S, its rows as operands ----
         const float of_s = times2(1.0f, -power);
         f4 R[4];
-        float top_r = 0.f;
+        float top_r = 0.f, least = __builtin_inff();
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -933,10 +1087,25 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 const float v = j & 1 ? hi_f32<BF>(V[t][j >> 1]) : lo_f32<BF>(V[t][j >> 1]);
                 R[t][j] = __builtin_fmaf(-(off[t][j] * of_s), ks[t][j], v);
                 top_r = __builtin_elementwise_maximum(top_r, __builtin_fabsf(R[t][j]));
+                least = fminf(least, __builtin_fabsf(R[t][j]));
             }
         top_r = top_of_column(top_r);
         uint64_t lost = 0;                     // rows that come after one that is not finite
-        if (__builtin_amdgcn_ballot_w64(!(top_r < __builtin_inff()))) {
+        // Sizes far apart, such as factors of them leave fp32, or what is not finite.  (By the last rows alone whether the
+        // next state's are large enough: that is where most heads have their heaviest.)
+        float of_last = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) of_last = fmaxf(of_last, __builtin_fabsf(R[3][j]) * heavy[j]);
+        const uint64_t enough = __builtin_amdgcn_ballot_w64(of_last >= kSmall * top_r);
+        const uint64_t odd = __builtin_amdgcn_ballot_w64(least < kLost * top_r || !(top_r < 0x1p100f) ||
+                                                         (top_r < 0x1p-100f && top_r > 0.f) || power < kTop - 100);
+        const bool look = odd || ((enough | enough >> 16 | enough >> 32 | enough >> 48) & 0xFFFF) != 0xFFFF;
+        if (WARY && look) {
+            // (opaque: what is made of it is not kept in registers through the other loop)
+            int lane = threadIdx.x & 63;
+            asm volatile("" : "+v"(lane));
+            const int b = lane >> 4;
+            const lds_u8 *const rows = val + C::kRows + 16 * b;
             uint64_t found = 0;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -956,6 +1125,22 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                 }
             top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
             top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
+            const int n = min(kChunk, s.n - first - kChunk * ci);
+            bool alone = lose(R, times2(1.0f, kTop - max(exponent(top_r), -100)), rows, gamma,
+                              times2(top_s, kTop - max(exponent(top_r), -100) + weigh_up - power),
+                              lost ? min(n, (int)__builtin_ctzll(lost)) : n, lane, b);
+            alone |= top_r >= 0x1p100f || top_r < 0x1p-100f || power < kTop - 100;
+            if (__builtin_amdgcn_ballot_w64(alone && top_r > 0.f)) {
+                lds_put(factors + 64, kWalked);
+                lds_put(lost_at, ~(uint64_t)0);
+                lds_barrier();                 // (2) as below
+                walk(ci);
+                return true;
+            }
+        }
+        if constexpr (WARY) {
+            asm volatile("" ::: "memory");     // (not before: registers are short there)
+            load_t();
         }
         const int up_r = kTop - max(exponent(top_r), -100);
         const float by_r = times2(1.0f, up_r);
@@ -994,10 +1179,11 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                         U[t] = mfma16x16x32(part < 2 ? th[tile_of(t, d)] : tl[tile_of(t, d)], part == 1 ? r.lo : r.hi, U[t]);
                     }
         }
+        if (!WARY && look) return false;       // (here, where the products above hide what this waits for)
 #pragma unroll
         for (int t = 0; t < 4; ++t) lds_put(hand + kU + 1024 * t + 16 * lane, U[t]);
         lds_put(factors, of_s);
-        lds_put(factors + 64, times2(1.0f, 20 - up_r));
+        lds_put(factors + 64, up_r);
         lds_put(lost_at, lost);
         lds_barrier();                         // (2) and U, and the next chunk is there
 
@@ -1031,13 +1217,27 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
 #pragma unroll
                 for (int t = 0; t < kRowTiles; ++t)
                     S[t] = mfma16x16x32(kt[t][part & 1], part == 0 ? u0.hi : part == 1 ? u1.hi : part == 2 ? u0.lo : u1.lo, S[t]);
-            if (__builtin_amdgcn_ballot_w64(lost != 0)) {
+            if (WARY && __builtin_amdgcn_ballot_w64(lost != 0)) {
 #pragma unroll
                 for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) S[t][j] = lost ? __builtin_nanf("") : S[t][j];
             }
         }
+        return true;
+    };
+    lds_barrier();                             // (0) the first chunk is there
+    // Whole chunks of ordinary numbers, in a loop of their own, so that its registers stay where they are, and
+    // the others.
+    const int whole = min(count, (s.n - first) / kChunk);
+    for (int ci = 0; ci < count; ++ci) {
+        bool again = false;
+        while (ci < whole) {
+            again = !one_chunk(std::false_type{}, ci, false);
+            if (again) break;
+            ++ci;
+        }
+        if (ci < count) one_chunk(std::true_type{}, ci, again);
     }
     {
         if (s.state < 0 && s.n - first <= kChunk * seg.chunks) return;     // (kept for the next segment only)

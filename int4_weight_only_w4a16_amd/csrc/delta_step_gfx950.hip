@@ -19,40 +19,6 @@ namespace {
 constexpr int kColumns = 16;           // of a wave
 constexpr int kWaves = 4;              // of a workgroup: whole lines of memory (64 sequences: 67 us, with one wave 95)
 
-// Sum over the lanes of one column, those that are equal mod 4, without LDS.
-__device__ __forceinline__ float over_rows(float v) {
-#define W4A16_ADD_ROR(N) \
-    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + N, 0xF, 0xF, true))
-    W4A16_ADD_ROR(8);
-    W4A16_ADD_ROR(4);
-#undef W4A16_ADD_ROR
-    const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
-    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
-}
-
-// x / sqrt(sum x^2 + eps) over the lanes of a column; in 64 bits where squares leave fp32.
-template <int N>
-__device__ __forceinline__ void to_unit(float (&x)[N], float eps) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum = __builtin_fmaf(x[i], x[i], sum);
-    sum = over_rows(sum) + eps;
-    if (sum > 1e-30f && sum < 1e38f) {
-        const float f = __builtin_amdgcn_rsqf(sum);        // (within 2^-23)
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] *= f;
-        return;
-    }
-    double wide = 0;
-    for (int i = 0; i < N; ++i) wide += (double)x[i] * x[i];
-#pragma unroll
-    for (int d = 4; d < 64; d *= 2) wide += __shfl_xor(wide, d);
-    const double f = 1.0 / sqrt(wide + eps);
-    for (int i = 0; i < N; ++i) x[i] = (float)(x[i] * f);
-}
-
 // What a lane needs of one token.
 template <int ROWS>
 struct Token {
@@ -115,8 +81,8 @@ __global__ void __launch_bounds__(64 * kWaves) step_kernel(DeltaArgs a) {
         }
         const f4 v = {lo_f32<BF>(x.v[0]), hi_f32<BF>(x.v[0]), lo_f32<BF>(x.v[1]), hi_f32<BF>(x.v[1])};
         if (a.unit) {
-            to_unit(k, a.eps);
-            to_unit(q, a.eps);
+            to_unit<4>(k, a.eps);
+            to_unit<4>(q, a.eps);
         }
         float qk = 0.f;
         f4 sk = {0.f, 0.f, 0.f, 0.f}, sq = sk;
@@ -126,11 +92,11 @@ __global__ void __launch_bounds__(64 * kWaves) step_kernel(DeltaArgs a) {
             sk += S[i] * k[i];
             sq += S[i] * q[i];
         }
-        qk = over_rows(qk);
+        qk = over_lanes<4>(qk);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            sk[e] = over_rows(sk[e]);
-            sq[e] = over_rows(sq[e]);
+            sk[e] = over_lanes<4>(sk[e]);
+            sq[e] = over_lanes<4>(sq[e]);
         }
         const f4 u = beta * (v - keep * sk);
 #pragma unroll

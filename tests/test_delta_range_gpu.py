@@ -39,7 +39,8 @@ def check(d, out, state, columns=slice(None)):
         g, beta = ref.gates(d.a[rows], d.b[rows], d.a_log, d.dt_bias)
         o, size, last = ref.delta(d.q[rows], d.k[rows], d.v[rows], g, beta, d.state[d.index[b]], dk ** -0.5, d.unit,
                                   d.eps, d.trees[b] if d.trees else None)
-        off = (out[rows] - o).abs()
+        most = torch.finfo(d.dtype).max                # (what lies beyond is infinite there)
+        off = (out[rows].clamp(-most, most) - o.clamp(-most, most)).abs()
         least = 2.0 ** -24 if d.dtype == F16 else 2.0 ** -126
         bound = 1.01 * ref.U[d.dtype] * o.abs() + 2.0 ** -10 * size + least
         bad = ~(off <= bound)
@@ -75,3 +76,72 @@ def test_a_state_keeps_its_precision_when_large_parts_have_gone(dev, n, power, h
             else:
                 d.state *= 2.0 ** power
             run(d, dev)
+
+
+def grow(d, rows, columns, ratio):
+    """Values `ratio` times the rest; fp16's as far as it goes, against smaller others."""
+    if d.dtype == F16:
+        ratio = min(ratio, 2.0 ** 20)
+    d.v[rows, :, columns] = (d.v[rows, :, columns].float() * ratio).to(d.dtype)
+    assert torch.isfinite(d.v).all()
+
+
+FEW, EVERY = slice(5, 6), slice(None)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("power", [16, 21, 24, 26, 30, 40])
+@pytest.mark.parametrize("columns", [FEW, EVERY], ids=["column", "row"])
+def test_no_token_loses_to_a_later_one(dev, columns, power, heads, dtype):  # noqa: F811
+    """Large values late in a chunk, early in it, after its first token, before and after a token alone."""
+    for rows in (slice(60, 61), slice(10, 40), slice(1, 64), slice(64 + 50, 64 + 52)):
+        d = made([64, 150, 17], heads, dtype, -0.02, seed=power)
+        grow(d, rows, columns, 2.0 ** power)
+        run(d, dev)
+    d = made([130], heads, dtype, -0.02, seed=power)
+    grow(d, slice(0, 30), columns, 2.0 ** power)
+    grow(d, slice(31, 64), columns, 2.0 ** power)
+    d.a[30] = d.a[31] = -80.0
+    run(d, dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("power", [13, 17, 20, 24, 30, 40])
+def test_tokens_after_large_ones_that_have_gone(dev, power, heads, dtype):  # noqa: F811
+    for columns in (FEW, EVERY):
+        for last in (40, 62, 63):
+            d = made([64, 90], heads, dtype, -0.02, seed=power)
+            grow(d, slice(3, 30), columns, 2.0 ** power)
+            d.a[last] = -90.0
+            run(d, dev)
+        # a token that writes nothing, as large as it may be
+        d = made([64, 90], heads, dtype, -0.3, seed=power)
+        grow(d, slice(20, 21), columns, 2.0 ** power)
+        d.b[20] = 0.0
+        run(d, dev)
+    d = made([64, 90], heads, dtype, -0.02, seed=power)
+    d.state *= 2.0 ** power
+    d.a[40] = -90.0
+    run(d, dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("g", [-0.01, -0.3, -0.7])
+def test_what_decays_over_values_of_zero(dev, g, dtype):  # noqa: F811
+    """Nothing new is written but what the keys take back of a state that fades: no part of it is lost."""
+    for index in (None, [-1]):
+        d = made([64], (1, 2, 128, 64), dtype, g, seed=3)
+        d.v[3:] = 0
+        if index:
+            d.v[:3] *= 64
+            d.state[:] = 0
+        run(d, dev)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 123, 2.0 ** 99, 2.0 ** -100])
+def test_sizes_at_the_ends_of_the_type(dev, size):  # noqa: F811
+    d = made([100, 20], (1, 2, 64, 64), BF16, -0.1, seed=1)
+    d.v, d.state = (d.v.float() * size).to(BF16), d.state * size
+    run(d, dev)
