@@ -52,7 +52,6 @@ constexpr int kChunk = 64;
 constexpr int kTop = 14;               // operands lie below 2^kTop
 constexpr int kTopK = 0;               // and keys below 2^kTopK
 constexpr int kTopU = 9;               // and rows of U for the next state below 2^kTopU
-constexpr float kDown = 1.0f / (1 << 20);      // U comes out below 2^34: 64 products of 2^14 each
 // What 16-bit parts take from a column's small rows for its largest's sake: from U as it comes out (rows of T below 2^14
 // by rows of R below 2^14) about 2^-10, so that what an output adds up is to be kLeastU of those at least, kLost
 // of R; from its weighed rows (2^-25 of U at most), the next state's, 2^-35, and kSmall of R in their heaviest.
@@ -153,6 +152,52 @@ __device__ __forceinline__ float top_of_column(float v) {
     return __builtin_elementwise_maximum(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
 }
 
+// One token of a head for the columns of a wave, in fp32 throughout as the kernel for tokens has it: moves S on
+// (rows 16 t + 4 b + j of column `col`, the (lane % 16)-th of the wave's) and returns the output.
+template <bool BF, int DK>
+__device__ __forceinline__ float one_token(const DeltaArgs &a, int64_t row, int h, int col, int b, float keep, float beta,
+                                           f4 (&S)[DK / 16]) {
+    constexpr int kTiles = DK / 16;
+    const int hk = h / (a.v_heads / a.k_heads);
+    const uint16_t *const qr = static_cast<const uint16_t *>(a.q) + row * a.q_stride + hk * DK + 4 * b;
+    const uint16_t *const kr = static_cast<const uint16_t *>(a.k) + row * a.k_stride + hk * DK + 4 * b;
+    const float v = lo_f32<BF>(static_cast<const uint16_t *>(a.v)[row * a.v_stride + (int64_t)h * a.value_dim + col]);
+    float q[4 * kTiles], k[4 * kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const u2 q4 = *reinterpret_cast<const u2 *>(qr + 16 * t), k4 = *reinterpret_cast<const u2 *>(kr + 16 * t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            q[4 * t + 2 * i] = lo_f32<BF>(q4[i]);
+            q[4 * t + 2 * i + 1] = hi_f32<BF>(q4[i]);
+            k[4 * t + 2 * i] = lo_f32<BF>(k4[i]);
+            k[4 * t + 2 * i + 1] = hi_f32<BF>(k4[i]);
+        }
+    }
+    if (a.unit) {
+        to_unit<16>(k, a.eps);
+        to_unit<16>(q, a.eps);
+    }
+    float qk = 0.f, sk = 0.f, sq = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            qk = __builtin_fmaf(q[4 * t + j], k[4 * t + j], qk);
+            sk = __builtin_fmaf(S[t][j], k[4 * t + j], sk);
+            sq = __builtin_fmaf(S[t][j], q[4 * t + j], sq);
+        }
+    qk = over_lanes<16>(qk);
+    sk = over_lanes<16>(sk);
+    sq = over_lanes<16>(sq);
+    const float u = beta * (v - keep * sk);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[t][j] = __builtin_fmaf(k[4 * t + j], u, keep * S[t][j]);
+    return a.scale * (keep * sq + qk * u);
+}
+
 constexpr int kMostHeads = 4;          // value heads of a workgroup
 
 // One chunk of `heads` value heads that share a key head: what the heads have in common, the products of
@@ -175,6 +220,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
     __shared__ __align__(16) float kf[kChunk], qf[kChunk];
     __shared__ int tau[kChunk];
     __shared__ uint64_t kin[kChunk];
+    __shared__ uint64_t redo_rows[TREE ? 16 : 1];      // of a group of columns, rows that go token by token
     __shared__ uint32_t bad_row[kChunk], bad_gate[kMostHeads][kChunk];     // 1: the key, 2: the query; a gate
 
     const int ci = blockIdx.x, h0 = blockIdx.y * heads, r = a.v_heads / a.k_heads, hk = h0 / r;
@@ -511,12 +557,15 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[lane])) * kf[lane], -tau[lane]);
             const int up = -25 - max(exponent(top_of_column(top_of_row(weigh))), -120);
             rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
-            rows[C::kWeigh / 4 + lane] = times2(weigh, up);
+            // (of a tree, T's diagonal, below zero where the path fades and infinite where nothing is written)
+            const float diagonal = times2(__builtin_fabsf(beta[lane]), tau[lane]);
+            if (TREE) rows[C::kWeigh / 4 + lane] = diagonal == 0.f || lane >= n ? __builtin_inff() : grow < kSmall ? -diagonal : diagonal;
+            else rows[C::kWeigh / 4 + lane] = times2(weigh, up);
             rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
             if constexpr (!TREE) {
                 rows[C::kKeep / 4 + lane] = exp_f32((float)(G[lane] - (lane ? G[lane - 1] : 0.0)));
                 reinterpret_cast<int *>(rows)[C::kTau / 4 + lane] = tau[lane];
-                rows[C::kDiagonal / 4 + lane] = times2(beta[lane], tau[lane]);
+                rows[C::kDiagonal / 4 + lane] = diagonal;
                 const float counts = times2(__builtin_fabsf(weigh * beta[lane]), tau[lane]);
                 const float most = top_of_column(top_of_row(counts));
                 if (lane >= 48) rows[C::kHeavy / 4 + lane - 48] = most > 0.f ? counts / most : 1.f;
@@ -589,14 +638,16 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             for (int u = 0; u < 2; ++u) {
                 if (g0 + 4 * u >= a.value_dim / 16) break;
                 f4 R[4];
-                float top = 0.f;
+                float top = 0.f, least = __builtin_inff();
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const f4 off = *reinterpret_cast<const f4 *>(&tree_rows[C::kOff / 4 + 16 * t + 4 * b]);
+                    const f4 diagonal = *reinterpret_cast<const f4 *>(&tree_rows[C::kWeigh / 4 + 16 * t + 4 * b]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         R[t][j] = __builtin_fmaf(-(off[j] * of_s[u]), ks[u][t][j], lo_f32<BF>(V[u][t][j]));
                         top = __builtin_elementwise_maximum(top, __builtin_fabsf(R[t][j]));
+                        least = fminf(least, __builtin_fabsf(R[t][j] * diagonal[j]));      // (0 x infinity does not count)
                     }
                 }
                 top = top_of_column(top);
@@ -622,6 +673,29 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                     top = top_of_column(top);
                 }
                 const int up = kTop - max(exponent(top), -100);
+                // Rows of R that are lost beside larger ones of their column, another branch's perhaps: as in the
+                // scan, but without the row before: what a row alone has by chance goes token by token too (one of some
+                // 2^24 elements, bfloat16; fp16 outputs, rounded to eight times less, leave less to lose).
+                const float small = times2(BF ? kLeastU / 4 : kLeastU, -up);
+                uint64_t redo = 0;
+                const bool beyond = top >= 0x1p100f || (top < 0x1p-100f && top > 0.f) || of_s[u] > 0x1p86f;
+                if (__builtin_amdgcn_ballot_w64(beyond || (least < small && top > 0.f))) {
+                    uint64_t mine = beyond && top > 0.f ? ~0ull : 0ull;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const f4 diagonal = *reinterpret_cast<const f4 *>(&tree_rows[C::kWeigh / 4 + 16 * t + 4 * b]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (__builtin_fabsf(R[t][j] * diagonal[j]) < small && top > 0.f && (R[t][j] != 0.f || diagonal[j] < 0.f))
+                                mine |= 1ull << (16 * t + 4 * b + j);
+                    }
+                    mine &= ~lost;
+#pragma unroll
+                    for (int d = 1; d < 64; d *= 2) mine |= __shfl_xor(mine, d);
+                    mine &= n < 64 ? (1ull << n) - 1 : ~0ull;
+                    redo = mine;
+                }
+                redo_rows[g0 + 4 * u] = redo;
                 const Split r0 = split(R[0], R[1], times2(1.0f, up)), r1 = split(R[2], R[3], times2(1.0f, up));
                 f4 U[4], o[4];
 #pragma unroll
@@ -639,8 +713,14 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                         U[t] = mfma16x16x32(lo, rows.hi, U[t]);
                     }
                 }
-                const Split v[2] = {split(U[0], U[1], kDown), split(U[2], U[3], kDown)};
-                const float of_u = times2(1.0f, 20 - up);
+                float top_u = 0.f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top_u = fmaxf(top_u, __builtin_fabsf(U[t][j]));
+                const int up_u = kTop - max(exponent(top_of_column(top_u)), -60);
+                const Split v[2] = {split(U[0], U[1], times2(1.0f, up_u)), split(U[2], U[3], times2(1.0f, up_u))};
+                const float of_u = times2(1.0f, -up - up_u);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (t >= row_tiles) break;
@@ -663,6 +743,52 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 }
             }
         }
+
+        // Those rows, a group of columns at a time: a row's state from the pool's, through the tokens that it descends from,
+        // or on from the last row's where that is one of them.
+#pragma unroll 1
+        for (int g = wave; g < a.value_dim / 16; g += 4) {
+            const uint64_t rows = redo_rows[g];
+            uint64_t todo = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(rows >> 32)) << 32 |
+                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)rows);
+            if (todo == 0) continue;
+            wait_loads<0>();                   // (these rows' stores above are done)
+            asm volatile("" : "+v"(lane), "+v"(m), "+v"(b) : : "memory");
+            const int col = 16 * g + m;
+            Gates gate{0.f, 0.f};
+            if (lane < n)
+                gate = gates_of<BF>(a, s.first + lane, h0, a.a_log ? expf(a.a_log[h0]) : 0.f, a.a_log ? a.dt_bias[h0] : 0.f);
+            const float all_keep = expf(gate.g);
+            f4 from_there[kRowTiles];
+            uint64_t seen = 0;                 // what that state has been through
+#pragma unroll 1
+            for (; todo; todo &= todo - 1) {
+                const int row = __builtin_ctzll(todo);
+                const uint64_t word = kin[row];
+                const uint64_t path = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(word >> 32)) << 32 |
+                                      (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)word);
+                if (seen == 0 || (seen & ~path)) {
+                    seen = 0;
+                    const float *const from = a.state + ((max(s.state, (int64_t)0) * a.v_heads + h0) * DK + 4 * b) * a.value_dim + col;
+#pragma unroll
+                    for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) from_there[t][j] = s.fresh ? 0.f : from[(int64_t)(16 * t + j) * a.value_dim];
+                }
+                float o = 0.f;
+#pragma unroll 1
+                for (uint64_t left = path & ~seen; left; left &= left - 1) {
+                    const int i = __builtin_ctzll(left);
+                    const float keep = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all_keep), i));
+                    const float strength = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate.beta), i));
+                    o = one_token<BF, DK>(a, s.first + i, h0, col, b, keep, strength, from_there);
+                }
+                seen = path;
+                if (b == 0)
+                    static_cast<uint16_t *>(a.out)[(s.first + row) * a.out_stride + (int64_t)h0 * a.value_dim + col] =
+                        (uint16_t)pack2<BF>(o, 0.f);
+            }
+        }
     }
 }
 
@@ -672,52 +798,6 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
     typedef __attribute__((address_space(3))) s4 lds_s4;
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)const_cast<lds_u8 *>(p)));
-}
-
-// One token of a head for the columns of a wave, in fp32 throughout as the kernel for tokens has it: moves S on
-// (rows 16 t + 4 b + j of column `col`, the (lane % 16)-th of the wave's) and returns the output.
-template <bool BF, int DK>
-__device__ __forceinline__ float one_token(const DeltaArgs &a, int64_t row, int h, int col, int b, float keep, float beta,
-                                           f4 (&S)[DK / 16]) {
-    constexpr int kTiles = DK / 16;
-    const int hk = h / (a.v_heads / a.k_heads);
-    const uint16_t *const qr = static_cast<const uint16_t *>(a.q) + row * a.q_stride + hk * DK + 4 * b;
-    const uint16_t *const kr = static_cast<const uint16_t *>(a.k) + row * a.k_stride + hk * DK + 4 * b;
-    const float v = lo_f32<BF>(static_cast<const uint16_t *>(a.v)[row * a.v_stride + (int64_t)h * a.value_dim + col]);
-    float q[4 * kTiles], k[4 * kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-        const u2 q4 = *reinterpret_cast<const u2 *>(qr + 16 * t), k4 = *reinterpret_cast<const u2 *>(kr + 16 * t);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            q[4 * t + 2 * i] = lo_f32<BF>(q4[i]);
-            q[4 * t + 2 * i + 1] = hi_f32<BF>(q4[i]);
-            k[4 * t + 2 * i] = lo_f32<BF>(k4[i]);
-            k[4 * t + 2 * i + 1] = hi_f32<BF>(k4[i]);
-        }
-    }
-    if (a.unit) {
-        to_unit<16>(k, a.eps);
-        to_unit<16>(q, a.eps);
-    }
-    float qk = 0.f, sk = 0.f, sq = 0.f;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            qk = __builtin_fmaf(q[4 * t + j], k[4 * t + j], qk);
-            sk = __builtin_fmaf(S[t][j], k[4 * t + j], sk);
-            sq = __builtin_fmaf(S[t][j], q[4 * t + j], sq);
-        }
-    qk = over_lanes<16>(qk);
-    sk = over_lanes<16>(sk);
-    sq = over_lanes<16>(sq);
-    const float u = beta * (v - keep * sk);
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[t][j] = __builtin_fmaf(k[4 * t + j], u, keep * S[t][j]);
-    return a.scale * (keep * sq + qk * u);
 }
 
 // A workgroup walks over the chunks with 16 GROUPS columns of one head.  Wave w < GROUPS takes what the

@@ -145,3 +145,33 @@ def test_sizes_at_the_ends_of_the_type(dev, size):  # noqa: F811
     d = made([100, 20], (1, 2, 64, 64), BF16, -0.1, seed=1)
     d.v, d.state = (d.v.float() * size).to(BF16), d.state * size
     run(d, dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("power", [13, 20, 24, 30, 40])
+@pytest.mark.parametrize("columns", [FEW, EVERY], ids=["column", "row"])
+def test_no_branch_of_a_tree_loses_to_another(dev, columns, power, heads, dtype):  # noqa: F811
+    """Large values on one branch, at the roots, and before drafts that have forgotten them."""
+    rng = random.Random(power)
+    # two roots side by side; one root with two branches; drafts anyhow; a chain
+    trees = [[-1, -1], [-1] + [0 if i < 3 else i - 2 for i in range(1, 40)], tr.random_tree(64, rng, 3), tr.chain(20)]
+    ns = [len(t) for t in trees]
+    for g, large in ((-0.02, (0, 3, 45, 125)), (-0.02, (1, 2 + 38, 42 + 63)), (-0.5, (2, 42, 106))):
+        d = made(ns, heads, dtype, g, seed=power, trees=trees)
+        for i in large:
+            grow(d, slice(i, i + 1), columns, 2.0 ** power)
+        d.a[106 + 10] = -90.0
+        run(d, dev)
+    d = made(ns, heads, dtype, -0.3, seed=power, trees=trees)
+    d.state *= 2.0 ** power
+    d.a[2] = d.a[42] = -90.0
+    run(d, dev)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 123, 2.0 ** 99, 2.0 ** -100])
+def test_sizes_at_the_ends_of_the_type_in_a_tree(dev, size):  # noqa: F811
+    trees = [tr.random_tree(30, random.Random(2), 2), tr.chain(5)]
+    d = made([30, 5], (1, 2, 64, 64), BF16, -0.1, seed=1, trees=trees)
+    d.v, d.state = (d.v.float() * size).to(BF16), d.state * size
+    run(d, dev)
