@@ -628,7 +628,7 @@ int w4a16_short_conv(const void *x, int64_t x_stride, const float *weight, const
 /* The gated delta rule, for each token and value head h (with key head
  * h / (v_heads / k_heads)):
  *     S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q
- *   q, k : [T, k_heads, key_dim], key_dim 64 or 128
+ *   q, k : [T, k_heads, key_dim], key_dim 64 or 128; their product must not leave fp32 (|q| |k| < 2^127)
  *   v, out : [T, v_heads, value_dim], value_dim 64, 128, 192 or 256, strides
  *     below 2^23; out must not overlap an input
  *   a_log, dt_bias : fp32 [v_heads]: g = -exp(a_log) softplus(a + dt_bias) and

@@ -57,6 +57,9 @@ constexpr int kTopU = 9;               // and rows of U for the next state below
 // of R; from its weighed rows (2^-25 of U at most), the next state's, 2^-35, and kSmall of R in their heaviest.
 constexpr float kLeastU = 2.0f, kLost = 1.0f / (1 << 26), kSmall = 1.0f / (1 << 17);
 constexpr int kLeastWeighed = -15;
+// Factors that chunks take: what comes off a row, products with queries, elements of T.  With rows and states below 2^100 none
+// of what is made of them leaves fp32.
+constexpr float kMostRow = 1 << 24, kMostProduct = 0x1p32f, kMostT = 1 << 20;
 constexpr int kWalked = -(1 << 30);    // in the place of U's power of two: the outputs are made already
 constexpr float kRestUp = 64.f;        // what fp16 leaves of a number below 2^14 is at most 4; with this, 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -73,8 +76,8 @@ struct Chunk {
     static constexpr int kHigh = 0, kLow = 6 * 1024, kWithin = 12 * 1024, kRest = 18 * 1024, kRows = BF ? kRest : 21 * 1024;
     static constexpr int kValue = kRows + 2 * 1024;
     // in kRows: fp32 [64] each: what comes off a row (e^G |k|-scale), what weighs a row of U for S, for the
-    // output of S and of U; e^G_last, the power of two in the second of them; what the last
-    // sixteen rows count for S, of the heaviest; e^g, T's power of two, and its diagonal
+    // output of S and of U; e^G_last, the power of two in the second of them; whether something is
+    // beyond; what the last sixteen rows count for S, of the heaviest (NaN then); e^g, T's power of two, and its diagonal
     static constexpr int kOff = 0, kWeigh = 256, kFromS = 512, kFromU = 768, kLast = 1024, kHeavy = 1040, kKeep = 1280, kTau = 1536, kDiagonal = 1792;
 };
 
@@ -152,7 +155,7 @@ __device__ __forceinline__ float top_of_column(float v) {
     return __builtin_elementwise_maximum(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
 }
 
-// One token of a head for the columns of a wave, in fp32 throughout as the kernel for tokens has it: moves S on
+// One token of a head for the columns of a wave, in fp32 throughout: moves S on
 // (rows 16 t + 4 b + j of column `col`, the (lane % 16)-th of the wave's) and returns the output.
 template <bool BF, int DK>
 __device__ __forceinline__ float one_token(const DeltaArgs &a, int64_t row, int h, int col, int b, float keep, float beta,
@@ -178,24 +181,21 @@ __device__ __forceinline__ float one_token(const DeltaArgs &a, int64_t row, int 
         to_unit<16>(k, a.eps);
         to_unit<16>(q, a.eps);
     }
-    float qk = 0.f, sk = 0.f, sq = 0.f;
+    // (the output from the new state, not by q . k, which may leave fp32)
+    float sk = 0.f, sq = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sk = __builtin_fmaf(S[t][j], k[4 * t + j], sk);
+    const float u = beta * (v - keep * over_lanes<16>(sk));
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            qk = __builtin_fmaf(q[4 * t + j], k[4 * t + j], qk);
-            sk = __builtin_fmaf(S[t][j], k[4 * t + j], sk);
+            S[t][j] = __builtin_fmaf(k[4 * t + j], u, keep * S[t][j]);
             sq = __builtin_fmaf(S[t][j], q[4 * t + j], sq);
         }
-    qk = over_lanes<16>(qk);
-    sk = over_lanes<16>(sk);
-    sq = over_lanes<16>(sq);
-    const float u = beta * (v - keep * sk);
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[t][j] = __builtin_fmaf(k[4 * t + j], u, keep * S[t][j]);
-    return a.scale * (keep * sq + qk * u);
+    return a.scale * over_lanes<16>(sq);
 }
 
 constexpr int kMostHeads = 4;          // value heads of a workgroup
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
     __shared__ int tau[kChunk];
     __shared__ uint64_t kin[kChunk];
     __shared__ uint64_t redo_rows[TREE ? 16 : 1];      // of a group of columns, rows that go token by token
+    __shared__ int marks[4];                   // of a wave: factors beyond what products of them hold
     __shared__ uint32_t bad_row[kChunk], bad_gate[kMostHeads][kChunk];     // 1: the key, 2: the query; a gate
 
     const int ci = blockIdx.x, h0 = blockIdx.y * heads, r = a.v_heads / a.k_heads, hk = h0 / r;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
 
     // ---- keys and queries as fp16 rows of a common size, and what came off them ----
     uint32_t bad = 0;
+    bool large = false;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const uint32_t limit = BF ? 0x7F80u : 0x7C00u;
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             float f = a.unit ? 1.0f / sqrtf(sum + times2(a.eps, 2 * up)) : times2(1.0f, -up);
             if (my_row >= n) f = 0.f;
             const bool ok = fine && f < __builtin_inff();
+            large |= !(f * (which ? a.scale : 1.0f) < kMostRow);
             (which ? qf : kf)[my_row] = ok ? f : 0.f;
             if (!ok) bad |= 1u + which;
             if (which) bad_row[my_row] = bad;
@@ -397,6 +400,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
         uint8_t *const to = seg.values + (slot * a.v_heads + h) * C::kValue;
         __syncthreads();                       // keys and queries, or the head before, are done with
         f4 p[4];
+        bool beyond = large;
         {
             // (all that is read comes before A is written, which the compiler takes to overlap it)
             const int row0 = 16 * wave + 4 * b;
@@ -418,8 +422,10 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 for (int j = 0; j < 4; ++j) {
                     const bool sees = TREE ? words[TREE ? j : 0] >> col & 1 : col <= row0 + j;
                     const float w = sees ? exp_f32((float)(of_row[j] - of_col[nt])) : 0.f;
-                    A[row0 + j][col] = strength[j] * (kk[nt][j] * w);
-                    p[nt][j] = qk[nt][j] * w;
+                    // (selects: a product may be infinite)
+                    A[row0 + j][col] = sees ? strength[j] * (kk[nt][j] * w) : 0.f;
+                    p[nt][j] = sees ? qk[nt][j] * w : 0.f;
+                    beyond |= !(__builtin_fabsf(p[nt][j]) < kMostProduct);
                 }
             }
         }
@@ -485,11 +491,17 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         t[d][e + i] = v[i] * w[i];
-                        top = fmaxf(top, __builtin_fabsf(t[d][e + i]));
+                        top = __builtin_elementwise_maximum(top, __builtin_fabsf(t[d][e + i]));
                     }
                 }
+            beyond |= !(top < kMostT) && row < n;
             const int up = kTop - max(exponent(top_of_column(top)), -60);
             if (b == 0) tau[row] = up;
+            if (__builtin_amdgcn_ballot_w64(beyond) == 0) {
+                if (lane == 0) marks[wave] = 0;
+            } else if (lane == 0) {
+                marks[wave] = 1;
+            }
             if constexpr (TREE) __syncthreads();               // X is done with: T comes in its place
             uint8_t *const tiles = TREE ? reinterpret_cast<uint8_t *>(&X[0][0]) : to;
 #pragma unroll
@@ -568,7 +580,9 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 rows[C::kDiagonal / 4 + lane] = diagonal;
                 const float counts = times2(__builtin_fabsf(weigh * beta[lane]), tau[lane]);
                 const float most = top_of_column(top_of_row(counts));
-                if (lane >= 48) rows[C::kHeavy / 4 + lane - 48] = most > 0.f ? counts / most : 1.f;
+                const int mark = marks[0] | marks[1] | marks[2] | marks[3];
+                if (lane >= 48) rows[C::kHeavy / 4 + lane - 48] = mark ? nan : most > 0.f ? counts / most : 1.f;
+                if (lane == 0) reinterpret_cast<int *>(rows)[C::kLast / 4 + 2] = mark;
             }
             if (!TREE && lane == 0) {
                 rows[C::kLast / 4] = exp_f32((float)G[kChunk - 1]);
@@ -580,6 +594,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
     // ======== a tree's outputs: as chunk_scan_kernel has them, two groups of columns at a time ========
     if constexpr (TREE) {
         __syncthreads();
+        const bool marked = __builtin_amdgcn_readfirstlane(marks[0] | marks[1] | marks[2] | marks[3]) != 0;
         const uint8_t *const tiles = reinterpret_cast<const uint8_t *>(&X[0][0]);
         const _Float16 *const P = reinterpret_cast<const _Float16 *>(&A[0][0]);
         const int v_row = 2 * (int)a.v_stride, out_row = 2 * (int)a.out_stride;
@@ -679,8 +694,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 const float small = times2(BF ? kLeastU / 4 : kLeastU, -up);
                 uint64_t redo = 0;
                 const bool beyond = top >= 0x1p100f || (top < 0x1p-100f && top > 0.f) || of_s[u] > 0x1p86f;
-                if (__builtin_amdgcn_ballot_w64(beyond || (least < small && top > 0.f))) {
-                    uint64_t mine = beyond && top > 0.f ? ~0ull : 0ull;
+                if (marked || __builtin_amdgcn_ballot_w64(beyond || (least < small && top > 0.f))) {
+                    uint64_t mine = marked || (beyond && top > 0.f) ? ~0ull : 0ull;
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         const f4 diagonal = *reinterpret_cast<const f4 *>(&tree_rows[C::kWeigh / 4 + 16 * t + 4 * b]);
@@ -689,7 +704,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                             if (__builtin_fabsf(R[t][j] * diagonal[j]) < small && top > 0.f && (R[t][j] != 0.f || diagonal[j] < 0.f))
                                 mine |= 1ull << (16 * t + 4 * b + j);
                     }
-                    mine &= ~lost;
+                    if (!marked) mine &= ~lost;
 #pragma unroll
                     for (int d = 1; d < 64; d *= 2) mine |= __shfl_xor(mine, d);
                     mine &= n < 64 ? (1ull << n) - 1 : ~0ull;
@@ -1173,9 +1188,9 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
         uint64_t lost = 0;                     // rows that come after one that is not finite
         // Sizes far apart, such as factors of them leave fp32, or what is not finite.  (By the last rows alone whether the
         // next state's are large enough: that is where most heads have their heaviest.)
-        float of_last = 0.f;
+        float of_last = __builtin_fabsf(R[3][0]) * heavy[0];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) of_last = fmaxf(of_last, __builtin_fabsf(R[3][j]) * heavy[j]);
+        for (int j = 1; j < 4; ++j) of_last = fmaxf(of_last, __builtin_fabsf(R[3][j]) * heavy[j]);
         const uint64_t enough = __builtin_amdgcn_ballot_w64(of_last >= kSmall * top_r);
         const uint64_t odd = __builtin_amdgcn_ballot_w64(least < kLost * top_r || !(top_r < 0x1p100f) ||
                                                          (top_r < 0x1p-100f && top_r > 0.f) || power < kTop - 100);
@@ -1210,7 +1225,8 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
                               times2(top_s, kTop - max(exponent(top_r), -100) + weigh_up - power),
                               lost ? min(n, (int)__builtin_ctzll(lost)) : n, lane, b);
             alone |= top_r >= 0x1p100f || top_r < 0x1p-100f || power < kTop - 100;
-            if (__builtin_amdgcn_ballot_w64(alone && top_r > 0.f)) {
+            alone = (alone && top_r > 0.f) || lds_get<int>(val + C::kRows + C::kLast + 8) != 0;
+            if (__builtin_amdgcn_ballot_w64(alone)) {
                 lds_put(factors + 64, kWalked);
                 lds_put(lost_at, ~(uint64_t)0);
                 lds_barrier();                 // (2) as below
