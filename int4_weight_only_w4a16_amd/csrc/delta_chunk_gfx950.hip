@@ -334,7 +334,10 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
         sum += __shfl_xor(sum, 2);
         if (my_part == 0) {
             // (rows past the sequence's are zeros and count for nothing)
-            float f = a.unit ? 1.0f / sqrtf(sum + times2(a.eps, 2 * up)) : times2(1.0f, -up);
+            const float eps = times2(a.eps, 2 * up);       // (infinite: then it is all that there is)
+            float f = !a.unit                  ? times2(1.0f, -up)
+                      : eps < __builtin_inff() ? 1.0f / sqrtf(sum + eps)
+                                               : times2(1.0f / sqrtf(a.eps), -up);
             if (my_row >= n) f = 0.f;
             const bool ok = fine && f < __builtin_inff();
             large |= !(f * (which ? a.scale : 1.0f) < kMostRow);

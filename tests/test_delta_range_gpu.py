@@ -234,3 +234,15 @@ def test_a_key_at_the_end_of_the_type(dev, n):  # noqa: F811
         # (fp32 has steps of 2^-149 for this state: eight roundings by half of one, through the key to u, 2^127 beta, and
         # back, 2^127: 2^7)
         check(d, *d.call(dev), steps=2.0 ** 7)
+
+
+@pytest.mark.parametrize("n", [5, 70])
+@pytest.mark.parametrize("tree", [False, True])
+def test_unit_length_of_rows_far_below_the_epsilon(dev, tree, n):  # noqa: F811
+    """x / sqrt(sum x^2 + eps) of rows so small that eps in their measure leaves fp32: 1000 x, not zero."""
+    n = min(n, 64) if tree else n
+    d = Delta([n], 1, 2, 64, 64, BF16, seed=3, trees=[tr.chain(n)] if tree else None)
+    for x, power in ((d.q, -70), (d.k, -75)):
+        x[1::3] = (x[1::3].float() * 2.0 ** power).to(BF16)
+        x[2::3] = (x[2::3].float() * 2.0 ** -8).to(BF16)
+    run(d, dev)
