@@ -30,9 +30,9 @@ inline void check(int status, const char *what) {
     throw py::error_already_set();
 }
 
-inline unsigned type_flag(at::ScalarType t) {
+inline unsigned type_flag(at::ScalarType t, const char *of = "q, k and v") {
     if (t == at::kBFloat16) return W4A16_X_BF16;
-    if (t != at::kHalf) refuse("q, k and v must be float16 or bfloat16");
+    if (t != at::kHalf) refuse(std::string(of) + " must be float16 or bfloat16");
     return 0;
 }
 

@@ -41,7 +41,7 @@ Tensor short_conv(const Tensor &x, const Tensor &weight, const Tensor &state, co
     if (x.dim() != 2 || weight.dim() != 2 || state.dim() != 3)
         refuse("x must be [tokens, channels], weight [channels, width] and state [states, width - 1, channels]");
     const int64_t T = x.size(0), C = x.size(1), W = weight.size(1);
-    const unsigned flags = type_flag(x.scalar_type()) | (silu ? W4A16_SILU : 0);
+    const unsigned flags = type_flag(x.scalar_type(), "x") | (silu ? W4A16_SILU : 0);
     const int64_t xs = rows_stride("x", x, T, C, x.scalar_type(), x.device());
     const auto *w = static_cast<float *>(plain("weight", weight, at::kFloat, x.device(), {C, W}));
     const float *bias_ptr = nullptr;

@@ -125,3 +125,11 @@ def test_a_chunk_s_triangular_form_is_the_recurrence():
         if parents == tr.chain(n):
             end = torch.exp(G[-1]) * S[0] + (torch.exp(G[-1] - G)[:, None] * kn).T @ U
             assert (end - last[0]).abs().max() < 1e-12
+
+
+def test_short_conv_names_its_own_argument(lib):  # noqa: F811
+    import torch
+    x, weight, state = torch.zeros(3, 16), torch.zeros(16, 4), torch.zeros(1, 3, 16)
+    index = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="^x must be float16 or bfloat16"):
+        w4.short_conv(x, weight, state, index, torch.tensor([0, 3], dtype=torch.int32), 3)
