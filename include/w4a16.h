@@ -650,7 +650,8 @@ int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_s
                      int64_t max_q, float scale, float eps, unsigned flags, void *workspace,
                      size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of w4a16_delta_rule, of either type (tree: whether one is given); 0 also for
+/* Workspace bytes of w4a16_delta_rule, of either type (tree: whether one is given), enough for any
+ * call of fewer sequences and shorter ones as well (the same heads and sizes); 0 also for
  * arguments it rejects. */
 size_t w4a16_delta_rule_workspace_bytes(int64_t batch, int64_t T, int64_t k_heads,
                                         int64_t v_heads, int64_t key_dim, int64_t value_dim,

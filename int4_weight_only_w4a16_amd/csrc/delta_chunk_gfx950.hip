@@ -1353,13 +1353,18 @@ size_t value_bytes(const DeltaArgs &a) { return a.bf16 ? Chunk<true, 128>::kValu
 size_t chunk_bytes(const DeltaArgs &a) { return a.k_heads * key_bytes(a) + a.v_heads * value_bytes(a); }
 int chunks_of(const DeltaArgs &a) { return (a.s.max_q + kChunk - 1) / kChunk; }
 
+// Chunks that the workspace holds at a time.
+size_t slots_of(const DeltaArgs &a) {
+    constexpr size_t kMost = (size_t)256 << 20;
+    return std::max<size_t>(1, kMost / chunk_bytes(a));
+}
+
 // How a call is cut: sequences and chunks of each that the workspace holds at a time.
 struct Cut {
     int batch, chunks;
 };
 Cut cut_of(const DeltaArgs &a) {
-    constexpr size_t kMost = (size_t)256 << 20;
-    const size_t slots = std::max<size_t>(1, kMost / chunk_bytes(a));
+    const size_t slots = slots_of(a);
     Cut c;
     c.chunks = (int)std::min<size_t>(chunks_of(a), slots);
     c.batch = (int)std::min<size_t>(a.s.batch, std::max<size_t>(1, slots / c.chunks));
@@ -1413,7 +1418,8 @@ hipError_t launch_tree(const DeltaArgs &a, hipStream_t stream) {
 size_t delta_chunk_workspace_bytes(const DeltaArgs &a) {
     if (a.s.tree) return 0;
     const Cut c = cut_of(a);
-    size_t bytes = chunk_bytes(a) * c.chunks * c.batch;
+    // (not by how this call is cut: a smaller one may fill more of what there is at a time)
+    size_t bytes = chunk_bytes(a) * std::min<size_t>(slots_of(a), (size_t)chunks_of(a) * a.s.batch);
     if (c.chunks < chunks_of(a)) bytes += (size_t)c.batch * a.v_heads * a.key_dim * a.value_dim * 4;
     return bytes;
 }

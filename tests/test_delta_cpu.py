@@ -133,3 +133,16 @@ def test_short_conv_names_its_own_argument(lib):  # noqa: F811
     index = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="^x must be float16 or bfloat16"):
         w4.short_conv(x, weight, state, index, torch.tensor([0, 3], dtype=torch.int32), 3)
+
+
+def test_a_workspace_for_the_largest_call_does_for_smaller_ones(lib):  # noqa: F811
+    """A program keeps one workspace, of the size for its most sequences and longest prompt."""
+    for hk, hv, dk, dv in ((16, 48, 128, 128), (16, 64, 128, 256), (1, 2, 64, 64)):
+        size = lambda batch, max_q, T: w4.delta_rule_workspace_bytes(batch, T, hk, hv, dk, dv, max_q)
+        for batch, max_q in ((64, 8192), (3, 20000), (7, 3000), (200, 700), (2, 11000)):
+            most = size(batch, max_q, batch * max_q)
+            for b in {1, 2, 3, batch // 2, batch - 1, batch}:
+                for q in {1, 17, 64, 65, max_q // 3, max_q // 2, max_q - 64, max_q}:
+                    if 1 <= b and 1 <= q:
+                        assert size(b, q, b * q) <= most, (batch, max_q, b, q)
+                        assert size(b, q, q) <= most
