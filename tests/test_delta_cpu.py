@@ -143,6 +143,6 @@ def test_a_workspace_for_the_largest_call_does_for_smaller_ones(lib):  # noqa: F
             most = size(batch, max_q, batch * max_q)
             for b in {1, 2, 3, batch // 2, batch - 1, batch}:
                 for q in {1, 17, 64, 65, max_q // 3, max_q // 2, max_q - 64, max_q}:
-                    if 1 <= b and 1 <= q:
+                    if 1 <= b <= batch and 1 <= q:
                         assert size(b, q, b * q) <= most, (batch, max_q, b, q)
                         assert size(b, q, q) <= most
