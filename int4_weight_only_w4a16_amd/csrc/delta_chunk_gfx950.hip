@@ -1204,25 +1204,27 @@ __global__ void __launch_bounds__(128 * GROUPS) chunk_scan_kernel(DeltaArgs a, S
             asm volatile("" : "+v"(lane));
             const int b = lane >> 4;
             const lds_u8 *const rows = val + C::kRows + 16 * b;
-            uint64_t found = 0;
+            if (__builtin_amdgcn_ballot_w64(!(top_r < __builtin_inff()))) {
+                uint64_t found = 0;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    found |= __builtin_fabsf(R[t][j]) < __builtin_inff() ? 0ull : 1ull << (16 * t + 4 * b + j);
-            found |= __shfl_xor(found, 16);
-            found |= __shfl_xor(found, 32);
-            lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
-            top_r = 0.f;
+                    for (int j = 0; j < 4; ++j)
+                        found |= __builtin_fabsf(R[t][j]) < __builtin_inff() ? 0ull : 1ull << (16 * t + 4 * b + j);
+                found |= __shfl_xor(found, 16);
+                found |= __shfl_xor(found, 32);
+                lost = found ? ~0ull << __builtin_ctzll(found) : 0ull;
+                top_r = 0.f;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    R[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? 0.f : R[t][j];
-                    top_r = fmaxf(top_r, __builtin_fabsf(R[t][j]));
-                }
-            top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
-            top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
+                    for (int j = 0; j < 4; ++j) {
+                        R[t][j] = lost >> (16 * t + 4 * b + j) & 1 ? 0.f : R[t][j];
+                        top_r = fmaxf(top_r, __builtin_fabsf(R[t][j]));
+                    }
+                top_r = fmaxf(top_r, __shfl_xor(top_r, 16));
+                top_r = fmaxf(top_r, __shfl_xor(top_r, 32));
+            }
             const int n = min(kChunk, s.n - first - kChunk * ci);
             bool alone = lose(R, times2(1.0f, kTop - max(exponent(top_r), -100)), rows, gamma,
                               times2(top_s, kTop - max(exponent(top_r), -100) + weigh_up - power),
