@@ -639,7 +639,15 @@ int w4a16_short_conv(const void *x, int64_t x_stride, const float *weight, const
  *   scale : finite and positive
  *   workspace : w4a16_delta_rule_workspace_bytes(...) bytes, caller-owned, no
  *     initial contents (null when that is 0); calls that overlap in time must
- *     not share one. */
+ *     not share one.
+ * Calls of up to 16 tokens a sequence go token by token in fp32, longer ones 64
+ * tokens at a time, every sequence of a call alike: how one is rounded goes by
+ * the call's max_q, within the same bounds.  A chunk whose numbers lie too far
+ * apart for that goes token by token too, and takes about as long as such calls
+ * do (some 70 us a chunk).  One long sequence beside many of a few tokens is
+ * better two calls: of 2048 tokens with 64 of one token, 1.3 ms; apart 0.16.
+ * Keys and queries enter long calls and trees with what is below 2^-25 (keys;
+ * queries 2^-39) of their row's largest element rounded away. */
 int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, const void *a, int64_t a_stride,
                      const void *b, int64_t b_stride, const float *a_log, const float *dt_bias,

@@ -127,6 +127,6 @@ void bind_delta(py::module_ &m) {
           "beta = sigmoid(b), a and b [T, value heads] of q's type; without, a is g (not positive) and b beta, fp32.\n"
           "scale: 1 / sqrt(key channels) unless given.  max_q: at least the most tokens of any sequence.  tree\n"
           "(int64 [T]): the tokens are a tree of drafts as in kv4_tree_attention, each continues the state that the\n"
-          "last token it descends from left, and the states stay as they are.  Returns out [T, value heads, value\n"
-          "channels].");
+          "last token it descends from left, and the states stay as they are.  One long sequence beside many of a few\n"
+          "tokens is better two calls.  Returns out [T, value heads, value channels].");
 }

@@ -18,9 +18,10 @@
 //
 // The state is fp32, and its sums keep that: each factor that is not an input enters in two
 // 16-bit parts of eleven bits (S, the rows V - e^G K S, T, the rows e^(G_last - G) U), three
-// products for a pair of such factors, lo x lo left out (2^-22).  Inputs are exact as they are, bfloat16
-// ones too, once a power of two for each row brings them into fp16's range; so do powers of
-// two for each row of T and each column of S and of the rows.  What goes into the output
+// products for a pair of such factors, lo x lo left out (2^-22).  Keys and queries of
+// either type enter as they are, once a power of two for each row brings them into fp16's range, but for
+// elements below about 2^-14 (keys; queries 2^-28) of their row's largest, which fp16's smallest place rounds: by at
+// most 2^-25 (2^-39) of that largest.  So do powers of two for each row of T and each column of S and of the rows.  What goes into the output
 // alone has one part (2^-12), an eighth of a bfloat16 output's own rounding.  An fp16 output would be
 // 1.7 times as far off as its rounding alone: there U has two parts and the triangle a second one
 // of e4m3 (1.1 times; five prompts 112 -> 119 us); a tree's have two of S and U (1.2 times).
@@ -29,11 +30,11 @@
 // Two parts hold 22 bits of what is within 2^-16 of the largest they are made with, and fewer of what is smaller:
 // of a row of R beside a column's largest, which may be a later token's, or one that has faded by the chunk's end.
 // So each chunk is looked at (least and weighed rows of R), and one where a row or the next state would lose by it
-// is gone through token by token, in fp32 from the inputs (0.7 us a token; the look, and U's powers of two by its own
-// largest, cost 2 %: 8191 tokens 300 -> 304 us, five prompts 122.6 -> 126).
+// is gone through token by token, in fp32 from the inputs (1.1 us a token; the look, and U's powers of two by its own
+// largest, cost 2 to 4 %: 8191 tokens 298 -> 304 us, five prompts 120 -> 124).  So is a chunk with products that leave fp32.
 //
 // Bound by the chain of chunks: one sequence of 8191 tokens, 16 + 48 heads of 128 x 128, bfloat16,
-// takes 76 us for the preparation and 232 to 244 for the scan, 1.9 a chunk (memory alone: 58).
+// takes 76 us for the preparation and 242 to 256 for the scan, 1.9 a chunk (memory alone: 58).
 
 // What is not finite (in a key, a gate, a value) would reach earlier rows, or a tree's other
 // branches, through products with zero.  Its row is taken out as zeros and marked, and the rows
@@ -202,7 +203,7 @@ constexpr int kMostHeads = 4;          // value heads of a workgroup
 
 // One chunk of `heads` value heads that share a key head: what the heads have in common, the products of
 // keys with keys and queries among it, is made once.  TREE: of one head, and its outputs as well, since there
-// is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 36 us with the outputs in a launch of their own).
+// is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 24.5 us; with the outputs in a launch of their own once 36 to 23).
 template <bool BF, int DK, bool TREE>
 __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
     using C = Chunk<BF, DK>;
@@ -819,7 +820,7 @@ __device__ __forceinline__ u2 read_column(const lds_u8 *p) {
 }
 
 // A workgroup walks over the chunks with 16 GROUPS columns of one head.  Wave w < GROUPS takes what the
-// next state needs, for sixteen columns; wave GROUPS + w, on the same SIMD, their outputs, from the state and
+// next state needs, for sixteen columns; wave GROUPS + w (with four groups on the same SIMD) their outputs, from the state and
 // the rows U that the first hands over in LDS, and the copies.  (All in one wave, the only one on its SIMD,
 // a chunk took 9300 cycles, of which instructions took 3300; now about 4500.)
 template <bool BF, int DK, int GROUPS>
@@ -1386,15 +1387,18 @@ hipError_t launch_row(const DeltaArgs &a, hipStream_t stream) {
             seg.batch = std::min(c.batch, a.s.batch - b0);
             seg.first_chunk = c0;
             seg.chunks = std::min(c.chunks, chunks_of(a) - c0);
-            // value heads that share a key head in one workgroup, as long as that leaves some for every CU
+            // Value heads that share a key head in one workgroup, as long as that leaves two for every CU (one sequence of
+            // 8191 tokens, 16 + 48 heads, the whole call: 307 us, each alone 323; 8 of 500: 127 and 139; but one of
+            // 1000, 768 workgroups: 58.5 together, 53.2 alone).
             int heads = 1;
             for (int i = 2; i <= kMostHeads; ++i)
                 if (a.v_heads / a.k_heads % i == 0 && (int64_t)seg.chunks * a.v_heads / i * seg.batch >= 512) heads = i;
             chunk_prep_kernel<BF, DK, false><<<dim3(seg.chunks, a.v_heads / heads, seg.batch), 256, 0, stream>>>(a, seg, heads);
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            // 32 columns a workgroup while each finds a CU of its own, else 64 (one sequence of 8191 tokens, 48
-            // heads, the whole call: 313 and 370 us; five of 333 to 2500, 32 heads: 133 and 121)
+            // 32 columns a workgroup while each finds a CU of its own, else 64 (the whole call: one sequence of 8191 tokens, 48
+            // heads, 192 workgroups 307 and 386 us; two of 4000, 32 heads, 256: 144 and 159; two of 2000, 48 heads, 384:
+            // 159 and 124; five of 2500, 32 heads: 273 and 228).
             if ((int64_t)a.value_dim / 32 * a.v_heads * seg.batch <= 256)
                 chunk_scan_kernel<BF, DK, 2><<<dim3(a.value_dim / 32, a.v_heads, seg.batch), 256, 0, stream>>>(a, seg);
             else

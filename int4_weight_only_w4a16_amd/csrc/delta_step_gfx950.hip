@@ -17,7 +17,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kColumns = 16;           // of a wave
-constexpr int kWaves = 4;              // of a workgroup: whole lines of memory (64 sequences: 67 us, with one wave 95)
+constexpr int kWaves = 4;              // of a workgroup: whole lines of memory (64 sequences, states cached in part: 67 us, with one wave 95)
 
 // What a lane needs of one token.
 template <int ROWS>

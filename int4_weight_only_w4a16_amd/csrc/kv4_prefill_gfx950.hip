@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(kManyThreads<D>)
             if constexpr (TREE && D == 256) {
                 // what a row sees is made again for these few stages (opaque: it is not kept in registers, which are
                 // short here: 176 bytes of a lane's in scratch, 152 so; with 128 channels, where they are not, it
-                // costs 143 -> 163 us for 64 drafts over 65000 slots)
+                // costs 143 -> 163 us for 64 drafts over 65000 slots; with 256 it costs 310 -> 325 us for
+                // 64 drafts over 30000 slots, groups of 32, and is for the scratch memory that a lane keeps)
                 int again = lane;
                 asm volatile("" : "+v"(again));
                 again = w.row0 + 32 * wave + (again & 31);

@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvArgs a, int channel_block
     }
 }
 
-// Tokens of a lane, and token blocks of a workgroup.
+// Tokens of a lane, and token blocks of a workgroup.  Without a tree four tokens a lane for short calls, for more lanes, else
+// eight, for fewer loads of weights and rows (10240 channels, us with four and eight: 4 sequences of 20 tokens 5.0 and
+// 5.5, 16 of 40 with 8192 8.9 and 9.4; of 64 tokens one 5.0 and 5.8, but 4 6.8 and 6.4, 16 12.2 and 10.6; 3 of 4000
+// 119 and 101).
 constexpr int kTreeTokens = 4;
 int tokens_of(const ConvArgs &a) { return a.s.tree ? kTreeTokens : a.s.max_q < 64 ? 4 : 8; }
 int rows_of(const ConvArgs &a) { return std::min(4, (a.s.max_q + tokens_of(a) - 1) / tokens_of(a)); }
