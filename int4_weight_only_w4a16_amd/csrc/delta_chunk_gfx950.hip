@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             float f = !a.unit                  ? times2(1.0f, -up)
                       : eps < __builtin_inff() ? 1.0f / sqrtf(sum + eps)
                                                : times2(1.0f / sqrtf(a.eps), -up);
-            if (my_row >= n) f = 0.f;
+            // (nor does a row of zeros, with 1 / sqrt(eps))
+            if (my_row >= n || (top == 0 && f < __builtin_inff())) f = 0.f;
             const bool ok = fine && f < __builtin_inff();
             large |= !(f * (which ? a.scale : 1.0f) < kMostRow);
             (which ? qf : kf)[my_row] = ok ? f : 0.f;

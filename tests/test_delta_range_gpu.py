@@ -242,3 +242,14 @@ def test_unit_length_of_rows_far_below_the_epsilon(dev, tree, n):  # noqa: F811
         x[1::3] = (x[1::3].float() * 2.0 ** power).to(BF16)
         x[2::3] = (x[2::3].float() * 2.0 ** -8).to(BF16)
     run(d, dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads", HEADS)
+def test_keys_of_zeros_count_for_nothing(dev, heads, dtype):  # noqa: F811
+    """Such a token writes nothing, whatever its value; sqrt(eps) does not make it the chunk's heaviest row."""
+    for ratio in (1.0, 2.0 ** 9):
+        d = made([64, 40, 130], heads, dtype, -0.05, seed=2)
+        d.k[::7] = 0
+        grow(d, slice(0, None, 7), EVERY, ratio)
+        run(d, dev)
