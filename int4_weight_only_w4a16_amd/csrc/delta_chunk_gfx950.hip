@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt > wave) continue;
-            const float down = times2(1.0f, -tau[16 * nt + m]);
+            // (what meets no row of U does not count for the power of two)
+            const float down = beta[16 * nt + m] != 0.f ? times2(1.0f, -tau[16 * nt + m]) : 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[nt][j] *= down;
         }
@@ -695,8 +696,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                 const int up = kTop - max(exponent(top), -100);
                 // Rows of R that are lost beside larger ones of their column, another branch's perhaps: as in the
                 // scan, but without the row before: what a row alone has by chance goes token by token too (one of some
-                // 2^24 elements, bfloat16; fp16 outputs, rounded to eight times less, leave less to lose).
-                const float small = times2(BF ? kLeastU / 4 : kLeastU, -up);
+                // 2^25 elements, bfloat16; fp16 outputs, rounded to eight times less, leave less to lose).
+                const float small = times2(BF ? kLeastU / 2 : kLeastU, -up);
                 uint64_t redo = 0;
                 const bool beyond = top >= 0x1p100f || (top < 0x1p-100f && top > 0.f) || of_s[u] > 0x1p86f;
                 if (marked || __builtin_amdgcn_ballot_w64(beyond || (least < small && top > 0.f))) {
@@ -712,7 +713,8 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                     if (!marked) mine &= ~lost;
 #pragma unroll
                     for (int d = 1; d < 64; d *= 2) mine |= __shfl_xor(mine, d);
-                    mine &= n < 64 ? (1ull << n) - 1 : ~0ull;
+                    // and what descends from them, which may have nothing of its own
+                    mine = __builtin_amdgcn_ballot_w64(lane < n && (kin[lane] & mine) != 0);
                     redo = mine;
                 }
                 redo_rows[g0 + 4 * u] = redo;

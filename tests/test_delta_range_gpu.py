@@ -253,3 +253,23 @@ def test_keys_of_zeros_count_for_nothing(dev, heads, dtype):  # noqa: F811
         d.k[::7] = 0
         grow(d, slice(0, None, 7), EVERY, ratio)
         run(d, dev)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("power", [10, 20, 30])
+def test_tokens_that_write_nothing_beside_large_ones(dev, power, dtype):  # noqa: F811
+    """beta 0, or values and states of zero: what their outputs add up is of the tokens before, as far as it is there."""
+    rng = random.Random(power)
+    trees = [[-1] + [max(0, i - rng.randint(1, 3)) for i in range(1, 60)], tr.random_tree(40, rng, 2)]
+    for of_tree in (trees, None):
+        for g in (-0.05, -0.6, -2.0):
+            d = made([60, 40] if of_tree else [130, 65], (1, 2, 128, 64), dtype, g, seed=power, trees=of_tree)
+            grow(d, slice(11, 14), EVERY, 2.0 ** power)
+            grow(d, slice(75, 77), FEW, 2.0 ** power)
+            d.b[::2] = 0.0
+            d.a[20::9] = -20.0
+            d.a[5::13] = -5.0
+            run(d, dev)
+            d.v[1::5] = 0
+            d.v[2::5] = 0
+            run(d, dev)
