@@ -647,7 +647,8 @@ int w4a16_short_conv(const void *x, int64_t x_stride, const float *weight, const
  * do (some 70 us a chunk).  One long sequence beside many of a few tokens is
  * better two calls: of 2048 tokens with 64 of one token, 1.3 ms; apart 0.16.
  * Keys and queries enter long calls and trees with what is below 2^-25 (keys;
- * queries 2^-39) of their row's largest element rounded away. */
+ * queries 2^-39) of their row's largest element rounded away, and what a chunk's
+ * or a tree's tokens forget by 2^-126 or more counts for nothing there. */
 int w4a16_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, const void *a, int64_t a_stride,
                      const void *b, int64_t b_stride, const float *a_log, const float *dt_bias,

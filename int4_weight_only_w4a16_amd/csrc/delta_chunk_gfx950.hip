@@ -31,7 +31,7 @@
 // of a row of R beside a column's largest, which may be a later token's, or one that has faded by the chunk's end.
 // So each chunk is looked at (least and weighed rows of R), and one where a row or the next state would lose by it
 // is gone through token by token, in fp32 from the inputs (1.1 us a token; the look, and U's powers of two by its own
-// largest, cost 2 to 4 %: 8191 tokens 298 -> 304 us, five prompts 120 -> 124).  So is a chunk with products that leave fp32.
+// largest, cost 3 to 5 %: 8191 tokens 297 -> 307 us, five prompts 120 -> 125).  So is a chunk with products that leave fp32.
 //
 // Bound by the chain of chunks: one sequence of 8191 tokens, 16 + 48 heads of 128 x 128, bfloat16,
 // takes 76 us for the preparation and 242 to 256 for the scan, 1.9 a chunk (memory alone: 58).
@@ -58,9 +58,9 @@ constexpr int kTopU = 9;               // and rows of U for the next state below
 // of R; from its weighed rows (2^-25 of U at most), the next state's, 2^-35, and kSmall of R in their heaviest.
 constexpr float kLeastU = 2.0f, kLost = 1.0f / (1 << 26), kSmall = 1.0f / (1 << 17);
 constexpr int kLeastWeighed = -15;
-// Factors that chunks take: what comes off a row, products with queries, elements of T.  With rows and states below 2^100 none
+// Factors that chunks take: keys beside the longest, what comes off a row, products with queries, elements of T.  With rows and states below 2^100 none
 // of what is made of them leaves fp32.
-constexpr float kMostRow = 1 << 24, kMostProduct = 0x1p32f, kMostT = 1 << 20;
+constexpr float kShortKey = 1.0f / (1 << 20), kMostRow = 1 << 24, kMostProduct = 0x1p32f, kMostT = 1 << 20;
 constexpr int kWalked = -(1 << 30);    // in the place of U's power of two: the outputs are made already
 constexpr float kRestUp = 64.f;        // what fp16 leaves of a number below 2^14 is at most 4; with this, 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -203,7 +203,7 @@ constexpr int kMostHeads = 4;          // value heads of a workgroup
 
 // One chunk of `heads` value heads that share a key head: what the heads have in common, the products of
 // keys with keys and queries among it, is made once.  TREE: of one head, and its outputs as well, since there
-// is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 24.5 us; with the outputs in a launch of their own once 36 to 23).
+// is no next chunk (8 trees of 12 to 47 drafts, 48 heads: 25 us; with the outputs in a launch of their own once 36 to 23).
 template <bool BF, int DK, bool TREE>
 __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs a, Segment seg, int heads) {
     using C = Chunk<BF, DK>;
@@ -349,6 +349,12 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
         }
     }
     __syncthreads();
+
+    if (wave == 0) {
+        // (products with long keys would take the short ones' bits, though their tokens may write nothing)
+        const float mine = kf[lane];
+        large |= mine > 0.f && mine < top_of_column(top_of_row(mine)) * kShortKey;
+    }
 
     // ---- keys and queries as operands ----
     if (!TREE && h0 % r == 0) {
@@ -575,9 +581,9 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
             const float weigh = times2(exp_f32((float)(G[kChunk - 1] - G[lane])) * kf[lane], -tau[lane]);
             const int up = -25 - max(exponent(top_of_column(top_of_row(weigh))), -120);
             rows[C::kOff / 4 + lane] = (bad_row[lane] & 1) | bad_gate[hi][lane] ? nan : grow * kf[lane];
-            // (of a tree, T's diagonal, below zero where the path fades and infinite where nothing is written)
+            // (of a tree, T's diagonal, infinite where nothing is written)
             const float diagonal = times2(__builtin_fabsf(beta[lane]), tau[lane]);
-            if (TREE) rows[C::kWeigh / 4 + lane] = diagonal == 0.f || lane >= n ? __builtin_inff() : grow < kSmall ? -diagonal : diagonal;
+            if (TREE) rows[C::kWeigh / 4 + lane] = diagonal == 0.f || lane >= n ? __builtin_inff() : diagonal;
             else rows[C::kWeigh / 4 + lane] = times2(weigh, up);
             rows[C::kFromS / 4 + lane] = bad_row[lane] & 2 ? nan : a.scale * qf[lane] * grow;
             if constexpr (!TREE) {
@@ -707,7 +713,7 @@ __global__ void __launch_bounds__(256, TREE ? 2 : 4) chunk_prep_kernel(DeltaArgs
                         const f4 diagonal = *reinterpret_cast<const f4 *>(&tree_rows[C::kWeigh / 4 + 16 * t + 4 * b]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (__builtin_fabsf(R[t][j] * diagonal[j]) < small && top > 0.f && (R[t][j] != 0.f || diagonal[j] < 0.f))
+                            if (__builtin_fabsf(R[t][j] * diagonal[j]) < small && top > 0.f)
                                 mine |= 1ull << (16 * t + 4 * b + j);
                     }
                     if (!marked) mine &= ~lost;

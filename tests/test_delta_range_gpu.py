@@ -273,3 +273,18 @@ def test_tokens_that_write_nothing_beside_large_ones(dev, power, dtype):  # noqa
             d.v[1::5] = 0
             d.v[2::5] = 0
             run(d, dev)
+
+
+@pytest.mark.parametrize("n", [40, 64, 130])
+@pytest.mark.parametrize("tree", [False, True])
+def test_raw_keys_of_very_different_lengths(dev, tree, n):  # noqa: F811
+    """Long keys whose tokens write nothing, and short ones whose tokens do."""
+    n = min(n, 64) if tree else n
+    for power in (12, 24, 40):
+        d = Delta([n], 1, 2, 64, 64, BF16, seed=power, raw=True, unit=False, trees=[tr.chain(n)] if tree else None)
+        d.a[:] = -0.02
+        d.state[:] = 0
+        d.v[::2] = 0
+        d.k[1::2] = (d.k[1::2].float() * 2.0 ** -power).to(BF16)
+        d.k[::2, :, ::2], d.k[1::2, :, 1::2] = 0, 0        # (of no common channel: nothing is taken back)
+        check(d, *d.call(dev))
