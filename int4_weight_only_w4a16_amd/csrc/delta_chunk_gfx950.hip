@@ -21,8 +21,8 @@
 // products for a pair of such factors, lo x lo left out (2^-22).  Keys and queries of
 // either type enter as they are, once a power of two for each row brings them into fp16's range, but for
 // elements below about 2^-14 (keys; queries 2^-28) of their row's largest, which fp16's smallest place rounds: by at
-// most 2^-25 (2^-39) of that largest.  So do powers of two for each row of T and each column of S and of the rows.  What goes into the output
-// alone has one part (2^-12), an eighth of a bfloat16 output's own rounding.  An fp16 output would be
+// most 2^-25 (2^-39) of that largest.  So do powers of two for each row of T and each column of S and of the rows.
+// What goes into the output alone has one part (2^-12), an eighth of a bfloat16 output's own rounding.  An fp16 output would be
 // 1.7 times as far off as its rounding alone: there U has two parts and the triangle a second one
 // of e4m3 (1.1 times; five prompts 112 -> 119 us); a tree's have two of S and U (1.2 times).
 // Powers of two come off in fp32.

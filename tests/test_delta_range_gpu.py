@@ -288,3 +288,38 @@ def test_raw_keys_of_very_different_lengths(dev, tree, n):  # noqa: F811
         d.k[1::2] = (d.k[1::2].float() * 2.0 ** -power).to(BF16)
         d.k[::2, :, ::2], d.k[1::2, :, 1::2] = 0, 0        # (of no common channel: nothing is taken back)
         check(d, *d.call(dev))
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_replayed_from_a_graph_with_large_values_and_without(dev, tree):  # noqa: F811
+    """What goes token by token is decided on the device, at each replay anew."""
+    import int4_weight_only_w4a16_amd as w4
+    rng = random.Random(4)
+    trees = [tr.random_tree(n, rng, 2) for n in (50, 64)] if tree else None
+    every = []
+    for large in (False, True):
+        d = made([50, 64] if tree else [70, 130], (1, 2, 64, 64), BF16, -0.05, seed=3, trees=trees)
+        if large:
+            grow(d, slice(7, 9), FEW, 2.0 ** 35)
+            grow(d, slice(100, 101), EVERY, 2.0 ** 35)
+        args = d.args(dev)
+        out = w4.gated_delta_rule(**{**args, "state": args["state"].clone()})
+        after = args["state"].clone()
+        w4.gated_delta_rule(**{**args, "state": after})
+        every.append((args, out, after))
+    live = {k: v.clone() if torch.is_tensor(v) else v for k, v in every[0][0].items()}
+    out = torch.zeros_like(every[0][1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        w4.gated_delta_rule(**live, out=out)
+    for i in (0, 1, 1, 0, 1):
+        for k, v in every[i][0].items():
+            if torch.is_tensor(v):
+                live[k].copy_(v)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, every[i][1]) and torch.equal(live["state"], every[i][2]), i
+        w4.gated_delta_rule(**{**every[0][0], "state": every[0][0]["state"].clone()})
